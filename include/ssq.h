@@ -306,6 +306,132 @@ ssq_status ssq_dequant(const ssq_state *state, float *out, void *stream);
  * SSQ_ERR_INVALID_ARG before anything is enqueued.  The caller owns both buffers. */
 ssq_status ssq_stream_copy(void *dst, const void *src, size_t bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Linear attention with a decay for each head, on the state of SSQ_MAMBA2.
+ *
+ * Per sequence and head, with key and query heads shared by nheads/ngroups
+ * value heads:
+ *   S_t = exp(g_t) S_(t-1) + v_t k_t^T,   o_t = scale * S_t q_t
+ * S is the P x N matrix whose rows the state stores (row p over the N = 128
+ * key entries).  It is the Mamba-2 recurrence with g = dt*A, v = dt*x, k = B,
+ * q = C, on tensors of the caller's type.
+ *
+ * Types and layouts (ssq_linattn_io): q, k [tokens][ngroups][128] and v, o
+ * [tokens][nheads][P] in `dtype`, each with a stride in elements from one
+ * token to the next, so that they may be slices of one projection's output;
+ * heads are packed within a token.  g [tokens][nheads] is fp32, g <= 0
+ * (-infinity forgets the state; NULL: no decay), with a stride of its own (0:
+ * the same decay at every token).  q, k, v and o and their strides in bytes
+ * are multiples of 16, the strides of q, k, v and g are >= 0 and o's is at
+ * least nheads*P.  o overlaps no input.  The state, every sum and every decay
+ * are fp32 or wider; o is rounded once to `dtype`.
+ *
+ * slots: device int32 [nseq], the sequence of the state (0 .. batch-1) that
+ * sequence i of the call is, each at most once (twice: the state and outputs
+ * of those are unspecified); a slot out of range skips the sequence, of which
+ * nothing is read or written.  NULL: i, and nseq <= batch.  Sequences of the
+ * state that no slot names are left as they are.  nseq = 0 is an empty call.
+ * ------------------------------------------------------------------------ */
+typedef enum { SSQ_DTYPE_FP32 = 0, SSQ_DTYPE_BF16 = 1, SSQ_DTYPE_FP16 = 2 } ssq_dtype;
+
+typedef struct {
+    int32_t dtype;    /* ssq_dtype of q, k, v and o */
+    float scale;      /* factor on o */
+    const void *q;
+    const void *k;
+    const void *v;
+    const float *g;
+    void *o;
+    int64_t q_stride; /* elements from one token to the next */
+    int64_t k_stride;
+    int64_t v_stride;
+    int64_t g_stride;
+    int64_t o_stride;
+} ssq_linattn_io;
+
+/* Bytes of device workspace ssq_linattn_prefill needs for these sizes (0: none);
+ * (size_t)-1 if the state is NULL or a delta state, or a size is negative. */
+size_t ssq_linattn_workspace(const ssq_state *state, int32_t nseq, int64_t tokens);
+
+/* Prompts, one after the other in `tokens` rows: sequence i has the tokens
+ * cu_seqlens[i] .. cu_seqlens[i+1]-1 (device int32 [nseq+1], not decreasing,
+ * within 0 .. tokens; values outside are clamped to it).  Rows that belong to
+ * no sequence, such as padding behind the last one, are not read and their o
+ * is left as it was.
+ * Each sequence goes on from its state, or from zero where fresh[i] is not 0
+ * (device uint8 [nseq]; NULL: all go on), and leaves its last state; an empty
+ * sequence leaves its state, zeroed if fresh.  The recurrence is fp32 from end
+ * to end; a quantized state is reconstructed at the start and refit and
+ * rounded once, at the end (as ssq_prefill with one chunk; a stochastic
+ * rounding draws the uniforms of the state's next token and advances it by
+ * one).  o is read from the fp32 recurrence.
+ * The tokens of a sequence are taken 64 at a time: products among them and
+ * with the state run on the matrix cores; where sequences and heads are too
+ * few to fill the card, a sequence is split and its parts are joined by their
+ * decays.  Results do not depend on other sequences of the call, but may
+ * differ in rounding with the call's sizes.
+ * workspace: device memory of at least ssq_linattn_workspace() bytes, 256-byte
+ * aligned, used by this call alone until the stream has passed it. */
+ssq_status ssq_linattn_prefill(ssq_state *state, const ssq_linattn_io *io, int32_t nseq, int64_t tokens,
+                               const int32_t *cu_seqlens, const int32_t *slots, const uint8_t *fresh,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+/* One token for each of nseq sequences (row i of the tensors is sequence i):
+ * lambda = fl32(exp(g)) (in double, rounded once), each entry
+ * h'_n = fma(lambda, h_n, fl(v_p*k_n)) on the reconstructed entry; a quantized
+ * row is then refit and rounded (nearest, or stochastically as in
+ * ssq_decode_step), and o is read from the new codes or from h' (`readout`). */
+ssq_status ssq_linattn_step(ssq_state *state, const ssq_linattn_io *io, int32_t nseq, const int32_t *slots,
+                            int32_t readout, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Beam search: the next beams of every request, and states that follow them.
+ * ------------------------------------------------------------------------ */
+#define SSQ_MAX_BEAMS 32
+
+typedef struct {
+    int32_t dtype;   /* ssq_dtype of the logits */
+    int32_t batch;   /* requests */
+    int32_t beams;   /* beams of each, 1 .. SSQ_MAX_BEAMS */
+    int32_t vocab;   /* tokens */
+    int32_t nselect; /* candidates kept of each request, 1 .. 2*beams */
+    int32_t pad_token; /* the token of a finished beam's candidate, 0 .. vocab-1 */
+    int64_t row_stride; /* elements from one beam's logits to the next's, >= vocab */
+} ssq_beam_desc;
+
+/* Bytes of device workspace ssq_beam_select needs; 0 if the description is invalid. */
+size_t ssq_beam_workspace(const ssq_beam_desc *desc);
+
+/* The nselect best continuations of every request over its beams and the
+ * vocabulary.  Candidate (beam, token) has the score
+ *   scores[beam] + (x - m) - log(sum exp(x - m)),  m the beam's largest logit,
+ * compared in double.  Candidates are ordered by descending score, of equal
+ * ones the lower beam first, and within a beam by descending logit, of equal
+ * ones the lower token first; they are written as scores [batch][nselect] (fp32), tokens and parents (the beam in 0 ..
+ * beams-1) int32.  A logit of -infinity is no candidate, nor is any token of a
+ * beam with the score -infinity or with nothing but -infinity; NaN logits
+ * count as -infinity.  A beam with finished[beam] != 0 (device uint8
+ * [batch][beams]; NULL: none) has one candidate, pad_token with the beam's
+ * score; its logits do not count.  Where there are fewer than nselect
+ * candidates, the places left get score -infinity, token -1 and parent
+ * (place mod beams).  Scores or logits of +infinity and scores that are NaN
+ * leave that request's outputs unspecified (parents stay in range).
+ * logits: aligned to their element; the rest as named; workspace as for
+ * ssq_linattn_prefill.  The outputs overlap no input. */
+ssq_status ssq_beam_select(const ssq_beam_desc *desc, const void *logits, const float *scores,
+                           const uint8_t *finished, float *out_scores, int32_t *out_tokens,
+                           int32_t *out_parents, void *workspace, size_t workspace_bytes, void *stream);
+
+/* States follow their beams: of every group of `beams` consecutive sequences
+ * r*beams .. r*beams+beams-1, sequence j becomes what sequence
+ * parents[r*beams + j] (0 .. beams-1, device int32 [batch]) of the group was;
+ * a parent out of range leaves sequence j.  In place, for `nstates` different
+ * states (the layers of a model; any kinds and formats, all of one batch that
+ * `beams` divides) at once.  Rounding modes and token counters stay.  Bytes
+ * move unchanged. */
+ssq_status ssq_state_reorder(ssq_state *const *states, int32_t nstates, const int32_t *parents, int32_t beams,
+                             void *stream);
+
 /* Static text for a status code (an ssq_status value); any other value gives
  * "unknown ssq_status".  Taken as int32_t so that an out-of-range code is an
  * ordinary argument, not an invalid enum value. */

@@ -29,6 +29,9 @@ SSQ_DAMP_NHI = 16
 SSQ_MAMBA2, SSQ_DELTA = 0, 1
 # ssq_readout
 SSQ_READ_POST_QUANT, SSQ_READ_PRE_QUANT = 0, 1
+# ssq_dtype
+SSQ_DTYPE_FP32, SSQ_DTYPE_BF16, SSQ_DTYPE_FP16 = range(3)
+SSQ_MAX_BEAMS = 32
 # ssq_rounding
 SSQ_ROUND_NEAREST, SSQ_ROUND_STOCHASTIC = 0, 1
 
@@ -54,6 +57,19 @@ class ssq_layout(ctypes.Structure):
                 ("codes_offset", ctypes.c_size_t), ("scale_offset", ctypes.c_size_t),
                 ("zero_offset", ctypes.c_size_t), ("total_bytes", ctypes.c_size_t),
                 ("hi_offset", ctypes.c_size_t), ("counter_offset", ctypes.c_size_t)]
+
+
+class ssq_linattn_io(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("g", ctypes.c_void_p), ("o", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64), ("g_stride", ctypes.c_int64),
+                ("o_stride", ctypes.c_int64)]
+
+
+class ssq_beam_desc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("batch", ctypes.c_int32), ("beams", ctypes.c_int32),
+                ("vocab", ctypes.c_int32), ("nselect", ctypes.c_int32), ("pad_token", ctypes.c_int32),
+                ("row_stride", ctypes.c_int64)]
 
 
 def _load():
@@ -97,6 +113,20 @@ def _load():
     L.ssq_set_rounding.restype = st
     L.ssq_get_rounding.argtypes = [vp, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(u64), ctypes.POINTER(u64), vp]
     L.ssq_get_rounding.restype = st
+    iop = ctypes.POINTER(ssq_linattn_io)
+    L.ssq_linattn_workspace.argtypes = [vp, ctypes.c_int32, ctypes.c_int64]
+    L.ssq_linattn_workspace.restype = ctypes.c_size_t
+    L.ssq_linattn_prefill.argtypes = [vp, iop, ctypes.c_int32, ctypes.c_int64, vp, vp, vp, vp, ctypes.c_size_t, vp]
+    L.ssq_linattn_prefill.restype = st
+    L.ssq_linattn_step.argtypes = [vp, iop, ctypes.c_int32, vp, ctypes.c_int32, vp]
+    L.ssq_linattn_step.restype = st
+    bdp = ctypes.POINTER(ssq_beam_desc)
+    L.ssq_beam_workspace.argtypes = [bdp]
+    L.ssq_beam_workspace.restype = ctypes.c_size_t
+    L.ssq_beam_select.argtypes = [bdp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
+    L.ssq_beam_select.restype = st
+    L.ssq_state_reorder.argtypes = [ctypes.POINTER(vp), ctypes.c_int32, vp, ctypes.c_int32, vp]
+    L.ssq_state_reorder.restype = st
     return L
 
 
@@ -316,3 +346,158 @@ def ssq_stream_copy(dst, src, nbytes: int | None = None, stream=None):
         raise ValueError("nbytes exceeds a tensor")
     _check(lib.ssq_stream_copy(ctypes.c_void_p(dst.data_ptr()), ctypes.c_void_p(src.data_ptr()), n, _stream(stream)),
            "ssq_stream_copy")
+
+
+_DTYPES = {torch.float32: SSQ_DTYPE_FP32, torch.bfloat16: SSQ_DTYPE_BF16, torch.float16: SSQ_DTYPE_FP16}
+
+
+def _here(t, name: str, dtype, shape=None):
+    """A tensor on the current device, of this dtype and shape (None: any extent)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, is {t.dtype}")
+    if shape is not None and (t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape))):
+        raise ValueError(f"{name} has the shape {tuple(t.shape)}, expected {shape}")
+    return t
+
+
+def _flat(t, name: str, dtype, shape):
+    if t is None:
+        return None
+    if not _here(t, name, dtype, shape).is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def _flags(t, name: str, shape):
+    if t is not None and isinstance(t, torch.Tensor) and t.dtype == torch.bool:
+        t = t.view(torch.uint8)
+    return _flat(t, name, torch.uint8, shape)
+
+
+def _token_stride(t, name: str) -> int:
+    """Elements from one token to the next of a [tokens][heads][width] or [tokens][heads] tensor whose tokens are packed."""
+    want = 1
+    for n, s in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if n != 1 and s != want:
+            raise ValueError(f"the heads of {name} must be packed within a token")
+        want *= n
+    return t.stride(0) if t.shape[0] > 1 else want
+
+
+def _workspace(given, need: int, stream):
+    """Device memory for one call on ``stream``: the caller's, or torch's, which is reused in the stream's order."""
+    if given is not None:
+        return _here(given, "workspace", torch.uint8)
+    if need == 0:
+        return None
+    if stream is None or stream == torch.cuda.current_stream():
+        return torch.empty(need, dtype=torch.uint8, device="cuda")
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(stream):
+        return torch.empty(need, dtype=torch.uint8, device="cuda")
+
+
+def _linattn_io(state: State, q, k, v, g, o, scale: float, tokens: int):
+    d = state.desc
+    if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPES:
+        raise ValueError("q must be a float32, bfloat16 or float16 tensor")
+    io = ssq_linattn_io(dtype=_DTYPES[q.dtype], scale=float(scale))
+    # a state of the other kind is rejected by the library
+    G, H, P, N = _sizes(state, SSQ_MAMBA2, d.ngroups, d.nheads, d.rows_per_head, d.row_len)
+    for name, t, dtype, shape in (("q", q, q.dtype, (tokens, G, N)), ("k", k, q.dtype, (tokens, G, N)),
+                                  ("v", v, q.dtype, (tokens, H, P)), ("o", o, q.dtype, (tokens, H, P)),
+                                  ("g", g, torch.float32, (tokens, H))):
+        if t is None and name == "g":
+            continue
+        _here(t, name, dtype, shape)
+        setattr(io, name + "_stride", _token_stride(t, name))
+        setattr(io, name, t.data_ptr())
+    return io
+
+
+def ssq_linattn_workspace(state: State, nseq: int, tokens: int) -> int:
+    """Bytes of workspace ``ssq_linattn_prefill`` needs for these sizes."""
+    n = int(lib.ssq_linattn_workspace(state.handle, nseq, tokens))
+    if n == ctypes.c_size_t(-1).value:
+        raise ValueError("linear attention runs on an SSQ_MAMBA2 state, sizes must not be negative")
+    return n
+
+
+def ssq_linattn_prefill(state: State, q, k, v, g, o, cu_seqlens, slots=None, fresh=None, scale: float = 1.0,
+                        workspace: torch.Tensor | None = None, stream=None):
+    """Ragged prompts through linear attention with a decay for each head.
+
+    q, k ``[tokens, ngroups, 128]``, v, o ``[tokens, nheads, P]`` (float32, bfloat16 or float16; any stride between
+    tokens that is a multiple of 16 bytes), g ``[tokens, nheads]`` float32 log decays or None, cu_seqlens int32
+    ``[nseq + 1]``, slots int32 ``[nseq]`` or None, fresh uint8 or bool ``[nseq]`` or None; all on the device.
+    ``workspace``: uint8, at least ``ssq_linattn_workspace`` bytes, or None to take it from torch."""
+    tokens = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() else 0
+    nseq = _here(cu_seqlens, "cu_seqlens", torch.int32, (None,)).numel() - 1
+    if nseq < 0:
+        raise ValueError("cu_seqlens has nseq + 1 entries")
+    io = _linattn_io(state, q, k, v, g, o, scale, tokens)
+    need = ssq_linattn_workspace(state, nseq, tokens) if state.desc.kind == SSQ_MAMBA2 else 0
+    ws = _workspace(workspace, need, stream)
+    _check(lib.ssq_linattn_prefill(state.handle, ctypes.byref(io), nseq, tokens,
+                                   _flat(cu_seqlens, "cu_seqlens", torch.int32, (nseq + 1,)),
+                                   _flat(slots, "slots", torch.int32, (nseq,)), _flags(fresh, "fresh", (nseq,)),
+                                   None if ws is None else ctypes.c_void_p(ws.data_ptr()),
+                                   0 if ws is None else ws.numel(), _stream(stream)), "ssq_linattn_prefill")
+
+
+def ssq_linattn_step(state: State, q, k, v, g, o, slots=None, scale: float = 1.0, readout: int = SSQ_READ_POST_QUANT,
+                     stream=None):
+    """One token of linear attention for ``nseq = q.shape[0]`` sequences: row i of the tensors (as in
+    ``ssq_linattn_prefill``) is sequence ``slots[i]`` of the state, or sequence i without slots."""
+    nseq = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() else 0
+    io = _linattn_io(state, q, k, v, g, o, scale, nseq)
+    _check(lib.ssq_linattn_step(state.handle, ctypes.byref(io), nseq, _flat(slots, "slots", torch.int32, (nseq,)),
+                                readout, _stream(stream)), "ssq_linattn_step")
+
+
+def ssq_beam_workspace(desc: ssq_beam_desc) -> int:
+    return int(lib.ssq_beam_workspace(ctypes.byref(desc)))
+
+
+def ssq_beam_select(logits, scores, out_scores, out_tokens, out_parents, finished=None, pad_token: int = 0,
+                    workspace: torch.Tensor | None = None, stream=None):
+    """The best ``out_scores.shape[1]`` continuations of every request over its beams and the vocabulary.
+
+    logits ``[batch, beams, vocab]`` (float32, bfloat16 or float16; beams any stride apart), scores ``[batch, beams]``
+    float32, out_scores float32, out_tokens and out_parents int32 ``[batch, nselect]``, finished uint8 or bool
+    ``[batch, beams]`` or None."""
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in _DTYPES or logits.dim() != 3:
+        raise ValueError("logits must be a float32, bfloat16 or float16 tensor [batch, beams, vocab]")
+    b, m, v = logits.shape
+    _here(logits, "logits", logits.dtype)
+    row = logits.stride(1) if m > 1 else (logits.stride(0) if b > 1 else v)
+    if v > 1 and logits.stride(2) != 1 or b > 1 and logits.stride(0) != m * row:
+        raise ValueError("the rows of logits must be contiguous and evenly spaced")
+    n = _here(out_scores, "out_scores", torch.float32, (b, None)).shape[1]
+    d = ssq_beam_desc(_DTYPES[logits.dtype], b, m, v, n, pad_token, row)
+    ws = _workspace(workspace, ssq_beam_workspace(d), stream)
+    _check(lib.ssq_beam_select(ctypes.byref(d), ctypes.c_void_p(logits.data_ptr()),
+                               _flat(scores, "scores", torch.float32, (b, m)), _flags(finished, "finished", (b, m)),
+                               _flat(out_scores, "out_scores", torch.float32, (b, n)),
+                               _flat(out_tokens, "out_tokens", torch.int32, (b, n)),
+                               _flat(out_parents, "out_parents", torch.int32, (b, n)),
+                               None if ws is None else ctypes.c_void_p(ws.data_ptr()),
+                               0 if ws is None else ws.numel(), _stream(stream)), "ssq_beam_select")
+
+
+def ssq_state_reorder(states, parents, stream=None):
+    """States follow their beams: of every group of ``parents.shape[1]`` consecutive sequences, sequence j becomes
+    what sequence ``parents[group, j]`` of the group was.  ``states``: a State or a sequence of them (the layers of a
+    model), each of ``parents.numel()`` sequences; parents int32 ``[groups, beams]``."""
+    states = [states] if isinstance(states, State) else list(states)
+    p = _flat(parents, "parents", torch.int32, (None, None))
+    for s in states:
+        if s.desc.batch != parents.numel():
+            raise ValueError(f"a state has {s.desc.batch} sequences, parents names {parents.numel()}")
+    handles = (ctypes.c_void_p * max(1, len(states)))(*[s.handle for s in states])
+    _check(lib.ssq_state_reorder(handles, len(states), p, parents.shape[1], _stream(stream)), "ssq_state_reorder")

@@ -14,6 +14,7 @@
 #include <string>
 
 #include "ssq_internal.h"
+#include "ssq_ops.h"
 
 struct ssq_state {
     ssq_desc desc;
@@ -489,6 +490,203 @@ ssq_status ssq_stream_copy(void* dst, const void* src, size_t bytes, void* strea
     const uintptr_t s = (uintptr_t)src, d = (uintptr_t)dst;
     SSQ_REQUIRE(d + bytes <= s || s + bytes <= d, SSQ_ERR_INVALID_ARG, "dst and src must not overlap");
     return from_hip(ssq::launch_stream_copy(dst, src, (int64_t)bytes, (hipStream_t)stream), "copy launch");
+}
+
+// ---------------------------------------------------------------------------
+// linear attention
+// ---------------------------------------------------------------------------
+static bool dtype_valid(int d) { return d >= SSQ_DTYPE_FP32 && d <= SSQ_DTYPE_FP16; }
+
+static ssq_status fill_linattn(ssq_state* st, const ssq_linattn_io* io, int32_t nseq, int64_t tokens,
+                               const int32_t* slots, ssq::LinArgs* a)
+{
+    SSQ_REQUIRE(st && io, SSQ_ERR_INVALID_ARG, "state or io is NULL");
+    SSQ_REQUIRE(st->desc.kind == SSQ_MAMBA2, SSQ_ERR_KIND_MISMATCH, "linear attention runs on an SSQ_MAMBA2 state");
+    SSQ_REQUIRE(dtype_valid(io->dtype), SSQ_ERR_INVALID_ARG, "unknown dtype");
+    SSQ_REQUIRE(nseq >= 0 && tokens >= 0, SSQ_ERR_INVALID_ARG, "nseq and tokens must not be negative");
+    SSQ_REQUIRE(slots || nseq <= st->desc.batch, SSQ_ERR_INVALID_ARG, "without slots nseq must not exceed the batch");
+    SSQ_REQUIRE(tokens == 0 || (io->q && io->k && io->v && io->o), SSQ_ERR_INVALID_ARG,
+                "an input or output pointer is NULL");
+    SSQ_REQUIRE(aligned(io->q, 16) && aligned(io->k, 16) && aligned(io->v, 16) && aligned(io->o, 16),
+                SSQ_ERR_INVALID_ARG, "q, k, v and o must be 16-byte aligned");
+    SSQ_REQUIRE(aligned(io->g, 4) && aligned(slots, 4), SSQ_ERR_INVALID_ARG, "g and slots must be 4-byte aligned");
+    const int64_t unit = io->dtype == SSQ_DTYPE_FP32 ? 4 : 8; // elements in 16 bytes
+    SSQ_REQUIRE(io->q_stride >= 0 && io->k_stride >= 0 && io->v_stride >= 0 && io->g_stride >= 0, SSQ_ERR_INVALID_ARG,
+                "strides must not be negative");
+    SSQ_REQUIRE(io->q_stride % unit == 0 && io->k_stride % unit == 0 && io->v_stride % unit == 0 && io->o_stride % unit == 0,
+                SSQ_ERR_INVALID_ARG, "the strides of q, k, v and o must be multiples of 16 bytes");
+    const int64_t row = (int64_t)st->desc.nheads * st->desc.rows_per_head;
+    SSQ_REQUIRE(tokens <= 1 || io->o_stride >= row, SSQ_ERR_INVALID_ARG, "the stride of o must be at least nheads*P");
+    // every offset a kernel forms stays below 2^62 bytes
+    const int64_t most = ((int64_t)1 << 59) / (tokens > 0 ? tokens : 1);
+    SSQ_REQUIRE(io->q_stride <= most && io->k_stride <= most && io->v_stride <= most && io->g_stride <= most &&
+                    io->o_stride <= most, SSQ_ERR_INVALID_ARG, "a stride is too large");
+    SSQ_REQUIRE(row <= ((int64_t)1 << 31) - 1, SSQ_ERR_UNSUPPORTED, "nheads*P must be below 2^31");
+    ssq_status s = check_device(st);
+    if (s != SSQ_OK) return s;
+    *a = ssq::LinArgs{};
+    if (fmt_quant(st->desc.format)) a->codes = codes_ptr(st);
+    else a->h32 = (float*)codes_ptr(st);
+    a->scale = scale_ptr(st);
+    a->zero = zero_ptr(st);
+    a->q = io->q;
+    a->k = io->k;
+    a->v = io->v;
+    a->g = io->g;
+    a->o = io->o;
+    a->qs = io->q_stride;
+    a->ks = io->k_stride;
+    a->vs = io->v_stride;
+    a->gs = io->g_stride;
+    a->os = io->o_stride;
+    a->slots = slots;
+    a->tokens = tokens;
+    a->nseq = nseq;
+    a->batch = st->desc.batch;
+    a->H = st->desc.nheads;
+    a->G = st->desc.ngroups;
+    a->P = st->desc.rows_per_head;
+    a->oscale = io->scale;
+    a->sr = sr_args(st);
+    return SSQ_OK;
+}
+
+size_t ssq_linattn_workspace(const ssq_state* st, int32_t nseq, int64_t tokens)
+{
+    if (!st || st->desc.kind != SSQ_MAMBA2 || nseq < 0 || tokens < 0) return (size_t)-1;
+    return ssq::linattn_workspace(st->desc.format, nseq, tokens, st->desc.nheads, st->desc.rows_per_head,
+                                  num_cus(st->device));
+}
+
+ssq_status ssq_linattn_prefill(ssq_state* st, const ssq_linattn_io* io, int32_t nseq, int64_t tokens,
+                               const int32_t* cu_seqlens, const int32_t* slots, const uint8_t* fresh, void* workspace,
+                               size_t workspace_bytes, void* stream)
+{
+    ssq::LinArgs a;
+    ssq_status s = fill_linattn(st, io, nseq, tokens, slots, &a);
+    if (s != SSQ_OK) return s;
+    SSQ_REQUIRE(nseq == 0 || cu_seqlens, SSQ_ERR_INVALID_ARG, "cu_seqlens is NULL");
+    SSQ_REQUIRE(aligned(cu_seqlens, 4), SSQ_ERR_INVALID_ARG, "cu_seqlens must be 4-byte aligned");
+    SSQ_REQUIRE(tokens <= 0x7FFFFFFF, SSQ_ERR_UNSUPPORTED, "cu_seqlens counts up to 2^31-1 tokens");
+    const size_t need = ssq_linattn_workspace(st, nseq, tokens);
+    SSQ_REQUIRE(need == 0 || (workspace && workspace_bytes >= need), SSQ_ERR_INVALID_ARG, "the workspace is too small");
+    SSQ_REQUIRE(aligned(workspace, 256), SSQ_ERR_INVALID_ARG, "the workspace must be 256-byte aligned");
+    if (nseq == 0) return ok();
+    a.cu = cu_seqlens;
+    a.fresh = fresh;
+    s = from_hip(ssq::launch_linattn_prefill(st->desc.format, io->dtype, a, workspace, num_cus(st->device),
+                                             (hipStream_t)stream),
+                 "linear attention prefill launch");
+    return s == SSQ_OK ? advance(st, 1, (hipStream_t)stream) : s;
+}
+
+ssq_status ssq_linattn_step(ssq_state* st, const ssq_linattn_io* io, int32_t nseq, const int32_t* slots,
+                            int32_t readout, void* stream)
+{
+    ssq::LinArgs a;
+    ssq_status s = fill_linattn(st, io, nseq, nseq, slots, &a);
+    if (s != SSQ_OK) return s;
+    SSQ_REQUIRE(readout == SSQ_READ_POST_QUANT || readout == SSQ_READ_PRE_QUANT, SSQ_ERR_INVALID_ARG,
+                "unknown readout");
+    if (nseq == 0) return ok();
+    s = from_hip(ssq::launch_linattn_step(st->desc.format, io->dtype, a, readout == SSQ_READ_PRE_QUANT,
+                                          (hipStream_t)stream),
+                 "linear attention step launch");
+    return s == SSQ_OK ? advance(st, 1, (hipStream_t)stream) : s;
+}
+
+// ---------------------------------------------------------------------------
+// beam search
+// ---------------------------------------------------------------------------
+static ssq_status check_beam(const ssq_beam_desc* d)
+{
+    SSQ_REQUIRE(d, SSQ_ERR_INVALID_ARG, "desc is NULL");
+    SSQ_REQUIRE(dtype_valid(d->dtype), SSQ_ERR_INVALID_ARG, "unknown dtype");
+    SSQ_REQUIRE(d->batch >= 0 && d->vocab > 0, SSQ_ERR_INVALID_ARG, "batch must not be negative, vocab positive");
+    SSQ_REQUIRE(d->beams > 0 && d->beams <= SSQ_MAX_BEAMS, SSQ_ERR_INVALID_ARG, "beams must be 1 .. SSQ_MAX_BEAMS");
+    SSQ_REQUIRE(d->nselect > 0 && d->nselect <= 2 * d->beams, SSQ_ERR_INVALID_ARG, "nselect must be 1 .. 2*beams");
+    SSQ_REQUIRE(d->pad_token >= 0 && d->pad_token < d->vocab, SSQ_ERR_INVALID_ARG, "pad_token must be 0 .. vocab-1");
+    SSQ_REQUIRE(d->row_stride >= d->vocab, SSQ_ERR_INVALID_ARG, "row_stride must be at least vocab");
+    const int64_t rows = (int64_t)d->batch * d->beams;
+    SSQ_REQUIRE(d->row_stride <= ((int64_t)1 << 59) / (rows > 0 ? rows : 1), SSQ_ERR_INVALID_ARG,
+                "row_stride is too large");
+    return SSQ_OK;
+}
+
+size_t ssq_beam_workspace(const ssq_beam_desc* d)
+{
+    if (check_beam(d) != SSQ_OK) return 0;
+    return ssq::beam_workspace(d->dtype, d->batch, d->beams, d->vocab, d->nselect);
+}
+
+ssq_status ssq_beam_select(const ssq_beam_desc* d, const void* logits, const float* scores, const uint8_t* finished,
+                           float* out_scores, int32_t* out_tokens, int32_t* out_parents, void* workspace,
+                           size_t workspace_bytes, void* stream)
+{
+    ssq_status s = check_beam(d);
+    if (s != SSQ_OK) return s;
+    if (d->batch == 0) return ok();
+    SSQ_REQUIRE(logits && scores && out_scores && out_tokens && out_parents, SSQ_ERR_INVALID_ARG,
+                "an input or output pointer is NULL");
+    SSQ_REQUIRE(aligned(logits, d->dtype == SSQ_DTYPE_FP32 ? 4 : 2), SSQ_ERR_INVALID_ARG,
+                "the logits must be aligned to their element");
+    SSQ_REQUIRE(aligned(scores, 4) && aligned(out_scores, 4) && aligned(out_tokens, 4) && aligned(out_parents, 4),
+                SSQ_ERR_INVALID_ARG, "scores and outputs must be 4-byte aligned");
+    SSQ_REQUIRE(workspace && aligned(workspace, 256) && workspace_bytes >= ssq_beam_workspace(d), SSQ_ERR_INVALID_ARG,
+                "the workspace is too small or not 256-byte aligned");
+    ssq::BeamArgs a{};
+    a.logits = logits;
+    a.scores = scores;
+    a.finished = finished;
+    a.out_scores = out_scores;
+    a.out_tokens = out_tokens;
+    a.out_parents = out_parents;
+    a.ws = workspace;
+    a.row_stride = d->row_stride;
+    a.batch = d->batch;
+    a.beams = d->beams;
+    a.vocab = d->vocab;
+    a.nselect = d->nselect;
+    a.pad = d->pad_token;
+    return from_hip(ssq::launch_beam_select(d->dtype, a, (hipStream_t)stream), "beam selection launch");
+}
+
+ssq_status ssq_state_reorder(ssq_state* const* states, int32_t nstates, const int32_t* parents, int32_t beams,
+                             void* stream)
+{
+    constexpr int kMost = 1024; // states of one call
+    SSQ_REQUIRE(nstates >= 0 && nstates <= kMost, SSQ_ERR_INVALID_ARG, "nstates must be 0 .. 1024");
+    if (nstates == 0) return ok();
+    SSQ_REQUIRE(states && parents, SSQ_ERR_INVALID_ARG, "states or parents is NULL");
+    SSQ_REQUIRE(aligned(parents, 4), SSQ_ERR_INVALID_ARG, "parents must be 4-byte aligned");
+    SSQ_REQUIRE(beams > 0 && beams <= SSQ_MAX_BEAMS, SSQ_ERR_INVALID_ARG, "beams must be 1 .. SSQ_MAX_BEAMS");
+    ssq::ReorderPart parts[4 * kMost];
+    int n = 0;
+    for (int i = 0; i < nstates; ++i) {
+        const ssq_state* st = states[i];
+        SSQ_REQUIRE(st, SSQ_ERR_INVALID_ARG, "a state is NULL");
+        SSQ_REQUIRE(st->desc.batch == states[0]->desc.batch, SSQ_ERR_INVALID_ARG, "the states differ in their batch");
+        SSQ_REQUIRE(st->desc.batch % beams == 0, SSQ_ERR_INVALID_ARG, "beams must divide the batch");
+        const ssq_status s = check_device(st);
+        if (s != SSQ_OK) return s;
+        // two handles over the same bytes would move them twice at once
+        const uintptr_t p = (uintptr_t)st->storage;
+        for (int j = 0; j < i; ++j) {
+            const uintptr_t q = (uintptr_t)states[j]->storage;
+            SSQ_REQUIRE(p + st->lay.total_bytes <= q || q + states[j]->lay.total_bytes <= p, SSQ_ERR_INVALID_ARG,
+                        "two of the states share memory");
+        }
+        // rows are ordered by sequence, and a sequence's rows are a multiple of 16: so are its bytes in every array
+        const int64_t rows = (int64_t)(st->lay.rows / (size_t)st->desc.batch);
+        const int64_t low = st->desc.format == SSQ_DAMP ? rows / 128 * (128 - SSQ_DAMP_NHI) : rows;
+        parts[n++] = {codes_ptr(st), low * (int64_t)st->lay.row_bytes};
+        if (scale_ptr(st)) parts[n++] = {(uint8_t*)scale_ptr(st), low * 4};
+        if (zero_ptr(st)) parts[n++] = {(uint8_t*)zero_ptr(st), low * 4};
+        if (hi_ptr(st)) parts[n++] = {(uint8_t*)hi_ptr(st), (rows - low) * 256};
+    }
+    if (beams == 1) return ok();
+    return from_hip(ssq::launch_reorder(parts, n, parents, beams, states[0]->desc.batch / beams, (hipStream_t)stream),
+                    "state reorder launch");
 }
 
 const char* ssq_status_string(int32_t status)
