@@ -108,11 +108,505 @@ __global__ __launch_bounds__(256) void k_linattn_scan(LinArgs a, int64_t units)
     store_f32<8>(p, h);
 }
 
-size_t linattn_workspace(int fmt, int nseq, int64_t tokens, int H, int P, int num_cus)
+
+// ---------------------------------------------------------------------------
+// bf16: chunks of 64 tokens on the matrix cores
+// ---------------------------------------------------------------------------
+// With c_i the sum of a chunk's g up to token i, S the state before it:
+//   o_i = scale * (exp(c_i) S q_i + sum_{j<=i} exp(c_i - c_j) (q_i.k_j) v_j)
+//   S'  = exp(c_last) S + sum_j (exp(c_last - c_j) v_j) k_j^T
+// Every exponent is a difference that is not positive, so nothing overflows; the sums c are taken
+// in double and kept as two floats, so that the difference of two far-decayed tokens is exact.
+//
+// A workgroup of four waves runs one span of tokens for up to 128 value columns that share keys:
+// two heads of 64, or one of 128.  A wave owns columns in tiles of 16 and keeps their state,
+// 16 x 128 fp32, in registers, laid out as a matrix product leaves it: lane (g, c) = (lane/16,
+// lane%16) holds column c and the key entries 32g .. 32g+31, which is at once the operand of the
+// next S q (any order of the summed index serves, if both operands have it).  Scores are
+// computed once for the heads that share keys and meet the waves through LDS, decayed per head.
+constexpr int kChunk = 64;
+constexpr int kPitch = 136;  // bf16 of a row of 128 in LDS: 16-byte reads of 8 rows fall in different banks
+constexpr int kScorePitch = 72;
+constexpr double kLog2e = 1.4426950408889634;
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c)
 {
-    (void)tokens;
-    (void)num_cus;
-    return fmt == FP32 ? 0 : (size_t)nseq * H * P * 512;
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// A block of 4 rows x 16 columns per 16 lanes, lane i naming four columns of row i/4; lane i
+// receives column i of the four rows.
+__device__ __forceinline__ bf16x4 lds_read_tr(const __bf16* p)
+{
+    typedef __attribute__((address_space(3))) i16x4* lds_ptr;
+    return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)p));
+}
+__device__ __forceinline__ bf16x8 join4(bf16x4 a, bf16x4 b)
+{
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// decays of one head over a chunk, in powers of two
+struct HeadDecay {
+    float hi[kChunk], lo[kChunk]; // c_i as the sum of two floats
+    float in[kChunk];             // exp(c_i)
+    float out[kChunk];            // exp(c_last - c_i)
+    float keep, change;           // exp(c_last) x = keep*x + change*x, keep 0 or 1: exact near 1
+};
+
+struct ChunkLds {
+    __bf16 q[kChunk][kPitch], k[kChunk][kPitch], v[kChunk][kPitch];
+    __bf16 p[2][kChunk][kScorePitch]; // decayed scores, [query][key]
+    HeadDecay d[2];
+};
+
+// exp2 of the double x, rounded to a few units of fp32 for any size of x
+__device__ __forceinline__ float exp2_of(double x)
+{
+    const float h = (float)x;
+    return __builtin_amdgcn_exp2f(h) * (1.0f + 0.6931472f * (float)(x - (double)h));
+}
+
+// one wave, lane = token of the chunk: g the token's log decay (0 behind the span's end)
+__device__ __forceinline__ void chunk_decays(float g, int lane, HeadDecay& d)
+{
+    // exp(-128) is 0 in fp32, and so is all that passes such a token
+    double c = (double)fmaxf(g, -128.0f) * kLog2e;
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+        const double up = __shfl_up(c, s);
+        if (lane >= s) c += up;
+    }
+    const double last = __shfl(c, 63);
+    d.hi[lane] = (float)c;
+    d.lo[lane] = (float)(c - (double)(float)c);
+    d.in[lane] = exp2_of(c);
+    d.out[lane] = exp2_of(last - c);
+    if (lane == 63) {
+        const double e = exp2(c);
+        d.keep = e >= 0.5 ? 1.0f : 0.0f;
+        d.change = (float)(e >= 0.5 ? e - 1.0 : e);
+    }
+}
+
+enum { WHOLE = 0, PART_STATE = 1, PART_OUT = 2 };
+
+struct ChunkArgs {
+    LinArgs a;
+    float* part_state;  // [parts][H*P][128]
+    float2* part_decay; // [parts][H]: keep, change
+    int part_tokens;    // a multiple of kChunk
+    int nparts;         // parts of all sequences at most
+    int blocks;         // column blocks
+    int block_cols;     // columns of a head in a block: P or 128
+    int pair;           // heads in a block: 1 or 2
+};
+
+// the place of a sequence's first part among all parts: sequences follow each other, each ending in a part of its own
+__device__ __forceinline__ int64_t first_part(const ChunkArgs& c, int64_t begin, int seq)
+{
+    return begin / c.part_tokens + seq;
+}
+
+template <int MODE, int NTW>
+__global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
+{
+    __shared__ ChunkLds s;
+    const LinArgs& a = c.a;
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // workgroups go to the 8 XCDs in turn: numbered so, each XCD has whole runs of blocks that share keys
+    const unsigned nb = gridDim.x;
+    const unsigned bid = nb % 8 == 0 ? (blockIdx.x % 8) * (nb / 8) + blockIdx.x / 8 : blockIdx.x;
+    const int block = bid % c.blocks;
+    const int item = bid / c.blocks;
+    int seq = item;
+    if constexpr (MODE != WHOLE) { // the last sequence whose first part is not behind the item
+        int lo = 0, hi = a.nseq - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            const SeqSpan m = seq_span(a, mid);
+            if (first_part(c, m.begin, mid) <= item) lo = mid;
+            else hi = mid - 1;
+        }
+        seq = lo;
+    }
+    const SeqSpan span = seq_span(a, seq);
+    if (span.slot < 0) return;
+    const bool fresh = a.fresh && a.fresh[seq];
+    int64_t begin = span.begin, end = span.end;
+    if constexpr (MODE == WHOLE) {
+        if (begin == end && !fresh) return;
+    } else {
+        const int64_t part = (int64_t)item - first_part(c, span.begin, seq);
+        begin += part * c.part_tokens;
+        if (part < 0 || begin >= end) return; // a place of no part
+        if (end > begin + c.part_tokens) end = begin + c.part_tokens;
+    }
+    // columns: heads head0 .. head0 + nh - 1 from column p0 of each
+    const int share = a.H / a.G;
+    int head0, nh, p0;
+    if (c.pair == 2) {
+        const int per_group = (share + 1) / 2;
+        head0 = block / per_group * share + block % per_group * 2;
+        nh = min(2, share - block % per_group * 2);
+        p0 = 0;
+    } else {
+        const int per_head = (a.P + c.block_cols - 1) / c.block_cols;
+        head0 = block / per_head;
+        nh = 1;
+        p0 = block % per_head * c.block_cols;
+    }
+    const int head_tiles = min(c.block_cols, a.P - p0) / 16, tiles = nh * head_tiles;
+    const int64_t col0 = (int64_t)head0 * a.P + p0; // of v and o, and the row of the state
+    const int kvh = head0 / share;
+
+    const __bf16* qp = static_cast<const __bf16*>(a.q) + kvh * 128;
+    const __bf16* kp = static_cast<const __bf16*>(a.k) + kvh * 128;
+    const __bf16* vp = static_cast<const __bf16*>(a.v) + col0;
+
+    // this wave's tiles: wave, wave + 4; their head within the block
+    int tile_head[NTW];
+    bool have[NTW];
+#pragma unroll
+    for (int x = 0; x < NTW; ++x) {
+        have[x] = wave + 4 * x < tiles;
+        tile_head[x] = have[x] ? (wave + 4 * x) / head_tiles : 0;
+    }
+
+    f32x4 S[NTW][8]; // n-tile t: entries 32g + 4t .. 32g + 4t + 3 of column l16
+    float* rows = nullptr;
+    if constexpr (MODE == WHOLE) rows = seq_rows(a, seq, span.slot) + col0 * 128;
+    else rows = c.part_state + ((int64_t)item * a.H * a.P + col0) * 128;
+#pragma unroll
+    for (int x = 0; x < NTW; ++x) {
+#pragma unroll
+        for (int t = 0; t < 8; ++t) S[x][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (have[x] && MODE != PART_STATE && !(MODE == WHOLE && fresh)) {
+            const f32x4* r = reinterpret_cast<const f32x4*>(rows + ((wave + 4 * x) * 16 + l16) * 128 + 32 * g);
+#pragma unroll
+            for (int t = 0; t < 8; ++t) S[x][t] = r[t];
+        }
+    }
+    if constexpr (MODE != PART_STATE) { // the tiles above the diagonal stay zero
+        for (int i = tid; i < 2 * kChunk * kScorePitch / 2; i += 256) reinterpret_cast<uint32_t*>(s.p)[i] = 0;
+    }
+
+    // 16 pieces of 16 bytes a row, 16 rows at once
+    const int prow = tid >> 4, piece = tid & 15;
+    const bool vpiece = piece * 8 < tiles * 16;
+    u32x4 rq[4], rk[4], rv[4];
+    float rg = 0.0f;
+    auto fetch = [&](int64_t t0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t t = t0 + prow + 16 * i;
+            const u32x4 z = {0, 0, 0, 0};
+            rq[i] = rk[i] = rv[i] = z;
+            if (t < end) {
+                if constexpr (MODE != PART_STATE) rq[i] = *reinterpret_cast<const u32x4*>(qp + t * a.qs + piece * 8);
+                rk[i] = *reinterpret_cast<const u32x4*>(kp + t * a.ks + piece * 8);
+                if (vpiece) rv[i] = *reinterpret_cast<const u32x4*>(vp + t * a.vs + piece * 8);
+            }
+        }
+        rg = 0.0f;
+        if (wave < nh && a.g && t0 + lane < end) rg = a.g[(t0 + lane) * a.gs + head0 + wave];
+    };
+    double total = 0.0; // PART_STATE: the head's decay over the part, in waves 0 .. nh-1
+    fetch(begin);
+    for (int64_t t0 = begin; t0 < end; t0 += kChunk) {
+        __syncthreads(); // the previous chunk has been read
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = prow + 16 * i;
+            if constexpr (MODE != PART_STATE) *reinterpret_cast<u32x4*>(&s.q[r][piece * 8]) = rq[i];
+            *reinterpret_cast<u32x4*>(&s.k[r][piece * 8]) = rk[i];
+            *reinterpret_cast<u32x4*>(&s.v[r][piece * 8]) = rv[i];
+        }
+        if (wave < nh) {
+            chunk_decays(rg, lane, s.d[wave]);
+            if constexpr (MODE == PART_STATE) {
+                double x = (double)fmaxf(rg, -128.0f) * kLog2e;
+#pragma unroll
+                for (int d = 32; d; d >>= 1) x += __shfl_xor(x, d);
+                total += x;
+            }
+        }
+        __syncthreads();
+        if (t0 + kChunk < end) fetch(t0 + kChunk);
+
+        f32x4 O[NTW][4]; // query tile i: columns of this tile 4g .. 4g+3, query l16
+        if constexpr (MODE != PART_STATE) {
+            // scores of the queries 16*wave .. +15: rows keys, columns queries
+            f32x4 A[4];
+            bf16x8 qf[4];
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) qf[ks] = *reinterpret_cast<const bf16x8*>(&s.q[wave * 16 + l16][ks * 32 + g * 8]);
+#pragma unroll
+            for (int jt = 0; jt < 4; ++jt) {
+                A[jt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                if (jt <= wave) {
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        A[jt] = mfma(*reinterpret_cast<const bf16x8*>(&s.k[jt * 16 + l16][ks * 32 + g * 8]), qf[ks], A[jt]);
+                }
+            }
+            const int qi = wave * 16 + l16;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (h >= nh) break;
+                const float ih = s.d[h].hi[qi], il = s.d[h].lo[qi];
+#pragma unroll
+                for (int jt = 0; jt < 4; ++jt) {
+                    if (jt > wave) break;
+                    const int j0 = jt * 16 + g * 4;
+                    const float4 jh = *reinterpret_cast<const float4*>(&s.d[h].hi[j0]);
+                    const float4 jl = *reinterpret_cast<const float4*>(&s.d[h].lo[j0]);
+                    const float jhs[4] = {jh.x, jh.y, jh.z, jh.w}, jls[4] = {jl.x, jl.y, jl.z, jl.w};
+                    bf16x4 w;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float e = __builtin_amdgcn_exp2f((ih - jhs[r]) + (il - jls[r]));
+                        w[r] = (__bf16)(j0 + r <= qi ? A[jt][r] * e : 0.0f);
+                    }
+                    *reinterpret_cast<bf16x4*>(&s.p[h][qi][j0]) = w;
+                }
+            }
+            // S q, the state as the sum of two bf16
+#pragma unroll
+            for (int x = 0; x < NTW; ++x)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) O[x][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+                bf16x8 hi[NTW], lo[NTW];
+#pragma unroll
+                for (int x = 0; x < NTW; ++x)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float v = S[x][2 * ks + e / 4][e % 4];
+                        hi[x][e] = (__bf16)v;
+                        lo[x][e] = (__bf16)(v - (float)hi[x][e]);
+                    }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const bf16x8 qq = *reinterpret_cast<const bf16x8*>(&s.q[i * 16 + l16][g * 32 + ks * 8]);
+#pragma unroll
+                    for (int x = 0; x < NTW; ++x) {
+                        O[x][i] = mfma(hi[x], qq, O[x][i]);
+                        O[x][i] = mfma(lo[x], qq, O[x][i]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < NTW; ++x)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float e = s.d[tile_head[x]].in[i * 16 + l16];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) O[x][i][r] *= e;
+                }
+            __syncthreads(); // the scores are written
+        }
+        bf16x8 vf[NTW][2]; // this wave's columns of v: column l16, tokens 32*kb + 8g .. +7
+#pragma unroll
+        for (int x = 0; x < NTW; ++x)
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                const int col = (wave + 4 * x) % 8 * 16 + 4 * (l16 & 3);
+                const int row = kb * 32 + g * 8 + (l16 >> 2);
+                vf[x][kb] = join4(lds_read_tr(&s.v[row][col]), lds_read_tr(&s.v[row + 4][col]));
+            }
+        if constexpr (MODE != PART_STATE) {
+#pragma unroll
+            for (int x = 0; x < NTW; ++x) {
+                if (!have[x]) break;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                    for (int kb = 0; kb <= i / 2; ++kb)
+                        O[x][i] = mfma(vf[x][kb], *reinterpret_cast<const bf16x8*>(&s.p[tile_head[x]][i * 16 + l16][kb * 32 + g * 8]), O[x][i]);
+                    const int64_t t = t0 + i * 16 + l16;
+                    if (t < end) {
+                        bf16x4 w;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) w[r] = (__bf16)(a.oscale * O[x][i][r]);
+                        *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(a.o) + t * a.os + col0 + (wave + 4 * x) * 16 + 4 * g) = w;
+                    }
+                }
+            }
+        }
+        // the state: decayed, and the chunk's writes with v's decay, as the sum of three bf16
+        if (MODE == PART_OUT && t0 + kChunk >= end) break; // the next part has its own
+#pragma unroll
+        for (int x = 0; x < NTW; ++x) {
+            const float keep = s.d[tile_head[x]].keep, change = s.d[tile_head[x]].change;
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) S[x][t][r] = __builtin_fmaf(S[x][t][r], change, S[x][t][r] * keep);
+        }
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            bf16x8 w[NTW][3];
+#pragma unroll
+            for (int x = 0; x < NTW; ++x) {
+                const float* od = &s.d[tile_head[x]].out[kb * 32 + g * 8];
+                const float4 o0 = *reinterpret_cast<const float4*>(od), o1 = *reinterpret_cast<const float4*>(od + 4);
+                const float oe[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float v = (float)vf[x][kb][e] * oe[e];
+#pragma unroll
+                    for (int j = 0; j < 3; ++j) {
+                        w[x][j][e] = (__bf16)v;
+                        v -= (float)w[x][j][e];
+                    }
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                const int col = (l16 & 3) * 32 + t * 4;
+                const int row = kb * 32 + g * 8 + (l16 >> 2);
+                const bf16x8 kf = join4(lds_read_tr(&s.k[row][col]), lds_read_tr(&s.k[row + 4][col]));
+#pragma unroll
+                for (int x = 0; x < NTW; ++x)
+#pragma unroll
+                    for (int j = 0; j < 3; ++j) S[x][t] = mfma(kf, w[x][j], S[x][t]);
+            }
+        }
+    }
+    if constexpr (MODE != PART_OUT) {
+#pragma unroll
+        for (int x = 0; x < NTW; ++x)
+            if (have[x]) {
+                f32x4* r = reinterpret_cast<f32x4*>(rows + ((wave + 4 * x) * 16 + l16) * 128 + 32 * g);
+#pragma unroll
+                for (int t = 0; t < 8; ++t) r[t] = S[x][t];
+            }
+    }
+    if constexpr (MODE == PART_STATE) {
+        if (wave < nh && lane == 0 && p0 == 0) {
+            const double e = exp2(total);
+            c.part_decay[(int64_t)item * a.H + head0 + wave] =
+                make_float2(e >= 0.5 ? 1.0f : 0.0f, (float)(e >= 0.5 ? e - 1.0 : e));
+        }
+    }
+}
+
+// The states before each part, from the parts' own, and the state after the last: a thread has
+// four entries of one (sequence, head).
+__global__ __launch_bounds__(256) void k_linattn_join(ChunkArgs c, int64_t units)
+{
+    const LinArgs& a = c.a;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= units) return;
+    const int64_t per_seq = (int64_t)a.H * a.P * 32;
+    const int seq = (int)(i / per_seq);
+    const int64_t e = i % per_seq;
+    const int head = (int)(e / ((int64_t)a.P * 32));
+    const SeqSpan span = seq_span(a, seq);
+    const bool fresh = a.fresh && a.fresh[seq];
+    if (span.slot < 0 || (span.begin == span.end && !fresh)) return;
+    f32x4* state = reinterpret_cast<f32x4*>(seq_rows(a, seq, span.slot)) + e;
+    f32x4 S = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (!fresh) S = *state;
+    const int64_t n = (span.end - span.begin + c.part_tokens - 1) / c.part_tokens;
+    const int64_t p0 = first_part(c, span.begin, seq);
+    for (int64_t p = p0; p < p0 + n; ++p) {
+        f32x4* part = reinterpret_cast<f32x4*>(c.part_state) + p * per_seq + e;
+        const f32x4 own = *part;
+        const float2 d = c.part_decay[p * a.H + head];
+        *part = S;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S[r] = __builtin_fmaf(S[r], d.y, S[r] * d.x) + own[r];
+    }
+    *state = S;
+}
+
+// ---------------------------------------------------------------------------
+// launch
+// ---------------------------------------------------------------------------
+struct ChunkPlan {
+    int blocks, block_cols, pair;
+    int part_tokens; // 0: sequences are not split
+    int64_t nparts;
+};
+
+// The columns of a block: two heads of up to 64 columns where they share keys, else up to 128 of
+// one head.
+static ChunkPlan chunk_plan(int nseq, int64_t tokens, int H, int G, int P, int num_cus)
+{
+    ChunkPlan p;
+    const int share = H / G;
+    if (P <= 64 && share > 1) {
+        p.pair = 2;
+        p.block_cols = P;
+        p.blocks = G * ((share + 1) / 2);
+    } else {
+        p.pair = 1;
+        p.block_cols = P < 128 ? P : 128;
+        p.blocks = H * ((P + 127) / 128);
+    }
+    p.part_tokens = 0;
+    p.nparts = 0;
+    const int64_t chunks = (tokens + kChunk - 1) / kChunk;
+    const int64_t slots = 2 * (int64_t)num_cus; // workgroups at once
+    if (chunks > 2 && nseq * (int64_t)p.blocks < slots) {
+        int64_t per = (chunks * p.blocks + slots - 1) / slots;
+        if (per < 2) per = 2;
+        p.part_tokens = (int)(per * kChunk);
+        p.nparts = tokens / p.part_tokens + nseq;
+    }
+    return p;
+}
+
+static size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+size_t linattn_workspace(int fmt, int nseq, int64_t tokens, int H, int G, int P, int num_cus)
+{
+    const ChunkPlan p = chunk_plan(nseq, tokens, H, G, P, num_cus);
+    const size_t rows = (size_t)H * P;
+    return (fmt == FP32 ? 0 : (size_t)nseq * rows * 512) + p.nparts * rows * 512 + align256(p.nparts * H * sizeof(float2));
+}
+
+template <int MODE>
+static hipError_t launch_chunk(const ChunkArgs& c, int64_t items, hipStream_t st)
+{
+    const int64_t blocks = items * c.blocks;
+    if (blocks > kMaxBlocks) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)blocks), wg(256);
+    if (c.pair * c.block_cols <= 64) hipLaunchKernelGGL((k_linattn_chunk<MODE, 1>), grid, wg, 0, st, c);
+    else hipLaunchKernelGGL((k_linattn_chunk<MODE, 2>), grid, wg, 0, st, c);
+    return hipGetLastError();
+}
+
+static hipError_t launch_chunks(const LinArgs& a, void* ws, int num_cus, hipStream_t st)
+{
+    const ChunkPlan p = chunk_plan(a.nseq, a.tokens, a.H, a.G, a.P, num_cus);
+    ChunkArgs c{};
+    c.a = a;
+    c.blocks = p.blocks;
+    c.block_cols = p.block_cols;
+    c.pair = p.pair;
+    if (p.part_tokens == 0) return launch_chunk<WHOLE>(c, a.nseq, st);
+    c.part_tokens = p.part_tokens;
+    c.nparts = (int)p.nparts;
+    c.part_state = static_cast<float*>(ws);
+    c.part_decay = reinterpret_cast<float2*>(c.part_state + p.nparts * a.H * a.P * 128);
+    hipError_t e = launch_chunk<PART_STATE>(c, p.nparts, st);
+    if (e != hipSuccess) return e;
+    const int64_t units = (int64_t)a.nseq * a.H * a.P * 32, blocks = (units + 255) / 256;
+    if (blocks > kMaxBlocks) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(k_linattn_join, dim3((unsigned)blocks), dim3(256), 0, st, c, units);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    return launch_chunk<PART_OUT>(c, p.nparts, st);
 }
 
 template <int F>
@@ -140,10 +634,13 @@ static hipError_t state_rows(int fmt, const LinArgs& a, bool store, hipStream_t 
 
 hipError_t launch_linattn_prefill(int fmt, int dtype, const LinArgs& args, void* ws, int num_cus, hipStream_t st)
 {
-    (void)num_cus;
     LinArgs a = args;
-    if (fmt == FP32) a.codes = nullptr;
-    else a.h32 = static_cast<float*>(ws);
+    if (fmt == FP32) {
+        a.codes = nullptr;
+    } else {
+        a.h32 = static_cast<float*>(ws);
+        ws = a.h32 + (int64_t)a.nseq * a.H * a.P * 128;
+    }
     hipError_t e = state_rows(fmt, a, false, st);
     if (e != hipSuccess) return e;
     const int64_t units = (int64_t)a.nseq * a.H * a.P / 4, blocks = (units + 3) / 4;
@@ -151,11 +648,11 @@ hipError_t launch_linattn_prefill(int fmt, int dtype, const LinArgs& args, void*
     const dim3 grid((unsigned)blocks), wg(256);
     switch (dtype) {
     case DT_FP32: hipLaunchKernelGGL(k_linattn_scan<DT_FP32>, grid, wg, 0, st, a, units); break;
-    case DT_BF16: hipLaunchKernelGGL(k_linattn_scan<DT_BF16>, grid, wg, 0, st, a, units); break;
+    case DT_BF16: e = launch_chunks(a, ws, num_cus, st); break;
     case DT_FP16: hipLaunchKernelGGL(k_linattn_scan<DT_FP16>, grid, wg, 0, st, a, units); break;
     default: return hipErrorInvalidValue;
     }
-    e = hipGetLastError();
+    if (e == hipSuccess) e = hipGetLastError();
     if (e != hipSuccess) return e;
     return state_rows(fmt, a, true, st);
 }

@@ -427,6 +427,24 @@ def test_offsets_outside_the_tensors_are_clamped():
         check_state(state[i], ws, sm, b - a, f"sequence {i}")
 
 
+@pytest.mark.parametrize("heads", [1, 40])
+def test_rows_before_the_first_sequence(heads):
+    say("rows before", heads)
+    gen = torch.Generator().manual_seed(16)
+    P, T, a, b = 64, 2000, 700, 1900
+    q, k, v, g = ref.inputs(gen, T, heads, 1, P, BF)
+    st = state_of(torch.zeros(2, heads, P, 128), 1)
+    o = torch.full_like(v, SENTINEL).cuda()
+    cu = torch.tensor([a, a + 300, b], dtype=torch.int32, device="cuda")
+    ssq.ssq_linattn_prefill(st, q.cuda(), k.cuda(), v.cuda(), g.cuda(), o, cu)
+    o, state = o.cpu(), values_of(st)
+    assert (o[:a] == SENTINEL).all() and (o[b:] == SENTINEL).all()
+    for i, s in enumerate((slice(a, a + 300), slice(a + 300, b))):
+        wo, ws, om, sm = ref.recurrence(q[s], k[s], v[s], g[s], torch.zeros(heads, P, 128), 1.0)
+        check_o(o[s], wo, om, 1200, BF, i)
+        check_state(state[i], ws, sm, 1200, i)
+
+
 def test_refusals():
     st = state_of(torch.zeros(2, 4, 32, 128), 2)
     t = lambda *s, d=BF: torch.zeros(*s, dtype=d, device="cuda")  # noqa: E731
