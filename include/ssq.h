@@ -322,8 +322,8 @@ ssq_status ssq_stream_copy(void *dst, const void *src, size_t bytes, void *strea
  * heads are packed within a token.  g [tokens][nheads] is fp32, g <= 0
  * (-infinity forgets the state; NULL: no decay), with a stride of its own (0:
  * the same decay at every token).  q, k, v and o and their strides in bytes
- * are multiples of 16, the strides of q, k, v and g are >= 0 and o's is at
- * least nheads*P.  o overlaps no input.  The state, every sum and every decay
+ * are multiples of 16, no stride but g's is shorter than a token's row, and
+ * none exceeds 2^23 elements.  o overlaps no input.  The state, every sum and every decay
  * are fp32 or wider; o is rounded once to `dtype`.
  *
  * slots: device int32 [nseq], the sequence of the state (0 .. batch-1) that

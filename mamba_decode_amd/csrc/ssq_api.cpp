@@ -511,17 +511,15 @@ static ssq_status fill_linattn(ssq_state* st, const ssq_linattn_io* io, int32_t 
                 SSQ_ERR_INVALID_ARG, "q, k, v and o must be 16-byte aligned");
     SSQ_REQUIRE(aligned(io->g, 4) && aligned(slots, 4), SSQ_ERR_INVALID_ARG, "g and slots must be 4-byte aligned");
     const int64_t unit = io->dtype == SSQ_DTYPE_FP32 ? 4 : 8; // elements in 16 bytes
-    SSQ_REQUIRE(io->q_stride >= 0 && io->k_stride >= 0 && io->v_stride >= 0 && io->g_stride >= 0, SSQ_ERR_INVALID_ARG,
-                "strides must not be negative");
     SSQ_REQUIRE(io->q_stride % unit == 0 && io->k_stride % unit == 0 && io->v_stride % unit == 0 && io->o_stride % unit == 0,
                 SSQ_ERR_INVALID_ARG, "the strides of q, k, v and o must be multiples of 16 bytes");
-    const int64_t row = (int64_t)st->desc.nheads * st->desc.rows_per_head;
-    SSQ_REQUIRE(tokens <= 1 || io->o_stride >= row, SSQ_ERR_INVALID_ARG, "the stride of o must be at least nheads*P");
-    // every offset a kernel forms stays below 2^62 bytes
-    const int64_t most = ((int64_t)1 << 59) / (tokens > 0 ? tokens : 1);
-    SSQ_REQUIRE(io->q_stride <= most && io->k_stride <= most && io->v_stride <= most && io->g_stride <= most &&
-                    io->o_stride <= most, SSQ_ERR_INVALID_ARG, "a stride is too large");
-    SSQ_REQUIRE(row <= ((int64_t)1 << 31) - 1, SSQ_ERR_UNSUPPORTED, "nheads*P must be below 2^31");
+    const int64_t row = (int64_t)st->desc.nheads * st->desc.rows_per_head, kv_row = (int64_t)st->desc.ngroups * 128;
+    SSQ_REQUIRE(io->q_stride >= kv_row && io->k_stride >= kv_row && io->v_stride >= row && io->o_stride >= row && io->g_stride >= 0,
+                SSQ_ERR_INVALID_ARG, "a stride is shorter than a token's row");
+    // a chunk's offsets stay below 2^31 bytes
+    const int64_t most = (int64_t)1 << 23;
+    SSQ_REQUIRE(io->q_stride <= most && io->k_stride <= most && io->v_stride <= most && io->g_stride <= most && io->o_stride <= most,
+                SSQ_ERR_UNSUPPORTED, "strides must not exceed 2^23 elements");
     ssq_status s = check_device(st);
     if (s != SSQ_OK) return s;
     *a = ssq::LinArgs{};

@@ -133,6 +133,8 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c)
 {
@@ -151,18 +153,29 @@ __device__ __forceinline__ bf16x8 join4(bf16x4 a, bf16x4 b)
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
+// two values rounded to nearest, ties to even, in one instruction; and back
+__device__ __forceinline__ bf16x2 to_bf16(float x, float y)
+{
+    return __builtin_convertvector(f32x2{x, y}, bf16x2);
+}
+__device__ __forceinline__ f32x2 from_bf16(bf16x2 v)
+{
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    return f32x2{__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u)};
+}
+
 // decays of one head over a chunk, in powers of two
-struct HeadDecay {
+struct alignas(16) HeadDecay {
     float hi[kChunk], lo[kChunk]; // c_i as the sum of two floats
     float in[kChunk];             // exp(c_i)
     float out[kChunk];            // exp(c_last - c_i)
     float keep, change;           // exp(c_last) x = keep*x + change*x, keep 0 or 1: exact near 1
 };
 
-struct ChunkLds {
+struct alignas(16) ChunkLds {
     __bf16 q[kChunk][kPitch], k[kChunk][kPitch], v[kChunk][kPitch];
     __bf16 p[2][kChunk][kScorePitch]; // decayed scores, [query][key]
-    HeadDecay d[2];
+    HeadDecay d[2][2]; // of this chunk and the next
 };
 
 // exp2 of the double x, rounded to a few units of fp32 for any size of x
@@ -173,7 +186,8 @@ __device__ __forceinline__ float exp2_of(double x)
 }
 
 // one wave, lane = token of the chunk: g the token's log decay (0 behind the span's end)
-__device__ __forceinline__ void chunk_decays(float g, int lane, HeadDecay& d)
+// returns the sum of all
+__device__ __forceinline__ double chunk_decays(float g, int lane, HeadDecay& d)
 {
     // exp(-128) is 0 in fp32, and so is all that passes such a token
     double c = (double)fmaxf(g, -128.0f) * kLog2e;
@@ -192,6 +206,7 @@ __device__ __forceinline__ void chunk_decays(float g, int lane, HeadDecay& d)
         d.keep = e >= 0.5 ? 1.0f : 0.0f;
         d.change = (float)(e >= 0.5 ? e - 1.0 : e);
     }
+    return last;
 }
 
 enum { WHOLE = 0, PART_STATE = 1, PART_OUT = 2 };
@@ -269,6 +284,7 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
     const __bf16* qp = static_cast<const __bf16*>(a.q) + kvh * 128;
     const __bf16* kp = static_cast<const __bf16*>(a.k) + kvh * 128;
     const __bf16* vp = static_cast<const __bf16*>(a.v) + col0;
+    __bf16* op = static_cast<__bf16*>(a.o) + col0;
 
     // this wave's tiles: wave, wave + 4; their head within the block
     int tile_head[NTW];
@@ -297,29 +313,36 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
         for (int i = tid; i < 2 * kChunk * kScorePitch / 2; i += 256) reinterpret_cast<uint32_t*>(s.p)[i] = 0;
     }
 
-    // 16 pieces of 16 bytes a row, 16 rows at once
-    const int prow = tid >> 4, piece = tid & 15;
-    const bool vpiece = piece * 8 < tiles * 16;
+    // Tiles come and go through buffer descriptors that end with the span: rows behind it read 0
+    // and are not written.  16 pieces of 16 bytes a row, 16 rows at once.
+    const uint32_t piece = tid & 15, prow = tid >> 4;
+    const uint32_t q_row = (uint32_t)a.qs * 2, k_row = (uint32_t)a.ks * 2, v_row = (uint32_t)a.vs * 2, o_row = (uint32_t)a.os * 2;
+    const uint32_t q_off = prow * q_row + piece * 16, k_off = prow * k_row + piece * 16;
+    const uint32_t v_off = piece * 8 < (uint32_t)tiles * 16 ? prow * v_row + piece * 16 : 0x80000000u; // no such column: 0
     u32x4 rq[4], rk[4], rv[4];
     float rg = 0.0f;
     auto fetch = [&](int64_t t0) {
+        const uint32_t last = (uint32_t)(end - t0 < kChunk ? end - t0 : kChunk) - 1;
+        const Rsrc bq = make_rsrc(qp + t0 * a.qs, last * q_row + 256);
+        const Rsrc bk = make_rsrc(kp + t0 * a.ks, last * k_row + 256);
+        const Rsrc bv = make_rsrc(vp + t0 * a.vs, last * v_row + tiles * 32);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t t = t0 + prow + 16 * i;
-            const u32x4 z = {0, 0, 0, 0};
-            rq[i] = rk[i] = rv[i] = z;
-            if (t < end) {
-                if constexpr (MODE != PART_STATE) rq[i] = *reinterpret_cast<const u32x4*>(qp + t * a.qs + piece * 8);
-                rk[i] = *reinterpret_cast<const u32x4*>(kp + t * a.ks + piece * 8);
-                if (vpiece) rv[i] = *reinterpret_cast<const u32x4*>(vp + t * a.vs + piece * 8);
-            }
+            if constexpr (MODE != PART_STATE) rq[i] = __builtin_amdgcn_raw_buffer_load_b128(bq, q_off + 16 * i * q_row, 0, 0);
+            rk[i] = __builtin_amdgcn_raw_buffer_load_b128(bk, k_off + 16 * i * k_row, 0, 0);
+            rv[i] = __builtin_amdgcn_raw_buffer_load_b128(bv, v_off + 16 * i * v_row, 0, 0);
         }
         rg = 0.0f;
         if (wave < nh && a.g && t0 + lane < end) rg = a.g[(t0 + lane) * a.gs + head0 + wave];
     };
     double total = 0.0; // PART_STATE: the head's decay over the part, in waves 0 .. nh-1
-    fetch(begin);
-    for (int64_t t0 = begin; t0 < end; t0 += kChunk) {
+    if (begin < end) { // an empty sequence has no row that a descriptor could end with
+        fetch(begin);
+        if (wave < nh) total += chunk_decays(rg, lane, s.d[0][wave]);
+    }
+    int buf = 0;
+    for (int64_t t0 = begin; t0 < end; t0 += kChunk, buf ^= 1) {
+        const HeadDecay* const sd = s.d[buf];
         __syncthreads(); // the previous chunk has been read
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -328,17 +351,9 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
             *reinterpret_cast<u32x4*>(&s.k[r][piece * 8]) = rk[i];
             *reinterpret_cast<u32x4*>(&s.v[r][piece * 8]) = rv[i];
         }
-        if (wave < nh) {
-            chunk_decays(rg, lane, s.d[wave]);
-            if constexpr (MODE == PART_STATE) {
-                double x = (double)fmaxf(rg, -128.0f) * kLog2e;
-#pragma unroll
-                for (int d = 32; d; d >>= 1) x += __shfl_xor(x, d);
-                total += x;
-            }
-        }
         __syncthreads();
-        if (t0 + kChunk < end) fetch(t0 + kChunk);
+        const bool more = t0 + kChunk < end;
+        if (more) fetch(t0 + kChunk);
 
         f32x4 O[NTW][4]; // query tile i: columns of this tile 4g .. 4g+3, query l16
         if constexpr (MODE != PART_STATE) {
@@ -360,21 +375,22 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 if (h >= nh) break;
-                const float ih = s.d[h].hi[qi], il = s.d[h].lo[qi];
+                const float ih = sd[h].hi[qi], il = sd[h].lo[qi];
 #pragma unroll
                 for (int jt = 0; jt < 4; ++jt) {
                     if (jt > wave) break;
                     const int j0 = jt * 16 + g * 4;
-                    const float4 jh = *reinterpret_cast<const float4*>(&s.d[h].hi[j0]);
-                    const float4 jl = *reinterpret_cast<const float4*>(&s.d[h].lo[j0]);
+                    const float4 jh = *reinterpret_cast<const float4*>(&sd[h].hi[j0]);
+                    const float4 jl = *reinterpret_cast<const float4*>(&sd[h].lo[j0]);
                     const float jhs[4] = {jh.x, jh.y, jh.z, jh.w}, jls[4] = {jl.x, jl.y, jl.z, jl.w};
-                    bf16x4 w;
+                    float w[4];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const float e = __builtin_amdgcn_exp2f((ih - jhs[r]) + (il - jls[r]));
-                        w[r] = (__bf16)(j0 + r <= qi ? A[jt][r] * e : 0.0f);
+                        w[r] = j0 + r <= qi ? A[jt][r] * e : 0.0f;
                     }
-                    *reinterpret_cast<bf16x4*>(&s.p[h][qi][j0]) = w;
+                    const bf16x2 w01 = to_bf16(w[0], w[1]), w23 = to_bf16(w[2], w[3]);
+                    *reinterpret_cast<bf16x4*>(&s.p[h][qi][j0]) = __builtin_shufflevector(w01, w23, 0, 1, 2, 3);
                 }
             }
             // S q, the state as the sum of two bf16
@@ -388,10 +404,15 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
 #pragma unroll
                 for (int x = 0; x < NTW; ++x)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float v = S[x][2 * ks + e / 4][e % 4];
-                        hi[x][e] = (__bf16)v;
-                        lo[x][e] = (__bf16)(v - (float)hi[x][e]);
+                    for (int e = 0; e < 8; e += 2) {
+                        const float v0 = S[x][2 * ks + e / 4][e % 4], v1 = S[x][2 * ks + e / 4][e % 4 + 1];
+                        const bf16x2 h = to_bf16(v0, v1);
+                        const f32x2 f = from_bf16(h);
+                        const bf16x2 l = to_bf16(v0 - f.x, v1 - f.y);
+                        hi[x][e] = h.x;
+                        hi[x][e + 1] = h.y;
+                        lo[x][e] = l.x;
+                        lo[x][e + 1] = l.y;
                     }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -407,7 +428,7 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
             for (int x = 0; x < NTW; ++x)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float e = s.d[tile_head[x]].in[i * 16 + l16];
+                    const float e = sd[tile_head[x]].in[i * 16 + l16];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) O[x][i][r] *= e;
                 }
@@ -423,6 +444,8 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
                 vf[x][kb] = join4(lds_read_tr(&s.v[row][col]), lds_read_tr(&s.v[row + 4][col]));
             }
         if constexpr (MODE != PART_STATE) {
+            const uint32_t last = (uint32_t)(end - t0 < kChunk ? end - t0 : kChunk) - 1;
+            const Rsrc bo = make_rsrc(op + t0 * a.os, last * o_row + tiles * 32);
 #pragma unroll
             for (int x = 0; x < NTW; ++x) {
                 if (!have[x]) break;
@@ -431,21 +454,17 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
 #pragma unroll
                     for (int kb = 0; kb <= i / 2; ++kb)
                         O[x][i] = mfma(vf[x][kb], *reinterpret_cast<const bf16x8*>(&s.p[tile_head[x]][i * 16 + l16][kb * 32 + g * 8]), O[x][i]);
-                    const int64_t t = t0 + i * 16 + l16;
-                    if (t < end) {
-                        bf16x4 w;
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) w[r] = (__bf16)(a.oscale * O[x][i][r]);
-                        *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(a.o) + t * a.os + col0 + (wave + 4 * x) * 16 + 4 * g) = w;
-                    }
+                    const f32x4 w = a.oscale * O[x][i];
+                    const u32x2 w4 = {__builtin_bit_cast(uint32_t, to_bf16(w.x, w.y)), __builtin_bit_cast(uint32_t, to_bf16(w.z, w.w))};
+                    __builtin_amdgcn_raw_buffer_store_b64(w4, bo, (i * 16 + l16) * o_row + (wave + 4 * x) * 32 + 8 * g, 0, 0);
                 }
             }
         }
         // the state: decayed, and the chunk's writes with v's decay, as the sum of three bf16
-        if (MODE == PART_OUT && t0 + kChunk >= end) break; // the next part has its own
+        if (MODE == PART_OUT && !more) break; // the next part has its own
 #pragma unroll
         for (int x = 0; x < NTW; ++x) {
-            const float keep = s.d[tile_head[x]].keep, change = s.d[tile_head[x]].change;
+            const float keep = sd[tile_head[x]].keep, change = sd[tile_head[x]].change;
 #pragma unroll
             for (int t = 0; t < 8; ++t)
 #pragma unroll
@@ -456,16 +475,22 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
             bf16x8 w[NTW][3];
 #pragma unroll
             for (int x = 0; x < NTW; ++x) {
-                const float* od = &s.d[tile_head[x]].out[kb * 32 + g * 8];
+                const float* od = &sd[tile_head[x]].out[kb * 32 + g * 8];
                 const float4 o0 = *reinterpret_cast<const float4*>(od), o1 = *reinterpret_cast<const float4*>(od + 4);
                 const float oe[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float v = (float)vf[x][kb][e] * oe[e];
+                for (int e = 0; e < 8; e += 2) {
+                    f32x2 v = from_bf16(bf16x2{vf[x][kb][e], vf[x][kb][e + 1]});
+                    v.x *= oe[e];
+                    v.y *= oe[e + 1];
 #pragma unroll
                     for (int j = 0; j < 3; ++j) {
-                        w[x][j][e] = (__bf16)v;
-                        v -= (float)w[x][j][e];
+                        const bf16x2 h = to_bf16(v.x, v.y);
+                        const f32x2 f = from_bf16(h);
+                        w[x][j][e] = h.x;
+                        w[x][j][e + 1] = h.y;
+                        v.x -= f.x;
+                        v.y -= f.y;
                     }
                 }
             }
@@ -480,6 +505,7 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
                     for (int j = 0; j < 3; ++j) S[x][t] = mfma(kf, w[x][j], S[x][t]);
             }
         }
+        if (more && wave < nh) total += chunk_decays(rg, lane, s.d[buf ^ 1][wave]);
     }
     if constexpr (MODE != PART_OUT) {
 #pragma unroll
