@@ -216,8 +216,9 @@ struct ChunkArgs {
     float* part_state;  // [parts][H*P][128]
     float2* part_decay; // [parts][H]: keep, change
     int part_tokens;    // a multiple of kChunk
-    int nparts;         // parts of all sequences at most
+    int items;          // sequences, or parts at most
     int blocks;         // column blocks
+    int run, runs;      // blocks on an XCD together, and such runs in `blocks`
     int block_cols;     // columns of a head in a block: P or 128
     int pair;           // heads in a block: 1 or 2
 };
@@ -235,11 +236,13 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
     const LinArgs& a = c.a;
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    // workgroups go to the 8 XCDs in turn: numbered so, each XCD has whole runs of blocks that share keys
-    const unsigned nb = gridDim.x;
-    const unsigned bid = nb % 8 == 0 ? (blockIdx.x % 8) * (nb / 8) + blockIdx.x / 8 : blockIdx.x;
-    const int block = bid % c.blocks;
-    const int item = bid / c.blocks;
+    // Workgroups go to the 8 XCDs in turn.  Runs of `run` blocks, which share keys, are dealt to
+    // the XCDs, so that an XCD's L2 reads those keys once.
+    const unsigned at = blockIdx.x / 8;
+    const unsigned deal = at / c.run * 8 + blockIdx.x % 8;
+    const unsigned block = deal % c.runs * c.run + at % c.run;
+    const int item = deal / c.runs;
+    if (item >= c.items || block >= (unsigned)c.blocks) return;
     int seq = item;
     if constexpr (MODE != WHOLE) { // the last sequence whose first part is not behind the item
         int lo = 0, hi = a.nseq - 1;
@@ -602,9 +605,17 @@ size_t linattn_workspace(int fmt, int nseq, int64_t tokens, int H, int G, int P,
 }
 
 template <int MODE>
-static hipError_t launch_chunk(const ChunkArgs& c, int64_t items, hipStream_t st)
+static hipError_t launch_chunk(ChunkArgs c, int64_t items, hipStream_t st)
 {
-    const int64_t blocks = items * c.blocks;
+    const LinArgs& a = c.a;
+    // all the blocks of a key head, fewer where that would leave XCDs without work
+    const int share = c.blocks / a.G;
+    int cut = (int)((32 + items * a.G - 1) / (items * a.G));
+    if (cut > share) cut = share;
+    c.items = (int)items;
+    c.run = (share + cut - 1) / cut;
+    c.runs = (c.blocks + c.run - 1) / c.run;
+    const int64_t blocks = (items * c.runs + 7) / 8 * 8 * c.run;
     if (blocks > kMaxBlocks) return hipErrorInvalidValue;
     const dim3 grid((unsigned)blocks), wg(256);
     if (c.pair * c.block_cols <= 64) hipLaunchKernelGGL((k_linattn_chunk<MODE, 1>), grid, wg, 0, st, c);
@@ -622,7 +633,6 @@ static hipError_t launch_chunks(const LinArgs& a, void* ws, int num_cus, hipStre
     c.pair = p.pair;
     if (p.part_tokens == 0) return launch_chunk<WHOLE>(c, a.nseq, st);
     c.part_tokens = p.part_tokens;
-    c.nparts = (int)p.nparts;
     c.part_state = static_cast<float*>(ws);
     c.part_decay = reinterpret_cast<float2*>(c.part_state + p.nparts * a.H * a.P * 128);
     hipError_t e = launch_chunk<PART_STATE>(c, p.nparts, st);
