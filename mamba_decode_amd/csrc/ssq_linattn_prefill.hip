@@ -185,30 +185,55 @@ __device__ __forceinline__ float exp2_of(double x)
     return __builtin_amdgcn_exp2f(h) * (1.0f + 0.6931472f * (float)(x - (double)h));
 }
 
-// one wave, lane = token of the chunk: g the token's log decay (0 behind the span's end)
+// x with the double of another lane added, or 0 where the row mask or the row's end leaves none
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double add_dpp(double x)
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xF, true);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xF, true);
+    return x + __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+// a decay of 2^c as keep*x + change*x: from 1/2 up the change alone is rounded
+__device__ __forceinline__ float2 decay_of(double c)
+{
+    return c > -1.0 ? make_float2(1.0f, expm1f((float)(c * 0.6931471805599453))) : make_float2(0.0f, exp2_of(c));
+}
+
+// one wave, lane = token of the chunk: g the token's log decay (0 behind the span's end);
 // returns the sum of all
 __device__ __forceinline__ double chunk_decays(float g, int lane, HeadDecay& d)
 {
     // exp(-128) is 0 in fp32, and so is all that passes such a token
     double c = (double)fmaxf(g, -128.0f) * kLog2e;
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-        const double up = __shfl_up(c, s);
-        if (lane >= s) c += up;
-    }
-    const double last = __shfl(c, 63);
+    c = add_dpp<0x111, 0xF>(c); // sums along the rows of 16 lanes: from 1, 2, 4 and 8 lanes before
+    c = add_dpp<0x112, 0xF>(c);
+    c = add_dpp<0x114, 0xF>(c);
+    c = add_dpp<0x118, 0xF>(c);
+    c = add_dpp<0x142, 0xA>(c); // the last lane of the row before to rows 1 and 3
+    c = add_dpp<0x143, 0xC>(c); // lane 31 to rows 2 and 3
+    const uint64_t u = __builtin_bit_cast(uint64_t, c);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, 63), hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
+    const double last = __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
     d.hi[lane] = (float)c;
     d.lo[lane] = (float)(c - (double)(float)c);
     d.in[lane] = exp2_of(c);
     d.out[lane] = exp2_of(last - c);
     if (lane == 63) {
-        const double e = exp2(c);
-        d.keep = e >= 0.5 ? 1.0f : 0.0f;
-        d.change = (float)(e >= 0.5 ? e - 1.0 : e);
+        const float2 e = decay_of(c);
+        d.keep = e.x;
+        d.change = e.y;
     }
     return last;
 }
 
+#ifndef SSQ_LA_W
+#define SSQ_LA_W 4
+#endif
+#ifndef SSQ_LA_OCC
+#define SSQ_LA_OCC 2
+#endif
 enum { WHOLE = 0, PART_STATE = 1, PART_OUT = 2 };
 
 struct ChunkArgs {
@@ -229,8 +254,9 @@ __device__ __forceinline__ int64_t first_part(const ChunkArgs& c, int64_t begin,
     return begin / c.part_tokens + seq;
 }
 
-template <int MODE, int NTW>
-__global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
+// WAVES waves of NTW tiles each; HEADS heads at most (2: the blocks of a pair)
+template <int MODE, int WAVES, int NTW, int HEADS>
+__global__ __launch_bounds__(64 * WAVES, SSQ_LA_OCC) void k_linattn_chunk(ChunkArgs c)
 {
     __shared__ ChunkLds s;
     const LinArgs& a = c.a;
@@ -269,10 +295,10 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
     // columns: heads head0 .. head0 + nh - 1 from column p0 of each
     const int share = a.H / a.G;
     int head0, nh, p0;
-    if (c.pair == 2) {
+    if constexpr (HEADS == 2) {
         const int per_group = (share + 1) / 2;
         head0 = block / per_group * share + block % per_group * 2;
-        nh = min(2, share - block % per_group * 2);
+        nh = min(2, share - (int)(block % per_group) * 2);
         p0 = 0;
     } else {
         const int per_head = (a.P + c.block_cols - 1) / c.block_cols;
@@ -289,13 +315,14 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
     const __bf16* vp = static_cast<const __bf16*>(a.v) + col0;
     __bf16* op = static_cast<__bf16*>(a.o) + col0;
 
-    // this wave's tiles: wave, wave + 4; their head within the block
+    // This wave's tiles: wave, wave + WAVES; their head within the block.  A tile that the block
+    // does not have runs on zeros and is not stored.
     int tile_head[NTW];
     bool have[NTW];
 #pragma unroll
     for (int x = 0; x < NTW; ++x) {
-        have[x] = wave + 4 * x < tiles;
-        tile_head[x] = have[x] ? (wave + 4 * x) / head_tiles : 0;
+        have[x] = wave + WAVES * x < tiles;
+        tile_head[x] = HEADS == 2 && have[x] ? (wave + WAVES * x) / head_tiles : 0;
     }
 
     f32x4 S[NTW][8]; // n-tile t: entries 32g + 4t .. 32g + 4t + 3 of column l16
@@ -307,22 +334,23 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
 #pragma unroll
         for (int t = 0; t < 8; ++t) S[x][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         if (have[x] && MODE != PART_STATE && !(MODE == WHOLE && fresh)) {
-            const f32x4* r = reinterpret_cast<const f32x4*>(rows + ((wave + 4 * x) * 16 + l16) * 128 + 32 * g);
+            const f32x4* r = reinterpret_cast<const f32x4*>(rows + ((wave + WAVES * x) * 16 + l16) * 128 + 32 * g);
 #pragma unroll
             for (int t = 0; t < 8; ++t) S[x][t] = r[t];
         }
     }
-    if constexpr (MODE != PART_STATE) { // the tiles above the diagonal stay zero
-        for (int i = tid; i < 2 * kChunk * kScorePitch / 2; i += 256) reinterpret_cast<uint32_t*>(s.p)[i] = 0;
-    }
 
     // Tiles come and go through buffer descriptors that end with the span: rows behind it read 0
-    // and are not written.  16 pieces of 16 bytes a row, 16 rows at once.
+    // and are not written.  16 pieces of 16 bytes a row.
+    constexpr int ROWS = 4 * WAVES, NR = kChunk / ROWS; // rows at once
     const uint32_t piece = tid & 15, prow = tid >> 4;
     const uint32_t q_row = (uint32_t)a.qs * 2, k_row = (uint32_t)a.ks * 2, v_row = (uint32_t)a.vs * 2, o_row = (uint32_t)a.os * 2;
     const uint32_t q_off = prow * q_row + piece * 16, k_off = prow * k_row + piece * 16;
     const uint32_t v_off = piece * 8 < (uint32_t)tiles * 16 ? prow * v_row + piece * 16 : 0x80000000u; // no such column: 0
-    u32x4 rq[4], rk[4], rv[4];
+    uint32_t o_off[NTW];
+#pragma unroll
+    for (int x = 0; x < NTW; ++x) o_off[x] = have[x] ? l16 * o_row + (wave + WAVES * x) * 32 + 8 * g : 0x80000000u;
+    u32x4 rq[NR], rk[NR], rv[NR];
     float rg = 0.0f;
     auto fetch = [&](int64_t t0) {
         const uint32_t last = (uint32_t)(end - t0 < kChunk ? end - t0 : kChunk) - 1;
@@ -330,10 +358,10 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
         const Rsrc bk = make_rsrc(kp + t0 * a.ks, last * k_row + 256);
         const Rsrc bv = make_rsrc(vp + t0 * a.vs, last * v_row + tiles * 32);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (MODE != PART_STATE) rq[i] = __builtin_amdgcn_raw_buffer_load_b128(bq, q_off + 16 * i * q_row, 0, 0);
-            rk[i] = __builtin_amdgcn_raw_buffer_load_b128(bk, k_off + 16 * i * k_row, 0, 0);
-            rv[i] = __builtin_amdgcn_raw_buffer_load_b128(bv, v_off + 16 * i * v_row, 0, 0);
+        for (int i = 0; i < NR; ++i) {
+            if constexpr (MODE != PART_STATE) rq[i] = __builtin_amdgcn_raw_buffer_load_b128(bq, q_off + ROWS * i * q_row, 0, 0);
+            rk[i] = __builtin_amdgcn_raw_buffer_load_b128(bk, k_off + ROWS * i * k_row, 0, 0);
+            rv[i] = __builtin_amdgcn_raw_buffer_load_b128(bv, v_off + ROWS * i * v_row, 0, 0);
         }
         rg = 0.0f;
         if (wave < nh && a.g && t0 + lane < end) rg = a.g[(t0 + lane) * a.gs + head0 + wave];
@@ -348,49 +376,45 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
         const HeadDecay* const sd = s.d[buf];
         __syncthreads(); // the previous chunk has been read
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = prow + 16 * i;
+        for (int i = 0; i < NR; ++i) {
+            const int r = prow + ROWS * i;
             if constexpr (MODE != PART_STATE) *reinterpret_cast<u32x4*>(&s.q[r][piece * 8]) = rq[i];
             *reinterpret_cast<u32x4*>(&s.k[r][piece * 8]) = rk[i];
             *reinterpret_cast<u32x4*>(&s.v[r][piece * 8]) = rv[i];
         }
         __syncthreads();
         const bool more = t0 + kChunk < end;
-        if (more) fetch(t0 + kChunk);
 
         f32x4 O[NTW][4]; // query tile i: columns of this tile 4g .. 4g+3, query l16
         if constexpr (MODE != PART_STATE) {
-            // scores of the queries 16*wave .. +15: rows keys, columns queries
-            f32x4 A[4];
+            // scores of 16 queries against NJ*16 keys: rows keys, columns queries.  Every wave runs
+            // the tiles above the diagonal too: the last one has none, and all wait for it.
+            constexpr int NJ = 16 / WAVES;
+            const int qi = (wave & 3) * 16 + l16, jt0 = wave / 4 * NJ;
+            f32x4 A[NJ];
             bf16x8 qf[4];
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) qf[ks] = *reinterpret_cast<const bf16x8*>(&s.q[wave * 16 + l16][ks * 32 + g * 8]);
+            for (int ks = 0; ks < 4; ++ks) qf[ks] = *reinterpret_cast<const bf16x8*>(&s.q[qi][ks * 32 + g * 8]);
 #pragma unroll
-            for (int jt = 0; jt < 4; ++jt) {
-                A[jt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-                if (jt <= wave) {
+            for (int jt = 0; jt < NJ; ++jt) A[jt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        A[jt] = mfma(*reinterpret_cast<const bf16x8*>(&s.k[jt * 16 + l16][ks * 32 + g * 8]), qf[ks], A[jt]);
-                }
-            }
-            const int qi = wave * 16 + l16;
+            for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (h >= nh) break;
+                for (int jt = 0; jt < NJ; ++jt)
+                    A[jt] = mfma(*reinterpret_cast<const bf16x8*>(&s.k[(jt0 + jt) * 16 + l16][ks * 32 + g * 8]), qf[ks], A[jt]);
+#pragma unroll
+            for (int h = 0; h < HEADS; ++h) {
                 const float ih = sd[h].hi[qi], il = sd[h].lo[qi];
 #pragma unroll
-                for (int jt = 0; jt < 4; ++jt) {
-                    if (jt > wave) break;
-                    const int j0 = jt * 16 + g * 4;
-                    const float4 jh = *reinterpret_cast<const float4*>(&sd[h].hi[j0]);
-                    const float4 jl = *reinterpret_cast<const float4*>(&sd[h].lo[j0]);
-                    const float jhs[4] = {jh.x, jh.y, jh.z, jh.w}, jls[4] = {jl.x, jl.y, jl.z, jl.w};
+                for (int jt = 0; jt < NJ; ++jt) {
+                    const int j0 = (jt0 + jt) * 16 + g * 4;
+                    const f32x4 jh = *reinterpret_cast<const f32x4*>(&sd[h].hi[j0]);
+                    const f32x4 jl = *reinterpret_cast<const f32x4*>(&sd[h].lo[j0]);
                     float w[4];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const float e = __builtin_amdgcn_exp2f((ih - jhs[r]) + (il - jls[r]));
-                        w[r] = j0 + r <= qi ? A[jt][r] * e : 0.0f;
+                        const float e = (ih - jh[r]) + (il - jl[r]);
+                        w[r] = A[jt][r] * __builtin_amdgcn_exp2f(j0 + r <= qi ? e : -1000.0f);
                     }
                     const bf16x2 w01 = to_bf16(w[0], w[1]), w23 = to_bf16(w[2], w[3]);
                     *reinterpret_cast<bf16x4*>(&s.p[h][qi][j0]) = __builtin_shufflevector(w01, w23, 0, 1, 2, 3);
@@ -401,8 +425,15 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
             for (int x = 0; x < NTW; ++x)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) O[x][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            bf16x8 qq[2][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) qq[0][i] = *reinterpret_cast<const bf16x8*>(&s.q[i * 16 + l16][g * 32]);
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
+                if (ks < 3)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        qq[(ks + 1) & 1][i] = *reinterpret_cast<const bf16x8*>(&s.q[i * 16 + l16][g * 32 + ks * 8 + 8]);
                 bf16x8 hi[NTW], lo[NTW];
 #pragma unroll
                 for (int x = 0; x < NTW; ++x)
@@ -418,31 +449,27 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
                         lo[x][e + 1] = l.y;
                     }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bf16x8 qq = *reinterpret_cast<const bf16x8*>(&s.q[i * 16 + l16][g * 32 + ks * 8]);
+                for (int x = 0; x < NTW; ++x)
 #pragma unroll
-                    for (int x = 0; x < NTW; ++x) {
-                        O[x][i] = mfma(hi[x], qq, O[x][i]);
-                        O[x][i] = mfma(lo[x], qq, O[x][i]);
-                    }
-                }
+                    for (int i = 0; i < 4; ++i) O[x][i] = mfma(hi[x], qq[ks & 1][i], O[x][i]);
+#pragma unroll
+                for (int x = 0; x < NTW; ++x)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) O[x][i] = mfma(lo[x], qq[ks & 1][i], O[x][i]);
             }
 #pragma unroll
             for (int x = 0; x < NTW; ++x)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float e = sd[tile_head[x]].in[i * 16 + l16];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) O[x][i][r] *= e;
-                }
+                for (int i = 0; i < 4; ++i) O[x][i] *= sd[tile_head[x]].in[i * 16 + l16];
             __syncthreads(); // the scores are written
         }
+        if (more) fetch(t0 + kChunk);
         bf16x8 vf[NTW][2]; // this wave's columns of v: column l16, tokens 32*kb + 8g .. +7
 #pragma unroll
         for (int x = 0; x < NTW; ++x)
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb) {
-                const int col = (wave + 4 * x) % 8 * 16 + 4 * (l16 & 3);
+                const int col = (wave + WAVES * x) * 16 + 4 * (l16 & 3);
                 const int row = kb * 32 + g * 8 + (l16 >> 2);
                 vf[x][kb] = join4(lds_read_tr(&s.v[row][col]), lds_read_tr(&s.v[row + 4][col]));
             }
@@ -451,15 +478,20 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
             const Rsrc bo = make_rsrc(op + t0 * a.os, last * o_row + tiles * 32);
 #pragma unroll
             for (int x = 0; x < NTW; ++x) {
-                if (!have[x]) break;
+                bf16x8 pf[6];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) pf[i] = *reinterpret_cast<const bf16x8*>(&s.p[tile_head[x]][i * 16 + l16][g * 8]);
+#pragma unroll
+                for (int i = 2; i < 4; ++i) pf[2 + i] = *reinterpret_cast<const bf16x8*>(&s.p[tile_head[x]][i * 16 + l16][32 + g * 8]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) O[x][i] = mfma(vf[x][0], pf[i], O[x][i]);
+#pragma unroll
+                for (int i = 2; i < 4; ++i) O[x][i] = mfma(vf[x][1], pf[2 + i], O[x][i]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-#pragma unroll
-                    for (int kb = 0; kb <= i / 2; ++kb)
-                        O[x][i] = mfma(vf[x][kb], *reinterpret_cast<const bf16x8*>(&s.p[tile_head[x]][i * 16 + l16][kb * 32 + g * 8]), O[x][i]);
                     const f32x4 w = a.oscale * O[x][i];
                     const u32x2 w4 = {__builtin_bit_cast(uint32_t, to_bf16(w.x, w.y)), __builtin_bit_cast(uint32_t, to_bf16(w.z, w.w))};
-                    __builtin_amdgcn_raw_buffer_store_b64(w4, bo, (i * 16 + l16) * o_row + (wave + 4 * x) * 32 + 8 * g, 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b64(w4, bo, o_off[x] + i * 16 * o_row, 0, 0);
                 }
             }
         }
@@ -473,13 +505,16 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) S[x][t][r] = __builtin_fmaf(S[x][t][r], change, S[x][t][r] * keep);
         }
+        const int krow = g * 8 + (l16 >> 2), kcol = (l16 & 3) * 32;
+        bf16x8 kf[2];
+        kf[0] = join4(lds_read_tr(&s.k[krow][kcol]), lds_read_tr(&s.k[krow + 4][kcol]));
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
             bf16x8 w[NTW][3];
 #pragma unroll
             for (int x = 0; x < NTW; ++x) {
                 const float* od = &sd[tile_head[x]].out[kb * 32 + g * 8];
-                const float4 o0 = *reinterpret_cast<const float4*>(od), o1 = *reinterpret_cast<const float4*>(od + 4);
+                const f32x4 o0 = *reinterpret_cast<const f32x4*>(od), o1 = *reinterpret_cast<const f32x4*>(od + 4);
                 const float oe[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
@@ -499,13 +534,15 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
             }
 #pragma unroll
             for (int t = 0; t < 8; ++t) {
-                const int col = (l16 & 3) * 32 + t * 4;
-                const int row = kb * 32 + g * 8 + (l16 >> 2);
-                const bf16x8 kf = join4(lds_read_tr(&s.k[row][col]), lds_read_tr(&s.k[row + 4][col]));
+                const int n = kb * 8 + t + 1; // the fragment after this one
+                if (n < 16) {
+                    const int row = n / 8 * 32 + krow, col = kcol + n % 8 * 4;
+                    kf[n & 1] = join4(lds_read_tr(&s.k[row][col]), lds_read_tr(&s.k[row + 4][col]));
+                }
 #pragma unroll
-                for (int x = 0; x < NTW; ++x)
+                for (int j = 0; j < 3; ++j)
 #pragma unroll
-                    for (int j = 0; j < 3; ++j) S[x][t] = mfma(kf, w[x][j], S[x][t]);
+                    for (int x = 0; x < NTW; ++x) S[x][t] = mfma(kf[t & 1], w[x][j], S[x][t]);
             }
         }
         if (more && wave < nh) total += chunk_decays(rg, lane, s.d[buf ^ 1][wave]);
@@ -514,16 +551,14 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
 #pragma unroll
         for (int x = 0; x < NTW; ++x)
             if (have[x]) {
-                f32x4* r = reinterpret_cast<f32x4*>(rows + ((wave + 4 * x) * 16 + l16) * 128 + 32 * g);
+                f32x4* r = reinterpret_cast<f32x4*>(rows + ((wave + WAVES * x) * 16 + l16) * 128 + 32 * g);
 #pragma unroll
                 for (int t = 0; t < 8; ++t) r[t] = S[x][t];
             }
     }
     if constexpr (MODE == PART_STATE) {
         if (wave < nh && lane == 0 && p0 == 0) {
-            const double e = exp2(total);
-            c.part_decay[(int64_t)item * a.H + head0 + wave] =
-                make_float2(e >= 0.5 ? 1.0f : 0.0f, (float)(e >= 0.5 ? e - 1.0 : e));
+            c.part_decay[(int64_t)item * a.H + head0 + wave] = decay_of(total);
         }
     }
 }
@@ -617,9 +652,15 @@ static hipError_t launch_chunk(ChunkArgs c, int64_t items, hipStream_t st)
     c.runs = (c.blocks + c.run - 1) / c.run;
     const int64_t blocks = (items * c.runs + 7) / 8 * 8 * c.run;
     if (blocks > kMaxBlocks) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)blocks), wg(256);
-    if (c.pair * c.block_cols <= 64) hipLaunchKernelGGL((k_linattn_chunk<MODE, 1>), grid, wg, 0, st, c);
-    else hipLaunchKernelGGL((k_linattn_chunk<MODE, 2>), grid, wg, 0, st, c);
+    const dim3 grid((unsigned)blocks);
+    const bool wide = c.pair * c.block_cols > 64;
+    if (c.pair == 2) {
+        if (wide) hipLaunchKernelGGL((k_linattn_chunk<MODE, SSQ_LA_W, 8 / SSQ_LA_W, 2>), grid, dim3(64 * SSQ_LA_W), 0, st, c);
+        else hipLaunchKernelGGL((k_linattn_chunk<MODE, 4, 1, 2>), grid, dim3(256), 0, st, c);
+    } else {
+        if (wide) hipLaunchKernelGGL((k_linattn_chunk<MODE, SSQ_LA_W, 8 / SSQ_LA_W, 1>), grid, dim3(64 * SSQ_LA_W), 0, st, c);
+        else hipLaunchKernelGGL((k_linattn_chunk<MODE, 4, 1, 1>), grid, dim3(256), 0, st, c);
+    }
     return hipGetLastError();
 }
 
