@@ -2,24 +2,34 @@
 //
 // A wave takes four rows of one (sequence, head) from the first token to the last: 16 lanes a
 // row, 8 entries a lane, the recurrence in fp32.
+#include <type_traits>
+
 #include "ssq_ops_device.h"
 
 namespace ssq {
 
-// sequence i of the call: its slot, or -1 if it is skipped, and its tokens
+// sequence i of the call: its slot, or -1 if it is skipped, and its tokens (below 2^31)
 struct SeqSpan {
-    int slot;
-    int64_t begin, end;
+    int slot, begin, end;
 };
 
 __device__ __forceinline__ SeqSpan seq_span(const LinArgs& a, int i)
 {
+    const int most = (int)a.tokens;
     SeqSpan s;
     s.slot = a.slots ? a.slots[i] : i;
     if (s.slot < 0 || s.slot >= a.batch) s.slot = -1;
-    const int64_t b = a.cu[i], e = a.cu[i + 1];
-    s.begin = b < 0 ? 0 : (b > a.tokens ? a.tokens : b);
-    s.end = e < s.begin ? s.begin : (e > a.tokens ? a.tokens : e);
+    s.begin = min(max(a.cu[i], 0), most);
+    s.end = min(max(a.cu[i + 1], s.begin), most);
+    return s;
+}
+// the same where i is the wave's: in scalar registers
+__device__ __forceinline__ SeqSpan seq_span_uniform(const LinArgs& a, int i)
+{
+    SeqSpan s = seq_span(a, i);
+    s.slot = __builtin_amdgcn_readfirstlane(s.slot);
+    s.begin = __builtin_amdgcn_readfirstlane(s.begin);
+    s.end = __builtin_amdgcn_readfirstlane(s.end);
     return s;
 }
 
@@ -164,12 +174,15 @@ __device__ __forceinline__ f32x2 from_bf16(bf16x2 v)
     return f32x2{__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u)};
 }
 
-// decays of one head over a chunk, in powers of two
+// Decays of one head over a chunk.  r_i is the sum of g, in powers of two, over the tokens of i's
+// tile of 16 up to i, c_i the sum over the chunk.
 struct alignas(16) HeadDecay {
-    float hi[kChunk], lo[kChunk]; // c_i as the sum of two floats
-    float in[kChunk];             // exp(c_i)
-    float out[kChunk];            // exp(c_last - c_i)
-    float keep, change;           // exp(c_last) x = keep*x + change*x, keep 0 or 1: exact near 1
+    float r[kChunk];       // r_i: scores of a tile on the diagonal decay by exp2(r_i - r_j) ...
+    float row[kChunk];     // ... and off it by scale * exp2(r_i) ...
+    float col[3][kChunk];  // ... times exp2(c - c_j) with c before the tiles 1, 2 and 3
+    float in[kChunk];      // scale * exp2(c_i)
+    float out[kChunk];     // exp2(c_last - c_i)
+    float keep, change;    // exp2(c_last) x = keep*x + change*x, keep 0 or 1: exact near 1
 };
 
 struct alignas(16) ChunkLds {
@@ -201,39 +214,75 @@ __device__ __forceinline__ float2 decay_of(double c)
     return c > -1.0 ? make_float2(1.0f, expm1f((float)(c * 0.6931471805599453))) : make_float2(0.0f, exp2_of(c));
 }
 
-// one wave, lane = token of the chunk: g the token's log decay (0 behind the span's end);
-// returns the sum of all
-__device__ __forceinline__ double chunk_decays(float g, int lane, HeadDecay& d)
+__device__ __forceinline__ double readlane_d(double x, int lane)
 {
-    // exp(-128) is 0 in fp32, and so is all that passes such a token
-    double c = (double)fmaxf(g, -128.0f) * kLog2e;
-    c = add_dpp<0x111, 0xF>(c); // sums along the rows of 16 lanes: from 1, 2, 4 and 8 lanes before
-    c = add_dpp<0x112, 0xF>(c);
-    c = add_dpp<0x114, 0xF>(c);
-    c = add_dpp<0x118, 0xF>(c);
-    c = add_dpp<0x142, 0xA>(c); // the last lane of the row before to rows 1 and 3
-    c = add_dpp<0x143, 0xC>(c); // lane 31 to rows 2 and 3
-    const uint64_t u = __builtin_bit_cast(uint64_t, c);
-    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, 63), hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
-    const double last = __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
-    d.hi[lane] = (float)c;
-    d.lo[lane] = (float)(c - (double)(float)c);
-    d.in[lane] = exp2_of(c);
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane), hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+// the log decay g in powers of two: 2^-184 is 0 in fp32, and so is all that passes such a token
+__device__ __forceinline__ double log2_decay(float g)
+{
+    return (double)fmaxf(g, -128.0f) * kLog2e;
+}
+// sums along the rows of 16 lanes, from those to the sums of all lanes up to this one
+__device__ __forceinline__ double row_sums(double x)
+{
+    x = add_dpp<0x111, 0xF>(x); // from 1, 2, 4 and 8 lanes before
+    x = add_dpp<0x112, 0xF>(x);
+    x = add_dpp<0x114, 0xF>(x);
+    return add_dpp<0x118, 0xF>(x);
+}
+__device__ __forceinline__ double wave_sums(double r)
+{
+    r = add_dpp<0x142, 0xA>(r); // the last lane of the row before to rows 1 and 3
+    return add_dpp<0x143, 0xC>(r); // lane 31 to rows 2 and 3
+}
+
+// one wave, lane = token of the chunk: g the token's log decay (0 behind the span's end)
+__device__ __forceinline__ void chunk_decays(float g, float scale, int lane, HeadDecay& d)
+{
+    const double r = row_sums(log2_decay(g)), c = wave_sums(r);
+    const double last = readlane_d(c, 63);
+    d.r[lane] = (float)r;
+    d.row[lane] = scale * __builtin_amdgcn_exp2f((float)r); // scores are rounded to bf16: a few units of fp32 do
+#pragma unroll
+    for (int i = 0; i < 3; ++i) // not positive for the tokens that use it
+        d.col[i][lane] = __builtin_amdgcn_exp2f(fminf((float)(readlane_d(c, 16 * i + 15) - c), 0.0f));
+    d.in[lane] = scale * exp2_of(c);
     d.out[lane] = exp2_of(last - c);
     if (lane == 63) {
         const float2 e = decay_of(c);
         d.keep = e.x;
         d.change = e.y;
     }
-    return last;
 }
 
-#ifndef SSQ_LA_W
-#define SSQ_LA_W 4
+// the same where only the writes count: exp2 of what follows the token in the chunk, and `after` it
+__device__ __forceinline__ void write_decays(float g, int lane, double& after, HeadDecay& d)
+{
+    const double c = wave_sums(row_sums(log2_decay(g)));
+    const double last = readlane_d(c, 63);
+    d.out[lane] = exp2_of(after + (last - c));
+    after += last;
+}
+
+#ifndef SSQ_LA_EARLY
+#define SSQ_LA_EARLY 1
 #endif
-#ifndef SSQ_LA_OCC
-#define SSQ_LA_OCC 2
+#ifndef SSQ_LA_TERMS
+#define SSQ_LA_TERMS 2
 #endif
+constexpr int kTerms = SSQ_LA_TERMS;
+// a descriptor of the wave's: without the readfirstlanes the compiler would loop over its lanes' values
+__device__ __forceinline__ Rsrc wave_rsrc(const void* base, uint32_t bytes)
+{
+    const uint64_t b = (uint64_t)base;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)b), hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32));
+    return make_rsrc((const void*)(((uint64_t)hi << 32) | lo), (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes));
+}
+
 enum { WHOLE = 0, PART_STATE = 1, PART_OUT = 2 };
 
 struct ChunkArgs {
@@ -254,9 +303,9 @@ __device__ __forceinline__ int64_t first_part(const ChunkArgs& c, int64_t begin,
     return begin / c.part_tokens + seq;
 }
 
-// WAVES waves of NTW tiles each; HEADS heads at most (2: the blocks of a pair)
-template <int MODE, int WAVES, int NTW, int HEADS>
-__global__ __launch_bounds__(64 * WAVES, SSQ_LA_OCC) void k_linattn_chunk(ChunkArgs c)
+// NTW tiles of 16 columns a wave, HEADS heads at most (2: the blocks of a pair)
+template <int MODE, int NTW, int HEADS>
+__global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
 {
     __shared__ ChunkLds s;
     const LinArgs& a = c.a;
@@ -274,15 +323,15 @@ __global__ __launch_bounds__(64 * WAVES, SSQ_LA_OCC) void k_linattn_chunk(ChunkA
         int lo = 0, hi = a.nseq - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            const SeqSpan m = seq_span(a, mid);
+            const SeqSpan m = seq_span_uniform(a, mid);
             if (first_part(c, m.begin, mid) <= item) lo = mid;
             else hi = mid - 1;
         }
         seq = lo;
     }
-    const SeqSpan span = seq_span(a, seq);
+    const SeqSpan span = seq_span_uniform(a, seq);
     if (span.slot < 0) return;
-    const bool fresh = a.fresh && a.fresh[seq];
+    const bool fresh = a.fresh && __builtin_amdgcn_readfirstlane((int)a.fresh[seq]);
     int64_t begin = span.begin, end = span.end;
     if constexpr (MODE == WHOLE) {
         if (begin == end && !fresh) return;
@@ -321,105 +370,140 @@ __global__ __launch_bounds__(64 * WAVES, SSQ_LA_OCC) void k_linattn_chunk(ChunkA
     bool have[NTW];
 #pragma unroll
     for (int x = 0; x < NTW; ++x) {
-        have[x] = wave + WAVES * x < tiles;
-        tile_head[x] = HEADS == 2 && have[x] ? (wave + WAVES * x) / head_tiles : 0;
+        have[x] = wave + 4 * x < tiles;
+        tile_head[x] = HEADS == 2 && have[x] ? (wave + 4 * x) / head_tiles : 0;
     }
 
     f32x4 S[NTW][8]; // n-tile t: entries 32g + 4t .. 32g + 4t + 3 of column l16
+    // A sequence's state is in rows, a part's as the registers hold it.
     float* rows = nullptr;
-    if constexpr (MODE == WHOLE) rows = seq_rows(a, seq, span.slot) + col0 * 128;
-    else rows = c.part_state + ((int64_t)item * a.H * a.P + col0) * 128;
+    if constexpr (MODE == WHOLE) rows = seq_rows(a, seq, span.slot) + col0 * 128 + l16 * 128 + 32 * g;
+    else rows = c.part_state + ((int64_t)item * a.H * a.P + col0) * 128 + lane * 4;
+    constexpr int kStep = MODE == WHOLE ? 4 : 256; // floats from one n-tile to the next
 #pragma unroll
     for (int x = 0; x < NTW; ++x) {
 #pragma unroll
         for (int t = 0; t < 8; ++t) S[x][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         if (have[x] && MODE != PART_STATE && !(MODE == WHOLE && fresh)) {
-            const f32x4* r = reinterpret_cast<const f32x4*>(rows + ((wave + WAVES * x) * 16 + l16) * 128 + 32 * g);
 #pragma unroll
-            for (int t = 0; t < 8; ++t) S[x][t] = r[t];
+            for (int t = 0; t < 8; ++t) S[x][t] = *reinterpret_cast<const f32x4*>(rows + (wave + 4 * x) * 2048 + t * kStep);
         }
+    }
+    if constexpr (MODE != PART_STATE) { // the scores above the diagonal's tiles stay zero
+        for (int i = tid; i < (int)sizeof(s.p) / 4; i += 256) reinterpret_cast<uint32_t*>(s.p)[i] = 0;
     }
 
     // Tiles come and go through buffer descriptors that end with the span: rows behind it read 0
     // and are not written.  16 pieces of 16 bytes a row.
-    constexpr int ROWS = 4 * WAVES, NR = kChunk / ROWS; // rows at once
     const uint32_t piece = tid & 15, prow = tid >> 4;
     const uint32_t q_row = (uint32_t)a.qs * 2, k_row = (uint32_t)a.ks * 2, v_row = (uint32_t)a.vs * 2, o_row = (uint32_t)a.os * 2;
     const uint32_t q_off = prow * q_row + piece * 16, k_off = prow * k_row + piece * 16;
     const uint32_t v_off = piece * 8 < (uint32_t)tiles * 16 ? prow * v_row + piece * 16 : 0x80000000u; // no such column: 0
     uint32_t o_off[NTW];
 #pragma unroll
-    for (int x = 0; x < NTW; ++x) o_off[x] = have[x] ? l16 * o_row + (wave + WAVES * x) * 32 + 8 * g : 0x80000000u;
-    u32x4 rq[NR], rk[NR], rv[NR];
-    float rg = 0.0f;
+    for (int x = 0; x < NTW; ++x) o_off[x] = have[x] ? l16 * o_row + (wave + 4 * x) * 32 + 8 * g : 0x80000000u;
+    u32x4 rq[4], rk[4], rv[4];
     auto fetch = [&](int64_t t0) {
         const uint32_t last = (uint32_t)(end - t0 < kChunk ? end - t0 : kChunk) - 1;
-        const Rsrc bq = make_rsrc(qp + t0 * a.qs, last * q_row + 256);
-        const Rsrc bk = make_rsrc(kp + t0 * a.ks, last * k_row + 256);
-        const Rsrc bv = make_rsrc(vp + t0 * a.vs, last * v_row + tiles * 32);
+        const Rsrc bq = wave_rsrc(qp + t0 * a.qs, last * q_row + 256);
+        const Rsrc bk = wave_rsrc(kp + t0 * a.ks, last * k_row + 256);
+        const Rsrc bv = wave_rsrc(vp + t0 * a.vs, last * v_row + tiles * 32);
 #pragma unroll
-        for (int i = 0; i < NR; ++i) {
-            if constexpr (MODE != PART_STATE) rq[i] = __builtin_amdgcn_raw_buffer_load_b128(bq, q_off + ROWS * i * q_row, 0, 0);
-            rk[i] = __builtin_amdgcn_raw_buffer_load_b128(bk, k_off + ROWS * i * k_row, 0, 0);
-            rv[i] = __builtin_amdgcn_raw_buffer_load_b128(bv, v_off + ROWS * i * v_row, 0, 0);
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (MODE != PART_STATE) rq[i] = __builtin_amdgcn_raw_buffer_load_b128(bq, q_off + 16 * i * q_row, 0, 0);
+            rk[i] = __builtin_amdgcn_raw_buffer_load_b128(bk, k_off + 16 * i * k_row, 0, 0);
+            rv[i] = __builtin_amdgcn_raw_buffer_load_b128(bv, v_off + 16 * i * v_row, 0, 0);
         }
-        rg = 0.0f;
-        if (wave < nh && a.g && t0 + lane < end) rg = a.g[(t0 + lane) * a.gs + head0 + wave];
     };
-    double total = 0.0; // PART_STATE: the head's decay over the part, in waves 0 .. nh-1
-    if (begin < end) { // an empty sequence has no row that a descriptor could end with
-        fetch(begin);
-        if (wave < nh) total += chunk_decays(rg, lane, s.d[0][wave]);
+    // One wave makes the decays, of both heads at once.  It has the fewest scores, and makes a
+    // chunk's while the chunk before it is run.
+    float rg[HEADS];
+    auto fetch_decays = [&](int64_t t0) {
+#pragma unroll
+        for (int h = 0; h < HEADS; ++h) {
+            rg[h] = 0.0f;
+            if (h < nh && a.g && t0 + lane < end) rg[h] = a.g[(t0 + lane) * a.gs + head0 + h];
+        }
+    };
+    double after[HEADS]; // PART_STATE: the decays of the chunks behind
+#pragma unroll
+    for (int h = 0; h < HEADS; ++h) after[h] = 0.0;
+    auto make_decays = [&](int buf) {
+#pragma unroll
+        for (int h = 0; h < HEADS; ++h) {
+            if constexpr (MODE == PART_STATE) write_decays(rg[h], lane, after[h], s.d[buf][h]);
+            else chunk_decays(rg[h], a.oscale, lane, s.d[buf][h]);
+        }
+    };
+    // PART_STATE runs from the last chunk to the first, so that what is summed need not decay
+    const int64_t chunks = (end - begin + kChunk - 1) / kChunk;
+    auto start = [&](int64_t n) { return begin + (MODE == PART_STATE ? chunks - 1 - n : n) * kChunk; };
+    if (chunks > 0) { // an empty sequence has no row that a descriptor could end with
+        fetch(start(0));
+        if (wave == 3) {
+            fetch_decays(start(0));
+            make_decays(0);
+            if (chunks > 1) fetch_decays(start(1));
+        }
     }
     int buf = 0;
-    for (int64_t t0 = begin; t0 < end; t0 += kChunk, buf ^= 1) {
+    for (int64_t n = 0; n < chunks; ++n, buf ^= 1) {
+        const int64_t t0 = start(n);
         const HeadDecay* const sd = s.d[buf];
         __syncthreads(); // the previous chunk has been read
 #pragma unroll
-        for (int i = 0; i < NR; ++i) {
-            const int r = prow + ROWS * i;
+        for (int i = 0; i < 4; ++i) {
+            const int r = prow + 16 * i;
             if constexpr (MODE != PART_STATE) *reinterpret_cast<u32x4*>(&s.q[r][piece * 8]) = rq[i];
             *reinterpret_cast<u32x4*>(&s.k[r][piece * 8]) = rk[i];
             *reinterpret_cast<u32x4*>(&s.v[r][piece * 8]) = rv[i];
         }
         __syncthreads();
-        const bool more = t0 + kChunk < end;
+        const bool more = n + 1 < chunks;
+        if (SSQ_LA_EARLY && more) fetch(start(n + 1));
+        if (wave == 3 && more) {
+            make_decays(buf ^ 1);
+            if (n + 2 < chunks) fetch_decays(start(n + 2));
+        }
 
         f32x4 O[NTW][4]; // query tile i: columns of this tile 4g .. 4g+3, query l16
         if constexpr (MODE != PART_STATE) {
-            // scores of 16 queries against NJ*16 keys: rows keys, columns queries.  Every wave runs
-            // the tiles above the diagonal too: the last one has none, and all wait for it.
-            constexpr int NJ = 16 / WAVES;
-            const int qi = (wave & 3) * 16 + l16, jt0 = wave / 4 * NJ;
-            f32x4 A[NJ];
-            bf16x8 qf[4];
+            // Scores in tiles of 16 queries x 16 keys: ten at and below the diagonal.  Each wave has
+            // one on it, and the first three have two others.
+            const int qd = wave == 3 ? 2 : wave == 2 ? 3 : wave;
+            const int qt[3] = {qd, wave == 0 ? 3 : wave, wave == 2 ? 2 : 3}, kt[3] = {qd, 0, wave == 1 ? 2 : 1};
+            auto scores = [&](auto slots) { // rows keys, columns queries
+                constexpr int N = decltype(slots)::value;
+                f32x4 A[N];
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) qf[ks] = *reinterpret_cast<const bf16x8*>(&s.q[qi][ks * 32 + g * 8]);
+                for (int i = 0; i < N; ++i) A[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int jt = 0; jt < NJ; ++jt) A[jt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
+                    for (int i = 0; i < N; ++i)
+                        A[i] = mfma(*reinterpret_cast<const bf16x8*>(&s.k[kt[i] * 16 + l16][ks * 32 + g * 8]),
+                                    *reinterpret_cast<const bf16x8*>(&s.q[qt[i] * 16 + l16][ks * 32 + g * 8]), A[i]);
 #pragma unroll
-                for (int jt = 0; jt < NJ; ++jt)
-                    A[jt] = mfma(*reinterpret_cast<const bf16x8*>(&s.k[(jt0 + jt) * 16 + l16][ks * 32 + g * 8]), qf[ks], A[jt]);
+                for (int h = 0; h < HEADS; ++h)
 #pragma unroll
-            for (int h = 0; h < HEADS; ++h) {
-                const float ih = sd[h].hi[qi], il = sd[h].lo[qi];
+                    for (int i = 0; i < N; ++i) {
+                        const int qi = qt[i] * 16 + l16, kj = kt[i] * 16 + g * 4;
+                        f32x4 w;
+                        if (i == 0) {
+                            const f32x4 rj = *reinterpret_cast<const f32x4*>(&sd[h].r[kj]);
+                            const float ri = sd[h].r[qi];
 #pragma unroll
-                for (int jt = 0; jt < NJ; ++jt) {
-                    const int j0 = (jt0 + jt) * 16 + g * 4;
-                    const f32x4 jh = *reinterpret_cast<const f32x4*>(&sd[h].hi[j0]);
-                    const f32x4 jl = *reinterpret_cast<const f32x4*>(&sd[h].lo[j0]);
-                    float w[4];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float e = (ih - jh[r]) + (il - jl[r]);
-                        w[r] = A[jt][r] * __builtin_amdgcn_exp2f(j0 + r <= qi ? e : -1000.0f);
+                            for (int r = 0; r < 4; ++r)
+                                w[r] = A[i][r] * (a.oscale * __builtin_amdgcn_exp2f(kj + r <= qi ? ri - rj[r] : -1000.0f));
+                        } else {
+                            w = A[i] * sd[h].row[qi] * *reinterpret_cast<const f32x4*>(&sd[h].col[qt[i] - 1][kj]);
+                        }
+                        const bf16x2 w01 = to_bf16(w.x, w.y), w23 = to_bf16(w.z, w.w);
+                        *reinterpret_cast<bf16x4*>(&s.p[h][qi][kj]) = __builtin_shufflevector(w01, w23, 0, 1, 2, 3);
                     }
-                    const bf16x2 w01 = to_bf16(w[0], w[1]), w23 = to_bf16(w[2], w[3]);
-                    *reinterpret_cast<bf16x4*>(&s.p[h][qi][j0]) = __builtin_shufflevector(w01, w23, 0, 1, 2, 3);
-                }
-            }
+            };
+            if (wave < 3) scores(std::integral_constant<int, 3>{});
+            else scores(std::integral_constant<int, 1>{});
             // S q, the state as the sum of two bf16
 #pragma unroll
             for (int x = 0; x < NTW; ++x)
@@ -463,19 +547,19 @@ __global__ __launch_bounds__(64 * WAVES, SSQ_LA_OCC) void k_linattn_chunk(ChunkA
                 for (int i = 0; i < 4; ++i) O[x][i] *= sd[tile_head[x]].in[i * 16 + l16];
             __syncthreads(); // the scores are written
         }
-        if (more) fetch(t0 + kChunk);
+        if (!SSQ_LA_EARLY && more) fetch(start(n + 1));
         bf16x8 vf[NTW][2]; // this wave's columns of v: column l16, tokens 32*kb + 8g .. +7
 #pragma unroll
         for (int x = 0; x < NTW; ++x)
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb) {
-                const int col = (wave + WAVES * x) * 16 + 4 * (l16 & 3);
+                const int col = (wave + 4 * x) * 16 + 4 * (l16 & 3);
                 const int row = kb * 32 + g * 8 + (l16 >> 2);
                 vf[x][kb] = join4(lds_read_tr(&s.v[row][col]), lds_read_tr(&s.v[row + 4][col]));
             }
         if constexpr (MODE != PART_STATE) {
             const uint32_t last = (uint32_t)(end - t0 < kChunk ? end - t0 : kChunk) - 1;
-            const Rsrc bo = make_rsrc(op + t0 * a.os, last * o_row + tiles * 32);
+            const Rsrc bo = wave_rsrc(op + t0 * a.os, last * o_row + tiles * 32);
 #pragma unroll
             for (int x = 0; x < NTW; ++x) {
                 bf16x8 pf[6];
@@ -489,28 +573,32 @@ __global__ __launch_bounds__(64 * WAVES, SSQ_LA_OCC) void k_linattn_chunk(ChunkA
                 for (int i = 2; i < 4; ++i) O[x][i] = mfma(vf[x][1], pf[2 + i], O[x][i]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const f32x4 w = a.oscale * O[x][i];
+                    const f32x4 w = O[x][i];
                     const u32x2 w4 = {__builtin_bit_cast(uint32_t, to_bf16(w.x, w.y)), __builtin_bit_cast(uint32_t, to_bf16(w.z, w.w))};
                     __builtin_amdgcn_raw_buffer_store_b64(w4, bo, o_off[x] + i * 16 * o_row, 0, 0);
                 }
             }
         }
-        // the state: decayed, and the chunk's writes with v's decay, as the sum of three bf16
+        // the state: decayed, and the chunk's writes with v's decay, as the sum of kTerms bf16
         if (MODE == PART_OUT && !more) break; // the next part has its own
+        if constexpr (MODE != PART_STATE) {
 #pragma unroll
-        for (int x = 0; x < NTW; ++x) {
-            const float keep = sd[tile_head[x]].keep, change = sd[tile_head[x]].change;
+            for (int x = 0; x < NTW; ++x) {
+                const float keep = sd[tile_head[x]].keep, change = sd[tile_head[x]].change;
 #pragma unroll
-            for (int t = 0; t < 8; ++t)
+                for (int t = 0; t < 8; ++t)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) S[x][t][r] = __builtin_fmaf(S[x][t][r], change, S[x][t][r] * keep);
+                    for (int r = 0; r < 4; ++r) S[x][t][r] = __builtin_fmaf(S[x][t][r], change, S[x][t][r] * keep);
+            }
         }
         const int krow = g * 8 + (l16 >> 2), kcol = (l16 & 3) * 32;
-        bf16x8 kf[2];
-        kf[0] = join4(lds_read_tr(&s.k[krow][kcol]), lds_read_tr(&s.k[krow + 4][kcol]));
+        auto k_frag = [&](int kb, int t) {
+            const int row = kb * 32 + krow, col = kcol + t * 4;
+            return join4(lds_read_tr(&s.k[row][col]), lds_read_tr(&s.k[row + 4][col]));
+        };
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
-            bf16x8 w[NTW][3];
+            bf16x8 w[NTW][kTerms];
 #pragma unroll
             for (int x = 0; x < NTW; ++x) {
                 const float* od = &sd[tile_head[x]].out[kb * 32 + g * 8];
@@ -522,7 +610,7 @@ __global__ __launch_bounds__(64 * WAVES, SSQ_LA_OCC) void k_linattn_chunk(ChunkA
                     v.x *= oe[e];
                     v.y *= oe[e + 1];
 #pragma unroll
-                    for (int j = 0; j < 3; ++j) {
+                    for (int j = 0; j < kTerms; ++j) {
                         const bf16x2 h = to_bf16(v.x, v.y);
                         const f32x2 f = from_bf16(h);
                         w[x][j][e] = h.x;
@@ -533,32 +621,30 @@ __global__ __launch_bounds__(64 * WAVES, SSQ_LA_OCC) void k_linattn_chunk(ChunkA
                 }
             }
 #pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                const int n = kb * 8 + t + 1; // the fragment after this one
-                if (n < 16) {
-                    const int row = n / 8 * 32 + krow, col = kcol + n % 8 * 4;
-                    kf[n & 1] = join4(lds_read_tr(&s.k[row][col]), lds_read_tr(&s.k[row + 4][col]));
-                }
+            for (int t = 0; t < 8; t += 2) {
+                const bf16x8 kf[2] = {k_frag(kb, t), k_frag(kb, t + 1)};
 #pragma unroll
-                for (int j = 0; j < 3; ++j)
+                for (int j = 0; j < kTerms; ++j)
 #pragma unroll
-                    for (int x = 0; x < NTW; ++x) S[x][t] = mfma(kf[t & 1], w[x][j], S[x][t]);
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int x = 0; x < NTW; ++x) S[x][t + u] = mfma(kf[u], w[x][j], S[x][t + u]);
             }
         }
-        if (more && wave < nh) total += chunk_decays(rg, lane, s.d[buf ^ 1][wave]);
     }
     if constexpr (MODE != PART_OUT) {
 #pragma unroll
         for (int x = 0; x < NTW; ++x)
             if (have[x]) {
-                f32x4* r = reinterpret_cast<f32x4*>(rows + ((wave + WAVES * x) * 16 + l16) * 128 + 32 * g);
 #pragma unroll
-                for (int t = 0; t < 8; ++t) r[t] = S[x][t];
+                for (int t = 0; t < 8; ++t) *reinterpret_cast<f32x4*>(rows + (wave + 4 * x) * 2048 + t * kStep) = S[x][t];
             }
     }
     if constexpr (MODE == PART_STATE) {
-        if (wave < nh && lane == 0 && p0 == 0) {
-            c.part_decay[(int64_t)item * a.H + head0 + wave] = decay_of(total);
+        if (wave == 3 && lane == 0 && p0 == 0) {
+#pragma unroll
+            for (int h = 0; h < HEADS; ++h)
+                if (h < nh) c.part_decay[(int64_t)item * a.H + head0 + h] = decay_of(after[h]);
         }
     }
 }
@@ -577,18 +663,33 @@ __global__ __launch_bounds__(256) void k_linattn_join(ChunkArgs c, int64_t units
     const SeqSpan span = seq_span(a, seq);
     const bool fresh = a.fresh && a.fresh[seq];
     if (span.slot < 0 || (span.begin == span.end && !fresh)) return;
-    f32x4* state = reinterpret_cast<f32x4*>(seq_rows(a, seq, span.slot)) + e;
+    // the parts' order within a tile of 16 columns: n-tile, then lane
+    const int lane = e & 63, t = e >> 6 & 7;
+    const int64_t row = (e >> 9) * 16 + (lane & 15);
+    f32x4* state = reinterpret_cast<f32x4*>(seq_rows(a, seq, span.slot) + row * 128 + 32 * (lane >> 4) + 4 * t);
     f32x4 S = {0.0f, 0.0f, 0.0f, 0.0f};
     if (!fresh) S = *state;
     const int64_t n = (span.end - span.begin + c.part_tokens - 1) / c.part_tokens;
     const int64_t p0 = first_part(c, span.begin, seq);
-    for (int64_t p = p0; p < p0 + n; ++p) {
-        f32x4* part = reinterpret_cast<f32x4*>(c.part_state) + p * per_seq + e;
-        const f32x4 own = *part;
-        const float2 d = c.part_decay[p * a.H + head];
-        *part = S;
+    f32x4* part = reinterpret_cast<f32x4*>(c.part_state) + p0 * per_seq + e;
+    const float2* decay = c.part_decay + p0 * a.H + head;
+    constexpr int AHEAD = 8; // parts in flight
+    for (int64_t p = 0; p < n; p += AHEAD) {
+        f32x4 own[AHEAD];
+        float2 d[AHEAD];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) S[r] = __builtin_fmaf(S[r], d.y, S[r] * d.x) + own[r];
+        for (int k = 0; k < AHEAD; ++k)
+            if (p + k < n) {
+                own[k] = part[(p + k) * per_seq];
+                d[k] = decay[(p + k) * a.H];
+            }
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            if (p + k < n) {
+                part[(p + k) * per_seq] = S;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) S[r] = __builtin_fmaf(S[r], d[k].y, S[r] * d[k].x) + own[k][r];
+            }
     }
     *state = S;
 }
@@ -653,13 +754,14 @@ static hipError_t launch_chunk(ChunkArgs c, int64_t items, hipStream_t st)
     const int64_t blocks = (items * c.runs + 7) / 8 * 8 * c.run;
     if (blocks > kMaxBlocks) return hipErrorInvalidValue;
     const dim3 grid((unsigned)blocks);
+    const dim3 wg(256);
     const bool wide = c.pair * c.block_cols > 64;
     if (c.pair == 2) {
-        if (wide) hipLaunchKernelGGL((k_linattn_chunk<MODE, SSQ_LA_W, 8 / SSQ_LA_W, 2>), grid, dim3(64 * SSQ_LA_W), 0, st, c);
-        else hipLaunchKernelGGL((k_linattn_chunk<MODE, 4, 1, 2>), grid, dim3(256), 0, st, c);
+        if (wide) hipLaunchKernelGGL((k_linattn_chunk<MODE, 2, 2>), grid, wg, 0, st, c);
+        else hipLaunchKernelGGL((k_linattn_chunk<MODE, 1, 2>), grid, wg, 0, st, c);
     } else {
-        if (wide) hipLaunchKernelGGL((k_linattn_chunk<MODE, SSQ_LA_W, 8 / SSQ_LA_W, 1>), grid, dim3(64 * SSQ_LA_W), 0, st, c);
-        else hipLaunchKernelGGL((k_linattn_chunk<MODE, 4, 1, 1>), grid, dim3(256), 0, st, c);
+        if (wide) hipLaunchKernelGGL((k_linattn_chunk<MODE, 2, 1>), grid, wg, 0, st, c);
+        else hipLaunchKernelGGL((k_linattn_chunk<MODE, 1, 1>), grid, wg, 0, st, c);
     }
     return hipGetLastError();
 }
