@@ -275,6 +275,10 @@ __device__ __forceinline__ void write_decays(float g, int lane, double& after, H
 #define SSQ_LA_TERMS 2
 #endif
 constexpr int kTerms = SSQ_LA_TERMS;
+#ifndef SSQ_LA_STERMS
+#define SSQ_LA_STERMS 2
+#endif
+constexpr int kStateTerms = SSQ_LA_STERMS;
 // a descriptor of the wave's: without the readfirstlanes the compiler would loop over its lanes' values
 __device__ __forceinline__ Rsrc wave_rsrc(const void* base, uint32_t bytes)
 {
@@ -364,15 +368,16 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
     const __bf16* vp = static_cast<const __bf16*>(a.v) + col0;
     __bf16* op = static_cast<__bf16*>(a.o) + col0;
 
-    // This wave's tiles: wave, wave + WAVES; their head within the block.  A tile that the block
-    // does not have runs on zeros and is not stored.
-    int tile_head[NTW];
+    // This wave's tiles: NTW next to each other in one head, `head` of the block, the first at
+    // `col` of the block's columns.  A tile that the head does not have runs on another's values
+    // and is not stored.
+    const int waves_per_head = (head_tiles + NTW - 1) / NTW;
+    const int head = HEADS == 2 && wave >= waves_per_head ? 1 : 0;
+    const int tile0 = (wave - head * waves_per_head) * NTW;
+    const int col = min(head * head_tiles + tile0, 8 - NTW) * 16;
     bool have[NTW];
 #pragma unroll
-    for (int x = 0; x < NTW; ++x) {
-        have[x] = wave + 4 * x < tiles;
-        tile_head[x] = HEADS == 2 && have[x] ? (wave + 4 * x) / head_tiles : 0;
-    }
+    for (int x = 0; x < NTW; ++x) have[x] = head < nh && tile0 + x < head_tiles;
 
     f32x4 S[NTW][8]; // n-tile t: entries 32g + 4t .. 32g + 4t + 3 of column l16
     // A sequence's state is in rows, a part's as the registers hold it.
@@ -386,7 +391,7 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
         for (int t = 0; t < 8; ++t) S[x][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         if (have[x] && MODE != PART_STATE && !(MODE == WHOLE && fresh)) {
 #pragma unroll
-            for (int t = 0; t < 8; ++t) S[x][t] = *reinterpret_cast<const f32x4*>(rows + (wave + 4 * x) * 2048 + t * kStep);
+            for (int t = 0; t < 8; ++t) S[x][t] = *reinterpret_cast<const f32x4*>(rows + (col / 16 + x) * 2048 + t * kStep);
         }
     }
     if constexpr (MODE != PART_STATE) { // the scores above the diagonal's tiles stay zero
@@ -401,7 +406,7 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
     const uint32_t v_off = piece * 8 < (uint32_t)tiles * 16 ? prow * v_row + piece * 16 : 0x80000000u; // no such column: 0
     uint32_t o_off[NTW];
 #pragma unroll
-    for (int x = 0; x < NTW; ++x) o_off[x] = have[x] ? l16 * o_row + (wave + 4 * x) * 32 + 8 * g : 0x80000000u;
+    for (int x = 0; x < NTW; ++x) o_off[x] = have[x] ? l16 * o_row + (col + x * 16) * 2 + 8 * g : 0x80000000u;
     u32x4 rq[4], rk[4], rv[4];
     auto fetch = [&](int64_t t0) {
         const uint32_t last = (uint32_t)(end - t0 < kChunk ? end - t0 : kChunk) - 1;
@@ -468,56 +473,25 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
 
         f32x4 O[NTW][4]; // query tile i: columns of this tile 4g .. 4g+3, query l16
         if constexpr (MODE != PART_STATE) {
-            // Scores in tiles of 16 queries x 16 keys: ten at and below the diagonal.  Each wave has
-            // one on it, and the first three have two others.
-            const int qd = wave == 3 ? 2 : wave == 2 ? 3 : wave;
-            const int qt[3] = {qd, wave == 0 ? 3 : wave, wave == 2 ? 2 : 3}, kt[3] = {qd, 0, wave == 1 ? 2 : 1};
-            auto scores = [&](auto slots) { // rows keys, columns queries
-                constexpr int N = decltype(slots)::value;
-                f32x4 A[N];
+            // S q, the state as the sum of two bf16, and the scores of this wave's 16 keys, which use
+            // the same fragments of q (rows keys, columns queries; those above the diagonal for nothing)
+            f32x4 A[4];
 #pragma unroll
-                for (int i = 0; i < N; ++i) A[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int i = 0; i < 4; ++i) {
+                A[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
+                for (int x = 0; x < NTW; ++x) O[x][i] = A[i];
+            }
+            bf16x8 qq[2][4], kk[2];
+            auto read_q = [&](int ks) {
+                kk[ks & 1] = *reinterpret_cast<const bf16x8*>(&s.k[wave * 16 + l16][g * 32 + ks * 8]);
 #pragma unroll
-                    for (int i = 0; i < N; ++i)
-                        A[i] = mfma(*reinterpret_cast<const bf16x8*>(&s.k[kt[i] * 16 + l16][ks * 32 + g * 8]),
-                                    *reinterpret_cast<const bf16x8*>(&s.q[qt[i] * 16 + l16][ks * 32 + g * 8]), A[i]);
-#pragma unroll
-                for (int h = 0; h < HEADS; ++h)
-#pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        const int qi = qt[i] * 16 + l16, kj = kt[i] * 16 + g * 4;
-                        f32x4 w;
-                        if (i == 0) {
-                            const f32x4 rj = *reinterpret_cast<const f32x4*>(&sd[h].r[kj]);
-                            const float ri = sd[h].r[qi];
-#pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                w[r] = A[i][r] * (a.oscale * __builtin_amdgcn_exp2f(kj + r <= qi ? ri - rj[r] : -1000.0f));
-                        } else {
-                            w = A[i] * sd[h].row[qi] * *reinterpret_cast<const f32x4*>(&sd[h].col[qt[i] - 1][kj]);
-                        }
-                        const bf16x2 w01 = to_bf16(w.x, w.y), w23 = to_bf16(w.z, w.w);
-                        *reinterpret_cast<bf16x4*>(&s.p[h][qi][kj]) = __builtin_shufflevector(w01, w23, 0, 1, 2, 3);
-                    }
+                for (int i = 0; i < 4; ++i) qq[ks & 1][i] = *reinterpret_cast<const bf16x8*>(&s.q[i * 16 + l16][g * 32 + ks * 8]);
             };
-            if (wave < 3) scores(std::integral_constant<int, 3>{});
-            else scores(std::integral_constant<int, 1>{});
-            // S q, the state as the sum of two bf16
-#pragma unroll
-            for (int x = 0; x < NTW; ++x)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) O[x][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            bf16x8 qq[2][4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) qq[0][i] = *reinterpret_cast<const bf16x8*>(&s.q[i * 16 + l16][g * 32]);
+            read_q(0);
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
-                if (ks < 3)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        qq[(ks + 1) & 1][i] = *reinterpret_cast<const bf16x8*>(&s.q[i * 16 + l16][g * 32 + ks * 8 + 8]);
+                if (ks < 3) read_q(ks + 1);
                 bf16x8 hi[NTW], lo[NTW];
 #pragma unroll
                 for (int x = 0; x < NTW; ++x)
@@ -533,18 +507,43 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
                         lo[x][e + 1] = l.y;
                     }
 #pragma unroll
+                for (int i = 0; i < 4; ++i) A[i] = mfma(kk[ks & 1], qq[ks & 1][i], A[i]);
+#pragma unroll
                 for (int x = 0; x < NTW; ++x)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) O[x][i] = mfma(hi[x], qq[ks & 1][i], O[x][i]);
+                if constexpr (kStateTerms == 2)
 #pragma unroll
-                for (int x = 0; x < NTW; ++x)
+                    for (int x = 0; x < NTW; ++x)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) O[x][i] = mfma(lo[x], qq[ks & 1][i], O[x][i]);
+                        for (int i = 0; i < 4; ++i) O[x][i] = mfma(lo[x], qq[ks & 1][i], O[x][i]);
             }
+            const int kj = wave * 16 + g * 4;
 #pragma unroll
-            for (int x = 0; x < NTW; ++x)
+            for (int h = 0; h < HEADS; ++h)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) O[x][i] *= sd[tile_head[x]].in[i * 16 + l16];
+                for (int i = 0; i < 4; ++i) {
+                    const int qi = i * 16 + l16;
+                    f32x4 w;
+                    if (i < wave) continue;
+                    if (i == wave) {
+                        const f32x4 rj = *reinterpret_cast<const f32x4*>(&sd[h].r[kj]);
+                        const float ri = sd[h].r[qi];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            w[r] = A[i][r] * (a.oscale * __builtin_amdgcn_exp2f(kj + r <= qi ? ri - rj[r] : -1000.0f));
+                    } else {
+                        w = A[i] * sd[h].row[qi] * *reinterpret_cast<const f32x4*>(&sd[h].col[i == 0 ? 0 : i - 1][kj]);
+                    }
+                    const bf16x2 w01 = to_bf16(w.x, w.y), w23 = to_bf16(w.z, w.w);
+                    *reinterpret_cast<bf16x4*>(&s.p[h][qi][kj]) = __builtin_shufflevector(w01, w23, 0, 1, 2, 3);
+                }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float in = sd[head].in[i * 16 + l16];
+#pragma unroll
+                for (int x = 0; x < NTW; ++x) O[x][i] *= in;
+            }
             __syncthreads(); // the scores are written
         }
         if (!SSQ_LA_EARLY && more) fetch(start(n + 1));
@@ -553,57 +552,66 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
         for (int x = 0; x < NTW; ++x)
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb) {
-                const int col = (wave + 4 * x) * 16 + 4 * (l16 & 3);
+                const int vcol = col + x * 16 + 4 * (l16 & 3);
                 const int row = kb * 32 + g * 8 + (l16 >> 2);
-                vf[x][kb] = join4(lds_read_tr(&s.v[row][col]), lds_read_tr(&s.v[row + 4][col]));
+                vf[x][kb] = join4(lds_read_tr(&s.v[row][vcol]), lds_read_tr(&s.v[row + 4][vcol]));
             }
         if constexpr (MODE != PART_STATE) {
             const uint32_t last = (uint32_t)(end - t0 < kChunk ? end - t0 : kChunk) - 1;
             const Rsrc bo = wave_rsrc(op + t0 * a.os, last * o_row + tiles * 32);
+            bf16x8 pf[6];
 #pragma unroll
-            for (int x = 0; x < NTW; ++x) {
-                bf16x8 pf[6];
+            for (int i = 0; i < 4; ++i) pf[i] = *reinterpret_cast<const bf16x8*>(&s.p[head][i * 16 + l16][g * 8]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) pf[i] = *reinterpret_cast<const bf16x8*>(&s.p[tile_head[x]][i * 16 + l16][g * 8]);
+            for (int i = 2; i < 4; ++i) pf[2 + i] = *reinterpret_cast<const bf16x8*>(&s.p[head][i * 16 + l16][32 + g * 8]);
 #pragma unroll
-                for (int i = 2; i < 4; ++i) pf[2 + i] = *reinterpret_cast<const bf16x8*>(&s.p[tile_head[x]][i * 16 + l16][32 + g * 8]);
+            for (int x = 0; x < NTW; ++x)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) O[x][i] = mfma(vf[x][0], pf[i], O[x][i]);
 #pragma unroll
+            for (int x = 0; x < NTW; ++x)
+#pragma unroll
                 for (int i = 2; i < 4; ++i) O[x][i] = mfma(vf[x][1], pf[2 + i], O[x][i]);
+#pragma unroll
+            for (int x = 0; x < NTW; ++x)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const f32x4 w = O[x][i];
                     const u32x2 w4 = {__builtin_bit_cast(uint32_t, to_bf16(w.x, w.y)), __builtin_bit_cast(uint32_t, to_bf16(w.z, w.w))};
                     __builtin_amdgcn_raw_buffer_store_b64(w4, bo, o_off[x] + i * 16 * o_row, 0, 0);
                 }
-            }
         }
         // the state: decayed, and the chunk's writes with v's decay, as the sum of kTerms bf16
         if (MODE == PART_OUT && !more) break; // the next part has its own
         if constexpr (MODE != PART_STATE) {
+            const float change = sd[head].change;
+            if (__builtin_amdgcn_readfirstlane(__float_as_int(sd[head].keep)) != 0) {
 #pragma unroll
-            for (int x = 0; x < NTW; ++x) {
-                const float keep = sd[tile_head[x]].keep, change = sd[tile_head[x]].change;
+                for (int x = 0; x < NTW; ++x)
 #pragma unroll
-                for (int t = 0; t < 8; ++t)
+                    for (int t = 0; t < 8; ++t)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) S[x][t][r] = __builtin_fmaf(S[x][t][r], change, S[x][t][r] * keep);
+                        for (int r = 0; r < 4; ++r) S[x][t][r] = __builtin_fmaf(S[x][t][r], change, S[x][t][r]);
+            } else {
+#pragma unroll
+                for (int x = 0; x < NTW; ++x)
+#pragma unroll
+                    for (int t = 0; t < 8; ++t) S[x][t] *= change;
             }
         }
         const int krow = g * 8 + (l16 >> 2), kcol = (l16 & 3) * 32;
         auto k_frag = [&](int kb, int t) {
-            const int row = kb * 32 + krow, col = kcol + t * 4;
-            return join4(lds_read_tr(&s.k[row][col]), lds_read_tr(&s.k[row + 4][col]));
+            const int row = kb * 32 + krow, n = kcol + t * 4;
+            return join4(lds_read_tr(&s.k[row][n]), lds_read_tr(&s.k[row + 4][n]));
         };
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
             bf16x8 w[NTW][kTerms];
+            const float* od = &sd[head].out[kb * 32 + g * 8];
+            const f32x4 o0 = *reinterpret_cast<const f32x4*>(od), o1 = *reinterpret_cast<const f32x4*>(od + 4);
+            const float oe[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
 #pragma unroll
             for (int x = 0; x < NTW; ++x) {
-                const float* od = &sd[tile_head[x]].out[kb * 32 + g * 8];
-                const f32x4 o0 = *reinterpret_cast<const f32x4*>(od), o1 = *reinterpret_cast<const f32x4*>(od + 4);
-                const float oe[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
                     f32x2 v = from_bf16(bf16x2{vf[x][kb][e], vf[x][kb][e + 1]});
@@ -637,7 +645,7 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
         for (int x = 0; x < NTW; ++x)
             if (have[x]) {
 #pragma unroll
-                for (int t = 0; t < 8; ++t) *reinterpret_cast<f32x4*>(rows + (wave + 4 * x) * 2048 + t * kStep) = S[x][t];
+                for (int t = 0; t < 8; ++t) *reinterpret_cast<f32x4*>(rows + (col / 16 + x) * 2048 + t * kStep) = S[x][t];
             }
     }
     if constexpr (MODE == PART_STATE) {
