@@ -208,10 +208,23 @@ __device__ __forceinline__ double add_dpp(double x)
     return x + __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
-// a decay of 2^c as keep*x + change*x: from 1/2 up the change alone is rounded
+// A decay of 2^c as keep*x + change*x.  From 1/2 up the change, exp(y) - 1 of y = c ln 2, is
+// taken by itself, as the exponential's series (to y^10: the rest is below 2^-26 of it), so that
+// the same decay, chunk after chunk, does not add up one rounding of a number next to 1.
 __device__ __forceinline__ float2 decay_of(double c)
 {
-    return c > -1.0 ? make_float2(1.0f, expm1f((float)(c * 0.6931471805599453))) : make_float2(0.0f, exp2_of(c));
+    const float y = fmaxf((float)(c * 0.6931471805599453), -0.6931472f);
+    float p = 1.0f / 3628800.0f;
+    p = __builtin_fmaf(p, y, 1.0f / 362880.0f);
+    p = __builtin_fmaf(p, y, 1.0f / 40320.0f);
+    p = __builtin_fmaf(p, y, 1.0f / 5040.0f);
+    p = __builtin_fmaf(p, y, 1.0f / 720.0f);
+    p = __builtin_fmaf(p, y, 1.0f / 120.0f);
+    p = __builtin_fmaf(p, y, 1.0f / 24.0f);
+    p = __builtin_fmaf(p, y, 1.0f / 6.0f);
+    p = __builtin_fmaf(p, y, 0.5f);
+    const bool near = c > -1.0;
+    return make_float2(near ? 1.0f : 0.0f, near ? __builtin_fmaf(p * y, y, y) : exp2_of(c));
 }
 
 __device__ __forceinline__ double readlane_d(double x, int lane)
@@ -420,32 +433,25 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
             rv[i] = __builtin_amdgcn_raw_buffer_load_b128(bv, v_off + 16 * i * v_row, 0, 0);
         }
     };
-    // One wave makes the decays, of both heads at once.  It has the fewest scores, and makes a
-    // chunk's while the chunk before it is run.
-    float rg[HEADS];
+    // The last waves, which have the fewest scores, make the decays of a head each, a chunk's
+    // while the chunk before it is run.
+    const int dhead = 3 - wave; // this wave's head, if there is such a one
+    float rg = 0.0f;
     auto fetch_decays = [&](int64_t t0) {
-#pragma unroll
-        for (int h = 0; h < HEADS; ++h) {
-            rg[h] = 0.0f;
-            if (h < nh && a.g && t0 + lane < end) rg[h] = a.g[(t0 + lane) * a.gs + head0 + h];
-        }
+        rg = 0.0f;
+        if (dhead < nh && a.g && t0 + lane < end) rg = a.g[(t0 + lane) * a.gs + head0 + dhead];
     };
-    double after[HEADS]; // PART_STATE: the decays of the chunks behind
-#pragma unroll
-    for (int h = 0; h < HEADS; ++h) after[h] = 0.0;
+    double after = 0.0; // PART_STATE: the decays of the chunks behind
     auto make_decays = [&](int buf) {
-#pragma unroll
-        for (int h = 0; h < HEADS; ++h) {
-            if constexpr (MODE == PART_STATE) write_decays(rg[h], lane, after[h], s.d[buf][h]);
-            else chunk_decays(rg[h], a.oscale, lane, s.d[buf][h]);
-        }
+        if constexpr (MODE == PART_STATE) write_decays(rg, lane, after, s.d[buf][dhead]);
+        else chunk_decays(rg, a.oscale, lane, s.d[buf][dhead]);
     };
     // PART_STATE runs from the last chunk to the first, so that what is summed need not decay
     const int64_t chunks = (end - begin + kChunk - 1) / kChunk;
     auto start = [&](int64_t n) { return begin + (MODE == PART_STATE ? chunks - 1 - n : n) * kChunk; };
     if (chunks > 0) { // an empty sequence has no row that a descriptor could end with
         fetch(start(0));
-        if (wave == 3) {
+        if (dhead < HEADS) {
             fetch_decays(start(0));
             make_decays(0);
             if (chunks > 1) fetch_decays(start(1));
@@ -466,7 +472,7 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
         __syncthreads();
         const bool more = n + 1 < chunks;
         if (SSQ_LA_EARLY && more) fetch(start(n + 1));
-        if (wave == 3 && more) {
+        if (dhead < HEADS && more) {
             make_decays(buf ^ 1);
             if (n + 2 < chunks) fetch_decays(start(n + 2));
         }
@@ -649,11 +655,7 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
             }
     }
     if constexpr (MODE == PART_STATE) {
-        if (wave == 3 && lane == 0 && p0 == 0) {
-#pragma unroll
-            for (int h = 0; h < HEADS; ++h)
-                if (h < nh) c.part_decay[(int64_t)item * a.H + head0 + h] = decay_of(after[h]);
-        }
+        if (dhead < nh && lane == 0 && p0 == 0) c.part_decay[(int64_t)item * a.H + head0 + dhead] = decay_of(after);
     }
 }
 
