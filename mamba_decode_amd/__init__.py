@@ -12,6 +12,7 @@ Importing this package fails loudly if the library has not been built
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch  # imported first: the library binds to the HIP runtime torch has loaded
@@ -350,82 +351,100 @@ def ssq_stream_copy(dst, src, nbytes: int | None = None, stream=None):
 
 _DTYPES = {torch.float32: SSQ_DTYPE_FP32, torch.bfloat16: SSQ_DTYPE_BF16, torch.float16: SSQ_DTYPE_FP16}
 
+# The calls below are short enough on the device that their checks count: one function sees to a
+# tensor's dtype, device, shape and layout and says what is wrong only if something is.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
-def _here(t, name: str, dtype, shape=None):
-    """A tensor on the current device, of this dtype and shape (None: any extent)."""
+
+def _stream_ptr(stream, dev: int) -> int:
+    if stream is None:
+        return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _refuse(t, name: str, dtype, shape, dev: int):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be on the current CUDA device")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, is {t.dtype}")
-    if shape is not None and (t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape))):
-        raise ValueError(f"{name} has the shape {tuple(t.shape)}, expected {shape}")
-    return t
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has the shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _flat(t, name: str, dtype, shape):
+def _ptr(t, name: str, dtype, shape, dev: int):
+    """Device pointer of a contiguous tensor of this dtype and shape on device ``dev``."""
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or t.shape != shape
+            or not t.is_contiguous()):
+        _refuse(t, name, dtype, shape, dev)
+    return t.data_ptr()
+
+
+def _flags(t, name: str, shape, dev: int):
+    """The same of uint8 or bool flags, or None."""
     if t is None:
         return None
-    if not _here(t, name, dtype, shape).is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return _ptr(t, name, torch.bool if isinstance(t, torch.Tensor) and t.dtype is torch.bool else torch.uint8, shape, dev)
 
 
-def _flags(t, name: str, shape):
-    if t is not None and isinstance(t, torch.Tensor) and t.dtype == torch.bool:
-        t = t.view(torch.uint8)
-    return _flat(t, name, torch.uint8, shape)
-
-
-def _token_stride(t, name: str) -> int:
-    """Elements from one token to the next of a [tokens][heads][width] or [tokens][heads] tensor whose tokens are packed."""
+def _tokens(t, name: str, dtype, shape, dev: int):
+    """Pointer and stride between tokens of a [tokens][heads][width] or [tokens][heads] tensor whose tokens are packed."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        _refuse(t, name, dtype, shape, dev)
+    if t.is_contiguous():
+        return t.data_ptr(), math.prod(shape[1:])
     want = 1
-    for n, s in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+    for n, s in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
         if n != 1 and s != want:
             raise ValueError(f"the heads of {name} must be packed within a token")
         want *= n
-    return t.stride(0) if t.shape[0] > 1 else want
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else want
 
 
-def _workspace(given, need: int, stream):
+def _workspace(given, need: int, stream, dev: int):
     """Device memory for one call on ``stream``: the caller's, or torch's, which is reused in the stream's order."""
     if given is not None:
-        return _here(given, "workspace", torch.uint8)
+        return given, _ptr(given, "workspace", torch.uint8, given.shape, dev), given.numel()
     if need == 0:
-        return None
-    if stream is None or stream == torch.cuda.current_stream():
-        return torch.empty(need, dtype=torch.uint8, device="cuda")
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream))
-    with torch.cuda.stream(stream):
-        return torch.empty(need, dtype=torch.uint8, device="cuda")
+        return None, None, 0
+    if stream is None:
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    else:
+        with torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))):
+            ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    return ws, ws.data_ptr(), need
 
 
-def _linattn_io(state: State, q, k, v, g, o, scale: float, tokens: int):
+def _linattn_io(state: State, q, k, v, g, o, scale: float, tokens: int, dev: int):
     d = state.desc
-    if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPES:
+    if d.kind != SSQ_MAMBA2:
+        raise SsqError(SSQ_ERR_KIND_MISMATCH, "linear attention", "it runs on an SSQ_MAMBA2 state")
+    dtype = q.dtype if isinstance(q, torch.Tensor) else None
+    if dtype not in _DTYPES:
         raise ValueError("q must be a float32, bfloat16 or float16 tensor")
-    io = ssq_linattn_io(dtype=_DTYPES[q.dtype], scale=float(scale))
-    # a state of the other kind is rejected by the library
-    G, H, P, N = _sizes(state, SSQ_MAMBA2, d.ngroups, d.nheads, d.rows_per_head, d.row_len)
-    for name, t, dtype, shape in (("q", q, q.dtype, (tokens, G, N)), ("k", k, q.dtype, (tokens, G, N)),
-                                  ("v", v, q.dtype, (tokens, H, P)), ("o", o, q.dtype, (tokens, H, P)),
-                                  ("g", g, torch.float32, (tokens, H))):
-        if t is None and name == "g":
-            continue
-        _here(t, name, dtype, shape)
-        setattr(io, name + "_stride", _token_stride(t, name))
-        setattr(io, name, t.data_ptr())
-    return io
+    keys, values = (tokens, d.ngroups, d.row_len), (tokens, d.nheads, d.rows_per_head)
+    qp, qs = _tokens(q, "q", dtype, keys, dev)
+    kp, ks = _tokens(k, "k", dtype, keys, dev)
+    vp, vs = _tokens(v, "v", dtype, values, dev)
+    op, os_ = _tokens(o, "o", dtype, values, dev)
+    gp, gs = (None, 0) if g is None else _tokens(g, "g", torch.float32, values[:2], dev)
+    if tokens == 0:  # no row is read: any stride serves
+        qs = ks = keys[1] * keys[2]
+        vs = os_ = values[1] * values[2]
+    return ssq_linattn_io(_DTYPES[dtype], scale, qp, kp, vp, gp, op, qs, ks, vs, gs, os_)
 
 
 def ssq_linattn_workspace(state: State, nseq: int, tokens: int) -> int:
     """Bytes of workspace ``ssq_linattn_prefill`` needs for these sizes."""
-    n = int(lib.ssq_linattn_workspace(state.handle, nseq, tokens))
-    if n == ctypes.c_size_t(-1).value:
+    n = lib.ssq_linattn_workspace(state.handle, nseq, tokens)
+    if n == _SIZE_MAX:
         raise ValueError("linear attention runs on an SSQ_MAMBA2 state, sizes must not be negative")
     return n
+
+
+_SIZE_MAX = ctypes.c_size_t(-1).value
 
 
 def ssq_linattn_prefill(state: State, q, k, v, g, o, cu_seqlens, slots=None, fresh=None, scale: float = 1.0,
@@ -433,71 +452,83 @@ def ssq_linattn_prefill(state: State, q, k, v, g, o, cu_seqlens, slots=None, fre
     """Ragged prompts through linear attention with a decay for each head.
 
     q, k ``[tokens, ngroups, 128]``, v, o ``[tokens, nheads, P]`` (float32, bfloat16 or float16; any stride between
-    tokens that is a multiple of 16 bytes), g ``[tokens, nheads]`` float32 log decays or None, cu_seqlens int32
-    ``[nseq + 1]``, slots int32 ``[nseq]`` or None, fresh uint8 or bool ``[nseq]`` or None; all on the device.
-    ``workspace``: uint8, at least ``ssq_linattn_workspace`` bytes, or None to take it from torch."""
+    tokens that is a multiple of 16 bytes and not below a token's row), g ``[tokens, nheads]`` float32 log decays or
+    None, cu_seqlens int32 ``[nseq + 1]``, slots int32 ``[nseq]`` or None, fresh uint8 or bool ``[nseq]`` or None; all
+    on the device.  ``workspace``: uint8, at least ``ssq_linattn_workspace`` bytes, or None to take it from torch."""
+    dev = torch.cuda.current_device()
     tokens = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() else 0
-    nseq = _here(cu_seqlens, "cu_seqlens", torch.int32, (None,)).numel() - 1
+    io = _linattn_io(state, q, k, v, g, o, scale, tokens, dev)
+    nseq = cu_seqlens.numel() - 1 if isinstance(cu_seqlens, torch.Tensor) else 0
     if nseq < 0:
         raise ValueError("cu_seqlens has nseq + 1 entries")
-    io = _linattn_io(state, q, k, v, g, o, scale, tokens)
-    need = ssq_linattn_workspace(state, nseq, tokens) if state.desc.kind == SSQ_MAMBA2 else 0
-    ws = _workspace(workspace, need, stream)
-    _check(lib.ssq_linattn_prefill(state.handle, ctypes.byref(io), nseq, tokens,
-                                   _flat(cu_seqlens, "cu_seqlens", torch.int32, (nseq + 1,)),
-                                   _flat(slots, "slots", torch.int32, (nseq,)), _flags(fresh, "fresh", (nseq,)),
-                                   None if ws is None else ctypes.c_void_p(ws.data_ptr()),
-                                   0 if ws is None else ws.numel(), _stream(stream)), "ssq_linattn_prefill")
+    cu = _ptr(cu_seqlens, "cu_seqlens", torch.int32, (nseq + 1,), dev)
+    sp = None if slots is None else _ptr(slots, "slots", torch.int32, (nseq,), dev)
+    fp = _flags(fresh, "fresh", (nseq,), dev)
+    ws, wp, wn = _workspace(workspace, ssq_linattn_workspace(state, nseq, tokens), stream, dev)
+    _check(lib.ssq_linattn_prefill(state.handle, io, nseq, tokens, cu, sp, fp, wp, wn, _stream_ptr(stream, dev)),
+           "ssq_linattn_prefill")
 
 
 def ssq_linattn_step(state: State, q, k, v, g, o, slots=None, scale: float = 1.0, readout: int = SSQ_READ_POST_QUANT,
                      stream=None):
     """One token of linear attention for ``nseq = q.shape[0]`` sequences: row i of the tensors (as in
     ``ssq_linattn_prefill``) is sequence ``slots[i]`` of the state, or sequence i without slots."""
+    dev = torch.cuda.current_device()
     nseq = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() else 0
-    io = _linattn_io(state, q, k, v, g, o, scale, nseq)
-    _check(lib.ssq_linattn_step(state.handle, ctypes.byref(io), nseq, _flat(slots, "slots", torch.int32, (nseq,)),
-                                readout, _stream(stream)), "ssq_linattn_step")
+    io = _linattn_io(state, q, k, v, g, o, scale, nseq, dev)
+    sp = None if slots is None else _ptr(slots, "slots", torch.int32, (nseq,), dev)
+    _check(lib.ssq_linattn_step(state.handle, io, nseq, sp, readout, _stream_ptr(stream, dev)), "ssq_linattn_step")
 
 
 def ssq_beam_workspace(desc: ssq_beam_desc) -> int:
-    return int(lib.ssq_beam_workspace(ctypes.byref(desc)))
+    """Bytes of workspace ``ssq_beam_select`` needs, 0 for an invalid description."""
+    return lib.ssq_beam_workspace(desc)
 
 
 def ssq_beam_select(logits, scores, out_scores, out_tokens, out_parents, finished=None, pad_token: int = 0,
                     workspace: torch.Tensor | None = None, stream=None):
     """The best ``out_scores.shape[1]`` continuations of every request over its beams and the vocabulary.
 
-    logits ``[batch, beams, vocab]`` (float32, bfloat16 or float16; beams any stride apart), scores ``[batch, beams]``
-    float32, out_scores float32, out_tokens and out_parents int32 ``[batch, nselect]``, finished uint8 or bool
-    ``[batch, beams]`` or None."""
+    logits ``[batch, beams, vocab]`` (float32, bfloat16 or float16; the beams any stride apart), scores
+    ``[batch, beams]`` float32, out_scores float32, out_tokens and out_parents int32 ``[batch, nselect]``, finished
+    uint8 or bool ``[batch, beams]`` or None."""
+    dev = torch.cuda.current_device()
     if not isinstance(logits, torch.Tensor) or logits.dtype not in _DTYPES or logits.dim() != 3:
         raise ValueError("logits must be a float32, bfloat16 or float16 tensor [batch, beams, vocab]")
+    if logits.get_device() != dev:
+        raise ValueError("logits must be on the current CUDA device")
     b, m, v = logits.shape
-    _here(logits, "logits", logits.dtype)
-    row = logits.stride(1) if m > 1 else (logits.stride(0) if b > 1 else v)
-    if v > 1 and logits.stride(2) != 1 or b > 1 and logits.stride(0) != m * row:
-        raise ValueError("the rows of logits must be contiguous and evenly spaced")
-    n = _here(out_scores, "out_scores", torch.float32, (b, None)).shape[1]
+    row = v
+    if not logits.is_contiguous():
+        s = logits.stride()
+        row = s[1] if m > 1 else s[0] if b > 1 else v
+        if v > 1 and s[2] != 1 or b > 1 and s[0] != m * row:
+            raise ValueError("the rows of logits must be contiguous and evenly spaced")
+    n = out_scores.shape[1] if isinstance(out_scores, torch.Tensor) and out_scores.dim() == 2 else 0
+    sp = _ptr(scores, "scores", torch.float32, (b, m), dev)
+    fp = _flags(finished, "finished", (b, m), dev)
+    osp = _ptr(out_scores, "out_scores", torch.float32, (b, n), dev)
+    otp = _ptr(out_tokens, "out_tokens", torch.int32, (b, n), dev)
+    opp = _ptr(out_parents, "out_parents", torch.int32, (b, n), dev)
     d = ssq_beam_desc(_DTYPES[logits.dtype], b, m, v, n, pad_token, row)
-    ws = _workspace(workspace, ssq_beam_workspace(d), stream)
-    _check(lib.ssq_beam_select(ctypes.byref(d), ctypes.c_void_p(logits.data_ptr()),
-                               _flat(scores, "scores", torch.float32, (b, m)), _flags(finished, "finished", (b, m)),
-                               _flat(out_scores, "out_scores", torch.float32, (b, n)),
-                               _flat(out_tokens, "out_tokens", torch.int32, (b, n)),
-                               _flat(out_parents, "out_parents", torch.int32, (b, n)),
-                               None if ws is None else ctypes.c_void_p(ws.data_ptr()),
-                               0 if ws is None else ws.numel(), _stream(stream)), "ssq_beam_select")
+    ws, wp, wn = _workspace(workspace, lib.ssq_beam_workspace(d), stream, dev)
+    _check(lib.ssq_beam_select(d, logits.data_ptr(), sp, fp, osp, otp, opp, wp, wn, _stream_ptr(stream, dev)),
+           "ssq_beam_select")
 
 
 def ssq_state_reorder(states, parents, stream=None):
     """States follow their beams: of every group of ``parents.shape[1]`` consecutive sequences, sequence j becomes
     what sequence ``parents[group, j]`` of the group was.  ``states``: a State or a sequence of them (the layers of a
     model), each of ``parents.numel()`` sequences; parents int32 ``[groups, beams]``."""
-    states = [states] if isinstance(states, State) else list(states)
-    p = _flat(parents, "parents", torch.int32, (None, None))
+    dev = torch.cuda.current_device()
+    states = [states] if isinstance(states, State) else states
+    if not isinstance(parents, torch.Tensor) or parents.dim() != 2:
+        raise ValueError("parents must be a tensor [groups, beams]")
+    p = _ptr(parents, "parents", torch.int32, parents.shape, dev)
+    batch = parents.numel()
     for s in states:
-        if s.desc.batch != parents.numel():
-            raise ValueError(f"a state has {s.desc.batch} sequences, parents names {parents.numel()}")
-    handles = (ctypes.c_void_p * max(1, len(states)))(*[s.handle for s in states])
-    _check(lib.ssq_state_reorder(handles, len(states), p, parents.shape[1], _stream(stream)), "ssq_state_reorder")
+        if s.desc.batch != batch:
+            raise ValueError(f"a state has {s.desc.batch} sequences, parents names {batch}")
+    n = len(states)
+    handles = (ctypes.c_void_p * max(1, n))(*[s.handle.value if s.handle is not None else None for s in states])
+    _check(lib.ssq_state_reorder(handles, n, p, parents.shape[1], _stream_ptr(stream, dev)), "ssq_state_reorder")
