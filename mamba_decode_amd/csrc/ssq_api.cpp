@@ -614,7 +614,7 @@ static ssq_status check_beam(const ssq_beam_desc* d)
 size_t ssq_beam_workspace(const ssq_beam_desc* d)
 {
     if (check_beam(d) != SSQ_OK) return 0;
-    return ssq::beam_workspace(d->dtype, d->batch, d->beams, d->vocab, d->nselect);
+    return ssq::beam_workspace(d->batch, d->beams, d->vocab, d->nselect);
 }
 
 ssq_status ssq_beam_select(const ssq_beam_desc* d, const void* logits, const float* scores, const uint8_t* finished,

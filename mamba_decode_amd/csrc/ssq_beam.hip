@@ -11,10 +11,11 @@
 //
 // Selection works on unique 64-bit keys, the logit's order-preserving bits above the inverted
 // token index, so that a larger key is a larger logit or, of equal ones, the lower token; the
-// result is a set, independent of the order in which lanes append to it.  A wave holds its
-// share of a tile in registers, ranks its lanes' largest keys, and takes the nselect-th of
-// those as a threshold: at least nselect elements reach it, and only elements of the nselect
-// best lanes can, which bounds the list whatever the values are.
+// result is a set, independent of the order in which lanes append to it.  A wave runs over tiles
+// of its row with the best nselect keys so far in LDS, and looks further at a tile only if its
+// maximum passes the last of them.  In a first tile it ranks its lanes' largest keys and takes
+// the nselect-th as a threshold: at least nselect elements reach it, and only elements of the
+// nselect best lanes can, which bounds the list whatever the values are.
 #include "ssq_ops_device.h"
 
 namespace ssq {
@@ -23,7 +24,10 @@ constexpr int kBeamMaxShares = 16; // workgroups per row at most
 constexpr int kBeamNarrow = 32;    // up to this many candidates a lane holds 32 elements, above 16: the same LDS
 
 // elements a lane holds at once
-constexpr int beam_lane_elems(int nselect) { return nselect <= kBeamNarrow ? 32 : 16; }
+#ifndef SSQ_BEAM_VPL
+#define SSQ_BEAM_VPL 32
+#endif
+constexpr int beam_lane_elems(int nselect) { return nselect <= kBeamNarrow ? SSQ_BEAM_VPL : 16; }
 
 struct BeamShare {
     float m;   // largest logit, -inf if there is none
@@ -65,43 +69,58 @@ __device__ __forceinline__ float wave_sum(float v)
     return v;
 }
 
-// the n-th largest of the wave's unique keys (0: an absent one); 0 if fewer are present
-__device__ __forceinline__ uint64_t wave_nth(uint64_t key, int n)
+// the n-th largest of the wave's unique keys (0: an absent one); 0 if fewer are present.
+// `room`: 64 keys of LDS of the wave's own.
+__device__ __forceinline__ uint64_t wave_nth(uint64_t key, int n, uint64_t* room)
 {
+    const int lane = threadIdx.x & 63;
+    room[lane] = key;
+    wave_lds_sync();
     int rank = 0;
+    const ulonglong2* all = reinterpret_cast<const ulonglong2*>(room);
 #pragma unroll 8
-    for (int i = 0; i < 64; ++i) {
-        const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)key, i);
-        const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(key >> 32), i);
-        rank += (((uint64_t)hi << 32) | lo) > key;
+    for (int i = 0; i < 32; ++i) {
+        const ulonglong2 two = all[i];
+        rank += (two.x > key) + (two.y > key);
     }
+    wave_lds_sync();
     const uint64_t at = __ballot(key != 0 && rank == n - 1);
     return at ? shfl_u64(key, __builtin_ctzll(at)) : 0;
+}
+
+// keys larger than `key` among list[0 .. count)
+__device__ __forceinline__ int keys_above(const uint64_t* list, int count, uint64_t key)
+{
+    int above = 0;
+    for (int j = 0; j < count; ++j) above += list[j] > key;
+    return above;
 }
 
 // ---------------------------------------------------------------------------
 // one share of one beam's row
 // ---------------------------------------------------------------------------
+// LDS of a wave: two lists of n, then VPL*n new keys (and at least the 64 of wave_nth)
+constexpr int beam_wave_keys(int vpl, int n) { return 2 * n + (vpl * n > 64 ? vpl * n : 64); }
+
 template <int DT, int VPL>
 __global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a, BeamShare* shares, uint64_t* best, int nshares)
 {
     constexpr int VE = DT == DT_FP32 ? 4 : 8; // elements in 16 bytes
     constexpr int NV = VPL / VE;
-    constexpr int TILE = 256 * VPL;           // elements of a workgroup's tile
-    extern __shared__ uint64_t lds[];         // two lists of nselect, then 4 * VPL * nselect new keys
-    __shared__ int count;
-    __shared__ uint64_t wave_thr[4];
+    constexpr int TILE = 64 * VPL;            // elements of a wave's tile
+    extern __shared__ __align__(16) uint64_t lds[];
     __shared__ BeamShare wave_share[4];
+    __shared__ int wave_kept[4];
     const int n = a.nselect;
-    uint64_t* kept = lds;
-    uint64_t* next = lds + n;
-    uint64_t* fresh = lds + 2 * n;
     const int row = blockIdx.x / nshares, share = blockIdx.x % nshares;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    BeamShare* out = shares + (int64_t)row * nshares + share;
-    uint64_t* out_best = best + ((int64_t)row * nshares + share) * n;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // a beam without candidates of its own, dead or finished: its share is not read
     if ((a.finished && a.finished[row]) || !(a.scores[row] > -INFINITY)) return;
+    uint64_t* const mine = lds + wave * beam_wave_keys(VPL, n);
+    uint64_t* kept = mine;
+    uint64_t* next = mine + n;
+    uint64_t* const fresh = mine + 2 * n;
     using T = typename Elem<DT>::T;
     const T* x = static_cast<const T*>(a.logits) + (int64_t)row * a.row_stride;
     // 16-byte pieces from the row's first aligned address down: `off` elements of piece 0 lie before the row
@@ -109,11 +128,13 @@ __global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a, BeamShare* shares
     const int64_t pieces = ((int64_t)a.vocab + off + VE - 1) / VE;
     const int64_t tiles = (pieces + TILE / VE - 1) / (TILE / VE);
 
-    float m = -INFINITY, s = 0.0f; // of this lane's elements, m of its wave's
+    float m = -INFINITY, s = 0.0f; // of this lane's elements
     int nkept = 0;
-    for (int64_t t = share; t < tiles; t += nshares) {
+    float last = -INFINITY;        // the n-th best so far; -inf while there are fewer
+    for (int64_t t = share * 4 + wave; t < tiles; t += 4 * nshares) {
         float v[VPL];
-        const int64_t p0 = t * (TILE / VE) + wave * (64 * NV) + lane;
+        const int64_t p0 = t * (TILE / VE) + lane;
+        auto token = [&](int i) { return (uint32_t)((p0 + (i / VE) * 64) * VE - off + i % VE); };
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int64_t e0 = (p0 + i * 64) * VE - off; // the piece's first element
@@ -131,91 +152,129 @@ __global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a, BeamShare* shares
             v[i] = fmaxf(v[i], -INFINITY); // a NaN is no candidate
             lm = fmaxf(lm, v[i]);
         }
-        const float wm = fmaxf(m, wave_max(lm));
-        if (wm > -INFINITY) {
-            float part = 0.0f;
+        const float wm = fmaxf(m, lm), shift = wm > -INFINITY ? wm : 0.0f; // exp(-inf - 0) is 0
+        float part = 0.0f;
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) part += __expf(v[i] - wm);
-            s = s * (m > -INFINITY ? __expf(m - wm) : 0.0f) + part;
-            m = wm;
+        for (int i = 0; i < VPL; ++i) part += __expf(v[i] - shift);
+        s = s * __expf(m - shift) + part;
+        m = wm;
+        // tiles come in the order of their tokens: an element equal to the last kept one comes behind it
+        if (!__ballot(lm > last)) continue;
+        uint64_t low = 1;
+        if (nkept == n) {
+            low = (uint64_t)(order_bits(last) + 1) << 32; // every larger value
+            int c = 0;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) c += v[i] > last;
+            if (__ballot(c > VPL * n / 64)) low = 0; // maybe more than the list takes: a threshold first
         }
-        // the lane's largest key: its first element with the largest logit
-        int first = 0;
+        if (nkept < n || low == 0) {
+            // the lane's largest key: its first element with the largest logit
+            int first = 0;
 #pragma unroll
-        for (int i = VPL - 1; i >= 0; --i) first = v[i] == lm ? i : first;
-        const int64_t fe = (p0 + (first / VE) * 64) * VE - off + first % VE;
-        const uint64_t mine = lm > -INFINITY ? beam_key(lm, (uint32_t)fe) : 0;
-        const uint64_t nth = wave_nth(mine, n);
-        if (lane == 0) wave_thr[wave] = nth;
-        if (tid == 0) count = 0;
-        for (int i = tid; i < n; i += 256) next[i] = 0;
-        __syncthreads();
-        // any wave's n-th key is a threshold for all, and so is the n-th of the tiles before
-        uint64_t low = nkept == n ? kept[n - 1] : 1;
+            for (int i = VPL - 1; i >= 0; --i) first = v[i] == lm ? i : first;
+            const uint64_t top = lm > -INFINITY ? beam_key(lm, token(first)) : 0;
+            const uint64_t nth = wave_nth(top, n, fresh);
+            low = nth > 1 ? nth : 1;
+            if (!(top >= low)) lm = -INFINITY; // only the other lanes, n at most, hold keys that reach it
+        }
+        const float low_value = low > 1 ? order_value((uint32_t)(low >> 32)) : -3.4028234663852886e38f;
+        int c = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) low = wave_thr[i] > low ? wave_thr[i] : low;
-        const uint32_t low_hi = (uint32_t)(low >> 32);
-        if (mine >= low) { // only these lanes, n of a wave at most, hold keys that reach it
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                if (v[i] > -INFINITY && order_bits(v[i]) >= low_hi) {
-                    const uint64_t key = beam_key(v[i], (uint32_t)((p0 + (i / VE) * 64) * VE - off + i % VE));
-                    if (key >= low) fresh[atomicAdd(&count, 1)] = key;
-                }
+        for (int i = 0; i < VPL; ++i) {
+            if (__ballot(lm > -INFINITY && v[i] >= low_value)) {
+                const uint64_t key = beam_key(v[i], token(i));
+                const bool take = lm > -INFINITY && v[i] >= low_value && key >= low;
+                const uint64_t who = __ballot(take);
+                if (take) fresh[c + __popcll(who & ((1ull << lane) - 1))] = key;
+                c += __popcll(who);
             }
         }
-        __syncthreads();
-        const int c = count; // at most 4 * n * VPL
-        for (int i = tid; i < nkept + c; i += 256) {
+        wave_lds_sync();
+        for (int i = lane; i < nkept + c; i += 64) {
             const uint64_t key = i < nkept ? kept[i] : fresh[i - nkept];
-            int rank = 0;
-            for (int j = 0; j < nkept; ++j) rank += kept[j] > key;
-            for (int j = 0; j < c; ++j) rank += fresh[j] > key;
+            const int rank = keys_above(kept, nkept, key) + keys_above(fresh, c, key);
             if (rank < n) next[rank] = key;
         }
+        wave_lds_sync();
         nkept = min(n, nkept + c);
         uint64_t* const swap = kept;
         kept = next;
         next = swap;
-        __syncthreads(); // the lists are written, and the counter and thresholds have been read
+        if (nkept == n) last = order_value((uint32_t)(kept[n - 1] >> 32));
     }
-    s = wave_sum(s);
-    if (lane == 0) wave_share[wave] = {m, s};
+    // the four waves' lists, each copied to its place at the front of the wave's LDS
+    const float wm = wave_max(m);
+    s = wave_sum(m > -INFINITY ? s * __expf(m - wm) : 0.0f);
+    if (kept != mine) {
+        for (int i = lane; i < nkept; i += 64) mine[i] = kept[i];
+    }
+    if (lane == 0) {
+        wave_share[wave] = {wm, s};
+        wave_kept[wave] = nkept;
+    }
     __syncthreads();
+    uint64_t* out_best = best + ((int64_t)row * nshares + share) * n;
+    int found = 0;
+    for (int w = 0; w < 4; ++w) found += wave_kept[w];
+    for (int i = tid; i < 4 * n; i += 256) {
+        const int w = i / n, r = i % n;
+        if (r >= wave_kept[w]) continue;
+        const uint64_t key = lds[w * beam_wave_keys(VPL, n) + r];
+        int rank = r;
+        for (int o = 0; o < 4; ++o)
+            if (o != w) rank += keys_above(lds + o * beam_wave_keys(VPL, n), wave_kept[o], key);
+        if (rank < n) out_best[rank] = key;
+    }
+    for (int i = found + tid; i < n; i += 256) out_best[i] = 0;
     if (tid == 0) {
         float M = -INFINITY, sum = 0.0f;
         for (int i = 0; i < 4; ++i) M = fmaxf(M, wave_share[i].m);
         for (int i = 0; i < 4; ++i)
             if (wave_share[i].m > -INFINITY) sum += wave_share[i].sum * __expf(wave_share[i].m - M);
-        *out = {M, sum};
+        shares[(int64_t)row * nshares + share] = {M, sum};
     }
-    for (int i = tid; i < n; i += 256) out_best[i] = i < nkept ? kept[i] : 0;
 }
 
 // ---------------------------------------------------------------------------
 // the shares of each beam, then the beams of each request
 // ---------------------------------------------------------------------------
+// a wave's work list: the keys of all shares, and at least the 64 of wave_nth
+__host__ __device__ constexpr int beam_join_keys(int nshares, int n) { return nshares * n > 64 ? nshares * n : 64; }
+
 struct BeamCand {
     double score;
     uint32_t beam, token;
 };
 
-__global__ __launch_bounds__(256) void k_beam_join(BeamArgs a, const BeamShare* shares, const uint64_t* best, int nshares)
+// a wave for each beam, up to 16
+__global__ __launch_bounds__(1024) void k_beam_join(BeamArgs a, const BeamShare* shares, const uint64_t* best, int nshares)
 {
     // LDS: a work list of each wave, the best [n], the beams' lists [beams][n]: scores, tokens
-    extern __shared__ uint64_t lds[];
+    extern __shared__ __align__(16) uint64_t lds[];
     __shared__ int counts[kMaxBeams];
     const int n = a.nselect, beams = a.beams;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    uint64_t* work = lds + wave * (kBeamMaxShares * n);
-    BeamCand* top = reinterpret_cast<BeamCand*>(lds + 4 * kBeamMaxShares * n);
+    const int waves = blockDim.x >> 6, room = beam_join_keys(nshares, n);
+    uint64_t* work = lds + wave * room;
+    BeamCand* top = reinterpret_cast<BeamCand*>(lds + waves * room);
     double* cand = reinterpret_cast<double*>(top + n);
     uint32_t* tokens = reinterpret_cast<uint32_t*>(cand + beams * n);
     const int64_t request = blockIdx.x;
 
-    for (int b = wave; b < beams; b += 4) {
+    for (int b = wave; b < beams; b += waves) {
         const int64_t row = request * beams + b;
         const float score = a.scores[row];
+        const int total = nshares * n; // at most 16 for each lane
+        const uint64_t* keys = best + row * total;
+        BeamShare sh = {-INFINITY, 0.0f};
+        if (lane < nshares) sh = shares[row * nshares + lane];
+        uint64_t k[kBeamMaxShares], mine = 0; // of a dead or finished beam never written, and not used
+#pragma unroll
+        for (int i = 0; i < kBeamMaxShares; ++i) {
+            k[i] = lane + 64 * i < total ? keys[lane + 64 * i] : 0;
+            mine = k[i] > mine ? k[i] : mine;
+        }
         if (!(score > -INFINITY)) {
             if (lane == 0) counts[b] = 0;
             continue;
@@ -228,27 +287,13 @@ __global__ __launch_bounds__(256) void k_beam_join(BeamArgs a, const BeamShare* 
             }
             continue;
         }
-        BeamShare sh = {-INFINITY, 0.0f};
-        if (lane < nshares) sh = shares[row * nshares + lane];
         const float M = wave_max(sh.m);
         if (!(M > -INFINITY)) {
             if (lane == 0) counts[b] = 0;
             continue;
         }
-        double sum = sh.m > -INFINITY ? (double)sh.sum * exp((double)sh.m - (double)M) : 0.0;
-#pragma unroll
-        for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
-        const double logz = log(sum);
-
-        const int total = nshares * n; // at most 16 for each lane
-        const uint64_t* keys = best + row * total;
-        uint64_t k[kBeamMaxShares], mine = 0;
-#pragma unroll
-        for (int i = 0; i < kBeamMaxShares; ++i) {
-            k[i] = lane + 64 * i < total ? keys[lane + 64 * i] : 0;
-            mine = k[i] > mine ? k[i] : mine;
-        }
-        const uint64_t nth = wave_nth(mine, n);
+        const double logz = log((double)wave_sum(sh.m > -INFINITY ? sh.sum * __expf(sh.m - M) : 0.0f));
+        const uint64_t nth = wave_nth(mine, n, work);
         const uint64_t low = nth ? nth : 1;
         int c = 0;
 #pragma unroll
@@ -260,8 +305,7 @@ __global__ __launch_bounds__(256) void k_beam_join(BeamArgs a, const BeamShare* 
         wave_lds_sync();
         for (int i = lane; i < c; i += 64) {
             const uint64_t key = work[i];
-            int rank = 0;
-            for (int j = 0; j < c; ++j) rank += work[j] > key;
+            const int rank = keys_above(work, c, key);
             if (rank < n) {
                 const double x = (double)order_value((uint32_t)(key >> 32));
                 cand[b * n + rank] = (double)score + ((x - (double)M) - logz);
@@ -276,7 +320,7 @@ __global__ __launch_bounds__(256) void k_beam_join(BeamArgs a, const BeamShare* 
     // others', which are sorted: found by halving.  Of equal scores the lower beam is first.
     int found = 0;
     for (int b = 0; b < beams; ++b) found += counts[b];
-    for (int i = tid; i < beams * n; i += 256) {
+    for (int i = tid; i < beams * n; i += blockDim.x) {
         const int b = i / n, r = i % n;
         if (r >= counts[b]) continue;
         const double me = cand[i];
@@ -295,7 +339,7 @@ __global__ __launch_bounds__(256) void k_beam_join(BeamArgs a, const BeamShare* 
         if (rank < n) top[rank] = {me, (uint32_t)b, tokens[i]};
     }
     __syncthreads();
-    for (int j = tid; j < n; j += 256) {
+    for (int j = tid; j < n; j += blockDim.x) {
         const bool have = j < found;
         const int64_t at = request * n + j;
         a.out_scores[at] = have ? (float)top[j].score : -INFINITY;
@@ -307,18 +351,23 @@ __global__ __launch_bounds__(256) void k_beam_join(BeamArgs a, const BeamShare* 
 // ---------------------------------------------------------------------------
 // launch
 // ---------------------------------------------------------------------------
-static int beam_shares(int vocab, int nselect)
+// Workgroups of a row: enough of all rows to fill the card (2048), no more than there are tiles of
+// four waves, nor than the join takes.
+static int beam_shares(int64_t rows, int vocab, int nselect)
 {
-    // one tile for a workgroup, and no more shares than the join takes
     const int tile = 256 * beam_lane_elems(nselect);
     const int64_t tiles = ((int64_t)vocab + 7 + tile - 1) / tile;
-    return tiles < kBeamMaxShares ? (int)tiles : kBeamMaxShares;
+    #ifndef SSQ_BEAM_WGS
+#define SSQ_BEAM_WGS 2048
+#endif
+    int64_t shares = (SSQ_BEAM_WGS + rows - 1) / (rows > 0 ? rows : 1);
+    if (shares > tiles) shares = tiles;
+    return (int)(shares < kBeamMaxShares ? shares : kBeamMaxShares);
 }
 
-size_t beam_workspace(int dtype, int batch, int beams, int vocab, int nselect)
+size_t beam_workspace(int batch, int beams, int vocab, int nselect)
 {
-    (void)dtype;
-    const size_t shares = (size_t)batch * beams * beam_shares(vocab, nselect);
+    const size_t shares = (size_t)batch * beams * beam_shares((int64_t)batch * beams, vocab, nselect);
     return (shares * sizeof(BeamShare) + 255) / 256 * 256 + shares * nselect * sizeof(uint64_t);
 }
 
@@ -327,7 +376,7 @@ static hipError_t launch_rows_of(const BeamArgs& a, BeamShare* shares, uint64_t*
 {
     const int64_t blocks = (int64_t)a.batch * a.beams * nshares;
     if (blocks > kMaxBlocks) return hipErrorInvalidValue;
-    const size_t lds = (size_t)(2 + 4 * VPL) * a.nselect * sizeof(uint64_t);
+    const size_t lds = 4 * (size_t)beam_wave_keys(VPL, a.nselect) * sizeof(uint64_t); // 34 KiB at most
     hipLaunchKernelGGL((k_beam_rows<DT, VPL>), dim3((unsigned)blocks), dim3(256), lds, st, a, shares, best, nshares);
     return hipGetLastError();
 }
@@ -335,17 +384,19 @@ static hipError_t launch_rows_of(const BeamArgs& a, BeamShare* shares, uint64_t*
 template <int DT>
 static hipError_t launch_beam_dt(const BeamArgs& a, hipStream_t st)
 {
-    const int nshares = beam_shares(a.vocab, a.nselect);
+    const int nshares = beam_shares((int64_t)a.batch * a.beams, a.vocab, a.nselect);
     const size_t rows = (size_t)a.batch * a.beams * nshares;
     BeamShare* shares = static_cast<BeamShare*>(a.ws);
     uint64_t* best = reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(a.ws) + (rows * sizeof(BeamShare) + 255) / 256 * 256);
     hipError_t e = a.nselect <= kBeamNarrow ? launch_rows_of<DT, beam_lane_elems(1)>(a, shares, best, nshares, st)
                                             : launch_rows_of<DT, beam_lane_elems(2 * kMaxBeams)>(a, shares, best, nshares, st);
     if (e != hipSuccess) return e;
-    // at most 32 KiB of work lists and 25 KiB of candidates
-    const size_t lds = 4 * (size_t)kBeamMaxShares * a.nselect * sizeof(uint64_t) +
-                       (size_t)a.nselect * (sizeof(BeamCand) + a.beams * (sizeof(double) + sizeof(uint32_t)));
-    hipLaunchKernelGGL(k_beam_join, dim3((unsigned)a.batch), dim3(256), lds, st, a, shares, best, nshares);
+    // the waves' lists within 32 KiB, at most 26 KiB of candidates
+    const size_t list = (size_t)beam_join_keys(nshares, a.nselect) * sizeof(uint64_t);
+    int waves = a.beams < 16 ? a.beams : 16;
+    while (waves * list > 32768) --waves;
+    const size_t lds = waves * list + (size_t)a.nselect * (sizeof(BeamCand) + a.beams * (sizeof(double) + sizeof(uint32_t)));
+    hipLaunchKernelGGL(k_beam_join, dim3((unsigned)a.batch), dim3(64 * waves), lds, st, a, shares, best, nshares);
     return hipGetLastError();
 }
 
