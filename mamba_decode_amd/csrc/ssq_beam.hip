@@ -12,22 +12,23 @@
 // Selection works on unique 64-bit keys, the logit's order-preserving bits above the inverted
 // token index, so that a larger key is a larger logit or, of equal ones, the lower token; the
 // result is a set, independent of the order in which lanes append to it.  A wave runs over tiles
-// of its row with the best nselect keys so far in LDS, and looks further at a tile only if its
-// maximum passes the last of them.  In a first tile it ranks its lanes' largest keys and takes
-// the nselect-th as a threshold: at least nselect elements reach it, and only elements of the
-// nselect best lanes can, which bounds the list whatever the values are.
+// of its row with the best nselect keys so far in LDS, and looks further at a tile only where a
+// lane's maximum passes the last of them.  The elements that do, or in a first tile those that
+// reach the nselect-th largest of the lanes' maxima (found to a few thousandths of their range by
+// halving: any value that nselect lanes reach serves), go into a short list; the list and the
+// kept keys are ranked together.  Where the list runs over (rows in order, or many equal logits),
+// the tile is taken in pieces of 16 elements a lane with an exact threshold, which bounds the list
+// whatever the values are.
 #include "ssq_ops_device.h"
 
 namespace ssq {
 
 constexpr int kBeamMaxShares = 16; // workgroups per row at most
-constexpr int kBeamNarrow = 32;    // up to this many candidates a lane holds 32 elements, above 16: the same LDS
-
-// elements a lane holds at once
 #ifndef SSQ_BEAM_VPL
 #define SSQ_BEAM_VPL 32
 #endif
-constexpr int beam_lane_elems(int nselect) { return nselect <= kBeamNarrow ? SSQ_BEAM_VPL : 16; }
+constexpr int kBeamLane = SSQ_BEAM_VPL; // elements a lane holds at once
+constexpr int kBeamPiece = 16;
 
 struct BeamShare {
     float m;   // largest logit, -inf if there is none
@@ -99,12 +100,35 @@ __device__ __forceinline__ int keys_above(const uint64_t* list, int count, uint6
 // ---------------------------------------------------------------------------
 // one share of one beam's row
 // ---------------------------------------------------------------------------
-// LDS of a wave: two lists of n, then VPL*n new keys (and at least the 64 of wave_nth)
-constexpr int beam_wave_keys(int vpl, int n) { return 2 * n + (vpl * n > 64 ? vpl * n : 64); }
+// LDS of a wave: two lists of n, then the new keys: n of a piece's lanes may have them all, and
+// wave_nth takes 64
+__host__ __device__ constexpr int beam_list_keys(int n) { return kBeamPiece * n > 64 ? kBeamPiece * n : 64; }
+__host__ __device__ constexpr int beam_wave_keys(int n) { return 2 * n + beam_list_keys(n); }
 
-template <int DT, int VPL>
+// A value that at least n of the lanes' values reach, close below the n-th largest.
+__device__ __forceinline__ float wave_threshold(float v, int n)
+{
+    const uint32_t o = order_bits(v);
+    const uint32_t top = order_bits(group_max<16>(v)), bottom = order_bits(group_min<16>(v));
+    uint32_t hi = 0, lo = 0xFFFFFFFFu;
+#pragma unroll
+    for (int r = 0; r < 64; r += 16) {
+        const uint32_t t = __builtin_amdgcn_readlane((int)top, r), b = __builtin_amdgcn_readlane((int)bottom, r);
+        hi = t > hi ? t : hi;
+        lo = b < lo ? b : lo;
+    }
+    for (int i = 0; i < 14 && lo < hi; ++i) {
+        const uint32_t mid = lo + (hi - lo) / 2 + 1;
+        if (__popcll(__ballot(o >= mid)) >= n) lo = mid;
+        else hi = mid - 1;
+    }
+    return order_value(lo);
+}
+
+template <int DT>
 __global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a, BeamShare* shares, uint64_t* best, int nshares)
 {
+    constexpr int VPL = kBeamLane;
     constexpr int VE = DT == DT_FP32 ? 4 : 8; // elements in 16 bytes
     constexpr int NV = VPL / VE;
     constexpr int TILE = 64 * VPL;            // elements of a wave's tile
@@ -117,7 +141,7 @@ __global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a, BeamShare* shares
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // a beam without candidates of its own, dead or finished: its share is not read
     if ((a.finished && a.finished[row]) || !(a.scores[row] > -INFINITY)) return;
-    uint64_t* const mine = lds + wave * beam_wave_keys(VPL, n);
+    uint64_t* const mine = lds + wave * beam_wave_keys(n);
     uint64_t* kept = mine;
     uint64_t* next = mine + n;
     uint64_t* const fresh = mine + 2 * n;
@@ -131,6 +155,20 @@ __global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a, BeamShare* shares
     float m = -INFINITY, s = 0.0f; // of this lane's elements
     int nkept = 0;
     float last = -INFINITY;        // the n-th best so far; -inf while there are fewer
+    auto merge = [&](int c) { // the new keys and the kept ones: the best n are kept
+        wave_lds_sync();
+        for (int i = lane; i < nkept + c; i += 64) {
+            const uint64_t key = i < nkept ? kept[i] : fresh[i - nkept];
+            const int rank = keys_above(kept, nkept, key) + keys_above(fresh, c, key);
+            if (rank < n) next[rank] = key;
+        }
+        wave_lds_sync();
+        nkept = min(n, nkept + c);
+        uint64_t* const swap = kept;
+        kept = next;
+        next = swap;
+        if (nkept == n) last = order_value((uint32_t)(kept[n - 1] >> 32));
+    };
     for (int64_t t = share * 4 + wave; t < tiles; t += 4 * nshares) {
         float v[VPL];
         const int64_t p0 = t * (TILE / VE) + lane;
@@ -160,48 +198,47 @@ __global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a, BeamShare* shares
         m = wm;
         // tiles come in the order of their tokens: an element equal to the last kept one comes behind it
         if (!__ballot(lm > last)) continue;
-        uint64_t low = 1;
-        if (nkept == n) {
-            low = (uint64_t)(order_bits(last) + 1) << 32; // every larger value
-            int c = 0;
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) c += v[i] > last;
-            if (__ballot(c > VPL * n / 64)) low = 0; // maybe more than the list takes: a threshold first
-        }
-        if (nkept < n || low == 0) {
-            // the lane's largest key: its first element with the largest logit
-            int first = 0;
-#pragma unroll
-            for (int i = VPL - 1; i >= 0; --i) first = v[i] == lm ? i : first;
-            const uint64_t top = lm > -INFINITY ? beam_key(lm, token(first)) : 0;
-            const uint64_t nth = wave_nth(top, n, fresh);
-            low = nth > 1 ? nth : 1;
-            if (!(top >= low)) lm = -INFINITY; // only the other lanes, n at most, hold keys that reach it
-        }
-        const float low_value = low > 1 ? order_value((uint32_t)(low >> 32)) : -3.4028234663852886e38f;
+        const int room = beam_list_keys(n);
+        const float reach = nkept == n ? order_value(order_bits(last) + 1) : wave_threshold(lm, n);
+        const float low_value = fmaxf(reach, -3.4028234663852886e38f); // -inf is no candidate
         int c = 0;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            if (__ballot(lm > -INFINITY && v[i] >= low_value)) {
-                const uint64_t key = beam_key(v[i], token(i));
-                const bool take = lm > -INFINITY && v[i] >= low_value && key >= low;
-                const uint64_t who = __ballot(take);
-                if (take) fresh[c + __popcll(who & ((1ull << lane) - 1))] = key;
+            const bool take = v[i] >= low_value;
+            const uint64_t who = __ballot(take);
+            if (who) {
+                const int at = c + __popcll(who & ((1ull << lane) - 1));
+                if (take && at < room) fresh[at] = beam_key(v[i], token(i));
                 c += __popcll(who);
             }
         }
-        wave_lds_sync();
-        for (int i = lane; i < nkept + c; i += 64) {
-            const uint64_t key = i < nkept ? kept[i] : fresh[i - nkept];
-            const int rank = keys_above(kept, nkept, key) + keys_above(fresh, c, key);
-            if (rank < n) next[rank] = key;
+        if (c <= room) {
+            merge(c);
+            continue;
         }
-        wave_lds_sync();
-        nkept = min(n, nkept + c);
-        uint64_t* const swap = kept;
-        kept = next;
-        next = swap;
-        if (nkept == n) last = order_value((uint32_t)(kept[n - 1] >> 32));
+#pragma unroll
+        for (int i0 = 0; i0 < VPL; i0 += kBeamPiece) {
+            // the lane's largest key: its first element with the largest logit
+            float pm = -INFINITY;
+            uint32_t first = 0;
+#pragma unroll
+            for (int i = i0 + kBeamPiece - 1; i >= i0; --i) {
+                first = v[i] >= pm ? token(i) : first;
+                pm = fmaxf(pm, v[i]);
+            }
+            const uint64_t top = pm > -INFINITY ? beam_key(pm, first) : 0;
+            const uint64_t nth = wave_nth(top, n, fresh), floor = nkept == n ? kept[n - 1] : 1;
+            const uint64_t low = nth > floor ? nth : floor;
+            c = 0;
+#pragma unroll
+            for (int i = i0; i < i0 + kBeamPiece; ++i) { // of n lanes at most
+                const uint64_t key = v[i] > -INFINITY ? beam_key(v[i], token(i)) : 0;
+                const uint64_t who = __ballot(key >= low);
+                if (key >= low) fresh[c + __popcll(who & ((1ull << lane) - 1))] = key;
+                c += __popcll(who);
+            }
+            merge(c);
+        }
     }
     // the four waves' lists, each copied to its place at the front of the wave's LDS
     const float wm = wave_max(m);
@@ -220,10 +257,10 @@ __global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a, BeamShare* shares
     for (int i = tid; i < 4 * n; i += 256) {
         const int w = i / n, r = i % n;
         if (r >= wave_kept[w]) continue;
-        const uint64_t key = lds[w * beam_wave_keys(VPL, n) + r];
+        const uint64_t key = lds[w * beam_wave_keys(n) + r];
         int rank = r;
         for (int o = 0; o < 4; ++o)
-            if (o != w) rank += keys_above(lds + o * beam_wave_keys(VPL, n), wave_kept[o], key);
+            if (o != w) rank += keys_above(lds + o * beam_wave_keys(n), wave_kept[o], key);
         if (rank < n) out_best[rank] = key;
     }
     for (int i = found + tid; i < n; i += 256) out_best[i] = 0;
@@ -353,13 +390,13 @@ __global__ __launch_bounds__(1024) void k_beam_join(BeamArgs a, const BeamShare*
 // ---------------------------------------------------------------------------
 // Workgroups of a row: enough of all rows to fill the card (2048), no more than there are tiles of
 // four waves, nor than the join takes.
-static int beam_shares(int64_t rows, int vocab, int nselect)
+static int beam_shares(int64_t rows, int vocab)
 {
-    const int tile = 256 * beam_lane_elems(nselect);
-    const int64_t tiles = ((int64_t)vocab + 7 + tile - 1) / tile;
-    #ifndef SSQ_BEAM_WGS
-#define SSQ_BEAM_WGS 2048
+#ifndef SSQ_BEAM_WGS
+#define SSQ_BEAM_WGS 1024
 #endif
+    const int tile = 256 * kBeamLane;
+    const int64_t tiles = ((int64_t)vocab + 7 + tile - 1) / tile;
     int64_t shares = (SSQ_BEAM_WGS + rows - 1) / (rows > 0 ? rows : 1);
     if (shares > tiles) shares = tiles;
     return (int)(shares < kBeamMaxShares ? shares : kBeamMaxShares);
@@ -367,29 +404,28 @@ static int beam_shares(int64_t rows, int vocab, int nselect)
 
 size_t beam_workspace(int batch, int beams, int vocab, int nselect)
 {
-    const size_t shares = (size_t)batch * beams * beam_shares((int64_t)batch * beams, vocab, nselect);
+    const size_t shares = (size_t)batch * beams * beam_shares((int64_t)batch * beams, vocab);
     return (shares * sizeof(BeamShare) + 255) / 256 * 256 + shares * nselect * sizeof(uint64_t);
 }
 
-template <int DT, int VPL>
+template <int DT>
 static hipError_t launch_rows_of(const BeamArgs& a, BeamShare* shares, uint64_t* best, int nshares, hipStream_t st)
 {
     const int64_t blocks = (int64_t)a.batch * a.beams * nshares;
     if (blocks > kMaxBlocks) return hipErrorInvalidValue;
-    const size_t lds = 4 * (size_t)beam_wave_keys(VPL, a.nselect) * sizeof(uint64_t); // 34 KiB at most
-    hipLaunchKernelGGL((k_beam_rows<DT, VPL>), dim3((unsigned)blocks), dim3(256), lds, st, a, shares, best, nshares);
+    const size_t lds = 4 * (size_t)beam_wave_keys(a.nselect) * sizeof(uint64_t); // 34 KiB at most
+    hipLaunchKernelGGL(k_beam_rows<DT>, dim3((unsigned)blocks), dim3(256), lds, st, a, shares, best, nshares);
     return hipGetLastError();
 }
 
 template <int DT>
 static hipError_t launch_beam_dt(const BeamArgs& a, hipStream_t st)
 {
-    const int nshares = beam_shares((int64_t)a.batch * a.beams, a.vocab, a.nselect);
+    const int nshares = beam_shares((int64_t)a.batch * a.beams, a.vocab);
     const size_t rows = (size_t)a.batch * a.beams * nshares;
     BeamShare* shares = static_cast<BeamShare*>(a.ws);
     uint64_t* best = reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(a.ws) + (rows * sizeof(BeamShare) + 255) / 256 * 256);
-    hipError_t e = a.nselect <= kBeamNarrow ? launch_rows_of<DT, beam_lane_elems(1)>(a, shares, best, nshares, st)
-                                            : launch_rows_of<DT, beam_lane_elems(2 * kMaxBeams)>(a, shares, best, nshares, st);
+    const hipError_t e = launch_rows_of<DT>(a, shares, best, nshares, st);
     if (e != hipSuccess) return e;
     // the waves' lists within 32 KiB, at most 26 KiB of candidates
     const size_t list = (size_t)beam_join_keys(nshares, a.nselect) * sizeof(uint64_t);
