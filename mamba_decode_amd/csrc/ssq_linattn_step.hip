@@ -6,13 +6,12 @@
 // on rows of 128 key entries, fp32 or quantized (then reconstructed, refit and rounded as
 // every state step does it).  The state is read and written once: bytes bound it.
 //
-// A wave takes 16 rows of one head (P is a multiple of 16), so that every wave has whole
-// rows of one (sequence, head) and its o is one run of 16 elements.
+// A wave takes 16, 32 or 64 rows of one head (P is a multiple of 16), so that q, k and the decay
+// of its (sequence, head) serve all of them and its o is one run of elements.  All of its rows are
+// in flight before the first is worked on.
 #include "ssq_ops_device.h"
 
 namespace ssq {
-
-constexpr int kStepRows = 16;
 
 // lanes per row: 16 bytes a lane and load.  A row of fp32 takes 16 lanes, each with the
 // entries 4l .. 4l+3 and 64+4l .. 64+4l+3, so that an instruction covers 256 contiguous bytes of
@@ -24,15 +23,24 @@ constexpr int linattn_lpr()
     return F == FP32 ? 16 : (Traits<F>::bits == 8 ? 8 : 4);
 }
 
-template <int F, int DT, bool PRE, bool SR>
-__global__ __launch_bounds__(256) void k_linattn_step(LinArgs a, int64_t units)
+// int4 holds 32 entries of q, k and the row in registers: three waves per SIMD by decree (168
+// registers, no spill) against two, 256 sequences of 128 heads asymmetric 91 us against 105.
+template <int F, bool SR>
+constexpr int linattn_step_waves()
 {
-    constexpr int LPR = linattn_lpr<F>(), E = 128 / LPR, RPW = 64 / LPR, K = kStepRows / RPW;
+    return F != FP32 && Traits<F>::bits == 4 && !SR ? 3 : 1;
+}
+
+template <int F, int DT, int ROWS, bool PRE, bool SR>
+__global__ __launch_bounds__(256, (linattn_step_waves<F, SR>())) void k_linattn_step(LinArgs a, int64_t units)
+{
+    constexpr int LPR = linattn_lpr<F>(), E = 128 / LPR, RPW = 64 / LPR, K = ROWS / RPW;
+    static_assert(K <= LPR, "a lane of each row stores one output");
     constexpr int NW = F == FP32 ? E : E * Traits<F>::bits / 32;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int64_t unit = (int64_t)blockIdx.x * 4 + wave;
     if (unit >= units) return;
-    const int parts = a.P / kStepRows;
+    const int parts = a.P / ROWS;
     const int part = (int)(unit % parts);
     const int64_t ih = unit / parts;
     const int head = (int)(ih % a.H);
@@ -40,7 +48,7 @@ __global__ __launch_bounds__(256) void k_linattn_step(LinArgs a, int64_t units)
     const int slot = a.slots ? a.slots[seq] : seq;
     if (slot < 0 || slot >= a.batch) return;
     const int lane = threadIdx.x & 63, sub = lane % LPR, grp = lane / LPR;
-    const int64_t row0 = ((int64_t)slot * a.H + head) * a.P + part * kStepRows;
+    const int64_t row0 = ((int64_t)slot * a.H + head) * a.P + part * ROWS;
     const int kvh = head / (a.H / a.G);
 
     uint32_t w[K][NW];
@@ -70,7 +78,7 @@ __global__ __launch_bounds__(256) void k_linattn_step(LinArgs a, int64_t units)
         load_elems<DT, E>(elem_ptr<DT>(kp, E * sub), k);
         load_elems<DT, E>(elem_ptr<DT>(qp, E * sub), q);
     }
-    const int64_t v0 = seq * a.vs + (int64_t)head * a.P + part * kStepRows;
+    const int64_t v0 = seq * a.vs + (int64_t)head * a.P + part * ROWS;
     float v[K];
 #pragma unroll
     for (int i = 0; i < K; ++i) v[i] = load_elem<DT>(a.v, v0 + i * RPW + grp);
@@ -116,35 +124,56 @@ __global__ __launch_bounds__(256) void k_linattn_step(LinArgs a, int64_t units)
             }
             if constexpr (!PRE) {
                 // fl(c' - z') of the new row: exact against Mr on the fast path
+                if (fast) {
 #pragma unroll
-                for (int e = 0; e < E; ++e)
-                    acc = __builtin_fmaf(q[e], fast ? h[e] - g.Mr : (h[e] - kMagic) - g.z, acc);
+                    for (int e = 0; e < E; ++e) acc = __builtin_fmaf(q[e], h[e] - g.Mr, acc);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc = __builtin_fmaf(q[e], (h[e] - kMagic) - g.z, acc);
+                }
             }
             acc = group_sum<LPR>(acc);
             if constexpr (!PRE) acc *= g.s;
         }
         if (sub == i) out = acc; // lane (grp, i) keeps the row that it stores
     }
-    if (sub < K) store_elem<DT>(a.o, seq * a.os + (int64_t)head * a.P + part * kStepRows + sub * RPW + grp, a.oscale * out);
+    if (sub < K) store_elem<DT>(a.o, seq * a.os + (int64_t)head * a.P + part * ROWS + sub * RPW + grp, a.oscale * out);
 }
 
-template <int F, int DT>
-static hipError_t launch_step_fd(const LinArgs& a, bool pre, hipStream_t st)
+template <int F, int DT, int ROWS>
+static hipError_t launch_step_rows(const LinArgs& a, bool pre, hipStream_t st)
 {
-    const int64_t units = (int64_t)a.nseq * a.H * (a.P / kStepRows);
+    const int64_t units = (int64_t)a.nseq * a.H * (a.P / ROWS);
     const int64_t blocks = (units + 3) / 4;
     if (blocks > kMaxBlocks) return hipErrorInvalidValue;
     const dim3 grid((unsigned)blocks), wg(256);
     if constexpr (F == FP32) {
-        hipLaunchKernelGGL((k_linattn_step<F, DT, true, false>), grid, wg, 0, st, a, units);
+        hipLaunchKernelGGL((k_linattn_step<F, DT, ROWS, true, false>), grid, wg, 0, st, a, units);
     } else if (a.sr.on) {
-        if (pre) hipLaunchKernelGGL((k_linattn_step<F, DT, true, true>), grid, wg, 0, st, a, units);
-        else hipLaunchKernelGGL((k_linattn_step<F, DT, false, true>), grid, wg, 0, st, a, units);
+        if (pre) hipLaunchKernelGGL((k_linattn_step<F, DT, ROWS, true, true>), grid, wg, 0, st, a, units);
+        else hipLaunchKernelGGL((k_linattn_step<F, DT, ROWS, false, true>), grid, wg, 0, st, a, units);
     } else {
-        if (pre) hipLaunchKernelGGL((k_linattn_step<F, DT, true, false>), grid, wg, 0, st, a, units);
-        else hipLaunchKernelGGL((k_linattn_step<F, DT, false, false>), grid, wg, 0, st, a, units);
+        if (pre) hipLaunchKernelGGL((k_linattn_step<F, DT, ROWS, true, false>), grid, wg, 0, st, a, units);
+        else hipLaunchKernelGGL((k_linattn_step<F, DT, ROWS, false, false>), grid, wg, 0, st, a, units);
     }
     return hipGetLastError();
+}
+
+// More rows a wave once that leaves 4096 waves, 4 on each SIMD: q, k and the decay, an exponential
+// in double, are then made for fewer waves.  256 sequences of 128 heads (2.1 M rows): int4
+// asymmetric 146 us at 16 rows, 91 at 64; int8 asymmetric 141 at 16, 111 at 32, 117 at 64.  61
+// sequences of 32 heads, int8: 12.2 us at 16 rows, 14.6 at 64.
+template <int F, int DT>
+static hipError_t launch_step_fd(const LinArgs& a, bool pre, hipStream_t st)
+{
+    constexpr int64_t kWaves = 4096;
+    if constexpr (F != FP32) {
+        const int64_t rows = (int64_t)a.nseq * a.H * a.P;
+        if constexpr (Traits<F>::bits == 4)
+            if (a.P % 64 == 0 && rows / 64 >= kWaves) return launch_step_rows<F, DT, 64>(a, pre, st);
+        if (a.P % 32 == 0 && rows / 32 >= kWaves) return launch_step_rows<F, DT, 32>(a, pre, st);
+    }
+    return launch_step_rows<F, DT, 16>(a, pre, st);
 }
 
 template <int F>

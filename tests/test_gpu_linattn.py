@@ -319,6 +319,24 @@ def test_tokens_are_the_decode_step(fmt, sr, pre):
         assert ((o.cpu().double() - y.cpu().double()).abs() <= 2 * 130 * 2.0 ** -24 * (mag + mag.mean())).all(), t
 
 
+@pytest.mark.parametrize("fmt", ["int8_asym", "int4_asym", "int4_sym"])
+def test_tokens_of_a_large_batch(fmt):
+    """Enough rows that a wave takes 32 or 64 of them: the same bytes as in small calls."""
+    say("large batch", fmt)
+    gen = torch.Generator(device="cuda").manual_seed(17)
+    for P in (64, 32):
+        B, H = 4096 * 64 // (32 * P), 32
+        start = torch.randn(B, H, P, 128, device="cuda", generator=gen)
+        one, two = state_of(start, 1, fmt), state_of(start, 1, fmt)
+        q, k, v, g = (x.cuda() for x in ref.inputs(torch.Generator().manual_seed(18), B, H, 1, P, BF))
+        o, o2 = torch.empty_like(v), torch.empty_like(v)
+        ssq.ssq_linattn_step(one, q, k, v, g, o)
+        for i in range(0, B, 16):
+            slots = torch.arange(i, i + 16, dtype=torch.int32, device="cuda")
+            ssq.ssq_linattn_step(two, q[i:i + 16], k[i:i + 16], v[i:i + 16], g[i:i + 16], o2[i:i + 16], slots=slots)
+        assert torch.equal(one.storage, two.storage) and torch.equal(o, o2)
+
+
 @pytest.mark.parametrize("dtype", [BF, HF])
 def test_tokens_of_half_types_on_a_quantized_state(dtype):
     """Half-type inputs are exact in fp32: the bytes are those of the same values in fp32."""
