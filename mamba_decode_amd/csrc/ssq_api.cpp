@@ -565,7 +565,7 @@ ssq_status ssq_linattn_prefill(ssq_state* st, const ssq_linattn_io* io, int32_t 
     if (s != SSQ_OK) return s;
     SSQ_REQUIRE(nseq == 0 || cu_seqlens, SSQ_ERR_INVALID_ARG, "cu_seqlens is NULL");
     SSQ_REQUIRE(aligned(cu_seqlens, 4), SSQ_ERR_INVALID_ARG, "cu_seqlens must be 4-byte aligned");
-    SSQ_REQUIRE(tokens <= 0x7FFFFFFF, SSQ_ERR_UNSUPPORTED, "cu_seqlens counts up to 2^31-1 tokens");
+    SSQ_REQUIRE(tokens < 0x7FFFFF80, SSQ_ERR_UNSUPPORTED, "a call takes up to 2^31-128 tokens");
     const size_t need = ssq_linattn_workspace(st, nseq, tokens);
     SSQ_REQUIRE(need == 0 || (workspace && workspace_bytes >= need), SSQ_ERR_INVALID_ARG, "the workspace is too small");
     SSQ_REQUIRE(aligned(workspace, 256), SSQ_ERR_INVALID_ARG, "the workspace must be 256-byte aligned");

@@ -1,9 +1,6 @@
-// ssq_linattn_prefill.hip -- linear attention with a decay for each head over ragged prompts.
-//
-// A wave takes four rows of one (sequence, head) from the first token to the last: 16 lanes a
-// row, 8 entries a lane, the recurrence in fp32.
-#include <type_traits>
-
+// ssq_linattn_prefill.hip -- linear attention with a decay for each head over ragged prompts,
+// gfx950: chunks of tokens on the matrix cores, bf16 products for bf16 tensors and fp32 products
+// for fp32 and fp16 ones.
 #include "ssq_ops_device.h"
 
 namespace ssq {
@@ -82,42 +79,6 @@ __device__ __forceinline__ float* seq_rows(const LinArgs& a, int seq, int slot)
 {
     return a.h32 + (int64_t)(a.codes ? seq : slot) * a.H * a.P * 128;
 }
-
-template <int DT>
-__global__ __launch_bounds__(256) void k_linattn_scan(LinArgs a, int64_t units)
-{
-    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int64_t unit = (int64_t)blockIdx.x * 4 + wave;
-    if (unit >= units) return;
-    const int parts = a.P / 4;
-    const int part = (int)(unit % parts), head = (int)(unit / parts % a.H), seq = (int)(unit / parts / a.H);
-    const SeqSpan s = seq_span(a, seq);
-    const bool fresh = a.fresh && a.fresh[seq];
-    if (s.slot < 0 || (!fresh && s.begin == s.end)) return;
-    const int lane = threadIdx.x & 63, sub = lane & 15, r = part * 4 + lane / 16;
-    const int kvh = head / (a.H / a.G);
-    float* p = seq_rows(a, seq, s.slot) + ((int64_t)head * a.P + r) * 128 + 8 * sub;
-    float h[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) h[e] = 0.0f;
-    if (!fresh) load_f32<8>(p, h);
-    for (int64_t t = s.begin; t < s.end; ++t) {
-        float k[8], q[8], acc = 0.0f;
-        load_elems<DT, 8>(elem_ptr<DT>(a.k, t * a.ks + kvh * 128 + 8 * sub), k);
-        load_elems<DT, 8>(elem_ptr<DT>(a.q, t * a.qs + kvh * 128 + 8 * sub), q);
-        const float v = load_elem<DT>(a.v, t * a.vs + (int64_t)head * a.P + r);
-        const float lam = a.g ? (float)exp((double)a.g[t * a.gs + head]) : 1.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            h[e] = __builtin_fmaf(lam, h[e], v * k[e]);
-            acc = __builtin_fmaf(q[e], h[e], acc);
-        }
-        acc = group_sum<16>(acc);
-        if (sub == 0) store_elem<DT>(a.o, t * a.os + (int64_t)head * a.P + r, a.oscale * acc);
-    }
-    store_f32<8>(p, h);
-}
-
 
 // ---------------------------------------------------------------------------
 // bf16: chunks of 64 tokens on the matrix cores
@@ -281,17 +242,17 @@ __device__ __forceinline__ void write_decays(float g, int lane, double& after, H
     after += last;
 }
 
-#ifndef SSQ_LA_EARLY
-#define SSQ_LA_EARLY 1
-#endif
-#ifndef SSQ_LA_TERMS
-#define SSQ_LA_TERMS 2
-#endif
-constexpr int kTerms = SSQ_LA_TERMS;
-#ifndef SSQ_LA_STERMS
-#define SSQ_LA_STERMS 2
-#endif
-constexpr int kStateTerms = SSQ_LA_STERMS;
+enum { WHOLE = 0, PART_STATE = 1, PART_OUT = 2 };
+
+// Terms of bf16 that stand for an fp32 operand.  The state as S q reads it, where o is rounded to
+// bf16 in the end: two (one would add an error as large as that rounding).  The decayed values that
+// are added to a state which is kept: three, all 24 bits (two leave 2e-6 of the state, as much as
+// a chain of fp32 sums; 128 heads x 8192 tokens take 7% less time with them); two where the state
+// only serves to the end of a part.
+constexpr int kReadTerms = 2;
+template <int MODE>
+constexpr int write_terms() { return MODE == PART_OUT ? 2 : 3; }
+
 // a descriptor of the wave's: without the readfirstlanes the compiler would loop over its lanes' values
 __device__ __forceinline__ Rsrc wave_rsrc(const void* base, uint32_t bytes)
 {
@@ -299,8 +260,6 @@ __device__ __forceinline__ Rsrc wave_rsrc(const void* base, uint32_t bytes)
     const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)b), hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32));
     return make_rsrc((const void*)(((uint64_t)hi << 32) | lo), (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes));
 }
-
-enum { WHOLE = 0, PART_STATE = 1, PART_OUT = 2 };
 
 struct ChunkArgs {
     LinArgs a;
@@ -311,13 +270,55 @@ struct ChunkArgs {
     int blocks;         // column blocks
     int run, runs;      // blocks on an XCD together, and such runs in `blocks`
     int block_cols;     // columns of a head in a block: P or 128
-    int pair;           // heads in a block: 1 or 2
 };
 
 // the place of a sequence's first part among all parts: sequences follow each other, each ending in a part of its own
 __device__ __forceinline__ int64_t first_part(const ChunkArgs& c, int64_t begin, int seq)
 {
     return begin / c.part_tokens + seq;
+}
+
+// What a workgroup does: a block of columns of a sequence, or of a part of one.
+struct Work {
+    int block, item, seq, slot;
+    bool fresh;
+    int64_t begin, end; // tokens
+};
+
+template <int MODE>
+__device__ __forceinline__ bool find_work(const ChunkArgs& c, Work& w)
+{
+    const LinArgs& a = c.a;
+    // Workgroups go to the 8 XCDs in turn.  Runs of `run` blocks, which share keys, are dealt to
+    // the XCDs, so that an XCD's L2 reads those keys once.
+    const unsigned at = blockIdx.x / 8;
+    const unsigned deal = at / c.run * 8 + blockIdx.x % 8;
+    w.block = (int)(deal % c.runs * c.run + at % c.run);
+    w.item = (int)(deal / c.runs);
+    if (w.item >= c.items || w.block >= c.blocks) return false;
+    w.seq = w.item;
+    if constexpr (MODE != WHOLE) { // the last sequence whose first part is not behind the item
+        int lo = 0, hi = a.nseq - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            const SeqSpan m = seq_span_uniform(a, mid);
+            if (first_part(c, m.begin, mid) <= w.item) lo = mid;
+            else hi = mid - 1;
+        }
+        w.seq = lo;
+    }
+    const SeqSpan span = seq_span_uniform(a, w.seq);
+    w.slot = span.slot;
+    if (span.slot < 0) return false;
+    w.fresh = a.fresh && __builtin_amdgcn_readfirstlane((int)a.fresh[w.seq]);
+    w.begin = span.begin;
+    w.end = span.end;
+    if constexpr (MODE == WHOLE) return w.begin < w.end || w.fresh;
+    const int64_t part = (int64_t)w.item - first_part(c, span.begin, w.seq);
+    w.begin += part * c.part_tokens;
+    if (part < 0 || w.begin >= w.end) return false; // a place of no part
+    if (w.end > w.begin + c.part_tokens) w.end = w.begin + c.part_tokens;
+    return true;
 }
 
 // NTW tiles of 16 columns a wave, HEADS heads at most (2: the blocks of a pair)
@@ -328,36 +329,10 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
     const LinArgs& a = c.a;
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    // Workgroups go to the 8 XCDs in turn.  Runs of `run` blocks, which share keys, are dealt to
-    // the XCDs, so that an XCD's L2 reads those keys once.
-    const unsigned at = blockIdx.x / 8;
-    const unsigned deal = at / c.run * 8 + blockIdx.x % 8;
-    const unsigned block = deal % c.runs * c.run + at % c.run;
-    const int item = deal / c.runs;
-    if (item >= c.items || block >= (unsigned)c.blocks) return;
-    int seq = item;
-    if constexpr (MODE != WHOLE) { // the last sequence whose first part is not behind the item
-        int lo = 0, hi = a.nseq - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            const SeqSpan m = seq_span_uniform(a, mid);
-            if (first_part(c, m.begin, mid) <= item) lo = mid;
-            else hi = mid - 1;
-        }
-        seq = lo;
-    }
-    const SeqSpan span = seq_span_uniform(a, seq);
-    if (span.slot < 0) return;
-    const bool fresh = a.fresh && __builtin_amdgcn_readfirstlane((int)a.fresh[seq]);
-    int64_t begin = span.begin, end = span.end;
-    if constexpr (MODE == WHOLE) {
-        if (begin == end && !fresh) return;
-    } else {
-        const int64_t part = (int64_t)item - first_part(c, span.begin, seq);
-        begin += part * c.part_tokens;
-        if (part < 0 || begin >= end) return; // a place of no part
-        if (end > begin + c.part_tokens) end = begin + c.part_tokens;
-    }
+    Work work;
+    if (!find_work<MODE>(c, work)) return;
+    const int block = work.block, item = work.item, seq = work.seq;
+    const int64_t begin = work.begin, end = work.end;
     // columns: heads head0 .. head0 + nh - 1 from column p0 of each
     const int share = a.H / a.G;
     int head0, nh, p0;
@@ -395,14 +370,14 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
     f32x4 S[NTW][8]; // n-tile t: entries 32g + 4t .. 32g + 4t + 3 of column l16
     // A sequence's state is in rows, a part's as the registers hold it.
     float* rows = nullptr;
-    if constexpr (MODE == WHOLE) rows = seq_rows(a, seq, span.slot) + col0 * 128 + l16 * 128 + 32 * g;
+    if constexpr (MODE == WHOLE) rows = seq_rows(a, seq, work.slot) + col0 * 128 + l16 * 128 + 32 * g;
     else rows = c.part_state + ((int64_t)item * a.H * a.P + col0) * 128 + lane * 4;
     constexpr int kStep = MODE == WHOLE ? 4 : 256; // floats from one n-tile to the next
 #pragma unroll
     for (int x = 0; x < NTW; ++x) {
 #pragma unroll
         for (int t = 0; t < 8; ++t) S[x][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        if (have[x] && MODE != PART_STATE && !(MODE == WHOLE && fresh)) {
+        if (have[x] && MODE != PART_STATE && !(MODE == WHOLE && work.fresh)) {
 #pragma unroll
             for (int t = 0; t < 8; ++t) S[x][t] = *reinterpret_cast<const f32x4*>(rows + (col / 16 + x) * 2048 + t * kStep);
         }
@@ -471,7 +446,7 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
         }
         __syncthreads();
         const bool more = n + 1 < chunks;
-        if (SSQ_LA_EARLY && more) fetch(start(n + 1));
+        if (more) fetch(start(n + 1));
         if (dhead < HEADS && more) {
             make_decays(buf ^ 1);
             if (n + 2 < chunks) fetch_decays(start(n + 2));
@@ -518,7 +493,7 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
                 for (int x = 0; x < NTW; ++x)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) O[x][i] = mfma(hi[x], qq[ks & 1][i], O[x][i]);
-                if constexpr (kStateTerms == 2)
+                if constexpr (kReadTerms == 2)
 #pragma unroll
                     for (int x = 0; x < NTW; ++x)
 #pragma unroll
@@ -552,7 +527,6 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
             }
             __syncthreads(); // the scores are written
         }
-        if (!SSQ_LA_EARLY && more) fetch(start(n + 1));
         bf16x8 vf[NTW][2]; // this wave's columns of v: column l16, tokens 32*kb + 8g .. +7
 #pragma unroll
         for (int x = 0; x < NTW; ++x)
@@ -587,7 +561,7 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
                     __builtin_amdgcn_raw_buffer_store_b64(w4, bo, o_off[x] + i * 16 * o_row, 0, 0);
                 }
         }
-        // the state: decayed, and the chunk's writes with v's decay, as the sum of kTerms bf16
+        // the state: decayed, and the chunk's writes with v's decay, as a sum of bf16
         if (MODE == PART_OUT && !more) break; // the next part has its own
         if constexpr (MODE != PART_STATE) {
             const float change = sd[head].change;
@@ -612,7 +586,7 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
         };
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
-            bf16x8 w[NTW][kTerms];
+            bf16x8 w[NTW][write_terms<MODE>()];
             const float* od = &sd[head].out[kb * 32 + g * 8];
             const f32x4 o0 = *reinterpret_cast<const f32x4*>(od), o1 = *reinterpret_cast<const f32x4*>(od + 4);
             const float oe[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
@@ -624,7 +598,7 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
                     v.x *= oe[e];
                     v.y *= oe[e + 1];
 #pragma unroll
-                    for (int j = 0; j < kTerms; ++j) {
+                    for (int j = 0; j < write_terms<MODE>(); ++j) {
                         const bf16x2 h = to_bf16(v.x, v.y);
                         const f32x2 f = from_bf16(h);
                         w[x][j][e] = h.x;
@@ -638,7 +612,7 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
             for (int t = 0; t < 8; t += 2) {
                 const bf16x8 kf[2] = {k_frag(kb, t), k_frag(kb, t + 1)};
 #pragma unroll
-                for (int j = 0; j < kTerms; ++j)
+                for (int j = 0; j < write_terms<MODE>(); ++j)
 #pragma unroll
                     for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -656,6 +630,270 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
     }
     if constexpr (MODE == PART_STATE) {
         if (dhead < nh && lane == 0 && p0 == 0) c.part_decay[(int64_t)item * a.H + head0 + dhead] = decay_of(after);
+    }
+}
+
+
+// ---------------------------------------------------------------------------
+// fp32 and fp16: chunks of 32 tokens, every product on the fp32 matrix instruction
+// ---------------------------------------------------------------------------
+// The same mathematics with nothing rounded below fp32: bf16 products would need three terms of
+// each operand, six products and as many instructions to split them.  The instruction sums four
+// products at a sixteenth of the bf16 rate, so a chunk is half as long, which halves its scores.
+// A workgroup of four waves has 64 columns of one head; a lane's 32 state entries are 32g + 8r + t
+// of column l16, so that its key and query operands are 16-byte reads.
+constexpr int kWideChunk = 32;
+constexpr int kWidePitch = 132;     // floats of a row of 128 in LDS
+constexpr int kWideColPitch = 68;   // of 64
+constexpr int kWideScorePitch = 36; // of 32
+
+struct alignas(16) WideDecay {
+    float r[kWideChunk], rlo[kWideChunk]; // sums of g, in powers of two, along tiles of 16, as two floats
+    float row[kWideChunk];                // scale * exp2(r_i)
+    float col[16];                        // exp2(c_15 - c_j)
+    float in[kWideChunk];                 // scale * exp2(c_i)
+    float out[kWideChunk];                // exp2(c_last - c_i), in PART_STATE with what follows the chunk
+    float keep, change;
+};
+struct alignas(16) WideLds {
+    float q[kWideChunk][kWidePitch], k[kWideChunk][kWidePitch];
+    float v[kWideChunk][kWideColPitch];
+    float p[kWideChunk][kWideScorePitch];
+    WideDecay d[2];
+};
+
+__device__ __forceinline__ f32x4 mfma_f32(float a, float b, f32x4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+}
+
+template <int MODE, int DT>
+__global__ __launch_bounds__(256, 2) void k_linattn_wide(ChunkArgs c)
+{
+    using T = typename Elem<DT>::T;
+    constexpr int SIZE = sizeof(T), PER = 16 / SIZE; // elements in 16 bytes
+    __shared__ WideLds s;
+    const LinArgs& a = c.a;
+    Work work;
+    if (!find_work<MODE>(c, work)) return;
+    const int64_t begin = work.begin, end = work.end;
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int per_head = (a.P + 63) / 64;
+    const int head = work.block / per_head, p0 = work.block % per_head * 64;
+    const int cols = min(64, a.P - p0);            // a multiple of 16
+    const bool have = wave * 16 < cols;            // a wave without columns runs on zeros and stores nothing
+    const int64_t col0 = (int64_t)head * a.P + p0; // of v and o, and the row of the state
+    const int kvh = head / (a.H / a.G);
+    const T* qp = static_cast<const T*>(a.q) + kvh * 128;
+    const T* kp = static_cast<const T*>(a.k) + kvh * 128;
+    const T* vp = static_cast<const T*>(a.v) + col0;
+    T* op = static_cast<T*>(a.o) + col0;
+
+    f32x4 S[8]; // S[t][r]: entry 32g + 8r + t of column l16
+    float* rows = nullptr;
+    if constexpr (MODE == WHOLE) rows = seq_rows(a, work.seq, work.slot) + (col0 + wave * 16 + l16) * 128 + 32 * g;
+    else rows = c.part_state + ((int64_t)work.item * a.H * a.P + col0 + wave * 16) * 128 + lane * 4;
+    constexpr int kStep = MODE == WHOLE ? 4 : 256; // floats from four entries to the next four
+#pragma unroll
+    for (int t = 0; t < 8; ++t) S[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (have && MODE != PART_STATE && !(MODE == WHOLE && work.fresh)) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const f32x4 x = *reinterpret_cast<const f32x4*>(rows + u * kStep);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[u % 2 * 4 + e][u / 2] = x[e];
+        }
+    }
+
+    // rows of 128 (q, k) and of 64 (v) in pieces of 16 bytes
+    constexpr int QP = 128 / PER, QR = 256 / QP, NQ = kWideChunk / QR;
+    constexpr int VP = 64 / PER, VR = 256 / VP, NV = kWideChunk / VR;
+    const uint32_t qpiece = tid % QP, qrow = tid / QP, vpiece = tid % VP, vrow = tid / VP;
+    const uint32_t q_row = (uint32_t)a.qs * SIZE, k_row = (uint32_t)a.ks * SIZE, v_row = (uint32_t)a.vs * SIZE, o_row = (uint32_t)a.os * SIZE;
+    const uint32_t q_off = qrow * q_row + qpiece * 16, k_off = qrow * k_row + qpiece * 16;
+    constexpr uint32_t kNone = 0x80000000u; // behind every range
+    const uint32_t v_off = (int)(vpiece * PER) < cols ? vrow * v_row + vpiece * 16 : kNone;
+    const uint32_t o_off = have ? l16 * o_row + (wave * 16 + 4 * g) * SIZE : kNone;
+    u32x4 rq[NQ], rk[NQ], rv[NV];
+    float rg = 0.0f;
+    auto fetch = [&](int64_t t0) {
+        const uint32_t last = (uint32_t)(end - t0 < kWideChunk ? end - t0 : kWideChunk) - 1;
+        const Rsrc bq = wave_rsrc(qp + t0 * a.qs, last * q_row + 128 * SIZE);
+        const Rsrc bk = wave_rsrc(kp + t0 * a.ks, last * k_row + 128 * SIZE);
+        const Rsrc bv = wave_rsrc(vp + t0 * a.vs, last * v_row + cols * SIZE);
+        rg = 0.0f;
+        if (wave == 3 && a.g && lane < kWideChunk && t0 + lane < end) rg = a.g[(t0 + lane) * a.gs + head];
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+            if constexpr (MODE != PART_STATE) rq[i] = __builtin_amdgcn_raw_buffer_load_b128(bq, q_off + QR * i * q_row, 0, 0);
+            rk[i] = __builtin_amdgcn_raw_buffer_load_b128(bk, k_off + QR * i * k_row, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) rv[i] = __builtin_amdgcn_raw_buffer_load_b128(bv, v_off + VR * i * v_row, 0, 0);
+    };
+    auto put = [&](float* to, u32x4 w) { // 16 bytes as floats
+        if constexpr (DT == DT_FP32) {
+            *reinterpret_cast<u32x4*>(to) = w;
+        } else {
+            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                *reinterpret_cast<f32x4*>(to + 4 * i) = f32x4{to_f32<DT>(ws[2 * i] & 0xFFFFu), to_f32<DT>(ws[2 * i] >> 16),
+                                                              to_f32<DT>(ws[2 * i + 1] & 0xFFFFu), to_f32<DT>(ws[2 * i + 1] >> 16)};
+        }
+    };
+    // the last wave has no scores and makes the decays, a chunk's while the one before it is run
+    double after = 0.0; // PART_STATE runs from the last chunk to the first: the decay of those behind
+    auto decays = [&](int buf) {
+        if (wave != 3) return;
+        WideDecay& d = s.d[buf];
+        const double r = row_sums(log2_decay(rg)), sum = wave_sums(r), last = readlane_d(sum, 63);
+        if constexpr (MODE == PART_STATE) {
+            if (lane < kWideChunk) d.out[lane] = exp2_of(after + (last - sum));
+            after += last;
+        } else if (lane < kWideChunk) {
+            const float hi = (float)r;
+            d.r[lane] = hi;
+            d.rlo[lane] = (float)(r - (double)hi);
+            d.row[lane] = a.oscale * exp2_of(r);
+            if (lane < 16) d.col[lane] = exp2_of(readlane_d(sum, 15) - sum);
+            d.in[lane] = a.oscale * exp2_of(sum);
+            d.out[lane] = exp2_of(last - sum);
+            if (lane == 0) {
+                const float2 e = decay_of(last);
+                d.keep = e.x;
+                d.change = e.y;
+            }
+        }
+    };
+    const int64_t chunks = (end - begin + kWideChunk - 1) / kWideChunk;
+    auto start = [&](int64_t n) { return begin + (MODE == PART_STATE ? chunks - 1 - n : n) * kWideChunk; };
+    if (chunks > 0) { // an empty sequence has no row that a descriptor could end with
+        fetch(start(0));
+        decays(0);
+    }
+    int buf = 0;
+    for (int64_t n = 0; n < chunks; ++n, buf ^= 1) {
+        const int64_t t0 = start(n);
+        const WideDecay& d = s.d[buf];
+        __syncthreads(); // the previous chunk has been read
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+            if constexpr (MODE != PART_STATE) put(&s.q[qrow + QR * i][qpiece * PER], rq[i]);
+            put(&s.k[qrow + QR * i][qpiece * PER], rk[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) put(&s.v[vrow + VR * i][vpiece * PER], rv[i]);
+        __syncthreads();
+        const bool more = n + 1 < chunks;
+        if (more) fetch(start(n + 1));
+
+        f32x4 O[2]; // query tile i: columns 4g .. 4g+3, query l16
+        if constexpr (MODE != PART_STATE) {
+            // S q, and the scores of one tile: (queries, keys) = (0, 0), (1, 0), (1, 1) of the first three waves
+            const int qt = wave == 0 ? 0 : 1, kt = wave == 2 ? 1 : 0;
+            f32x4 A = {0.0f, 0.0f, 0.0f, 0.0f};
+            O[0] = O[1] = A;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int n0 = 32 * g + 8 * r + 4 * h;
+                    const f32x4 q0 = *reinterpret_cast<const f32x4*>(&s.q[l16][n0]);
+                    const f32x4 q1 = *reinterpret_cast<const f32x4*>(&s.q[16 + l16][n0]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        O[0] = mfma_f32(S[4 * h + e][r], q0[e], O[0]);
+                        O[1] = mfma_f32(S[4 * h + e][r], q1[e], O[1]);
+                    }
+                    if (wave < 3) { // rows keys, columns queries
+                        const f32x4 kk = *reinterpret_cast<const f32x4*>(&s.k[kt * 16 + l16][n0]);
+                        const f32x4 qq = qt ? q1 : q0;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) A = mfma_f32(kk[e], qq[e], A);
+                    }
+                }
+            if (wave < 3) {
+                const int qi = qt * 16 + l16, kj = kt * 16 + 4 * g;
+                f32x4 w;
+                if (qt == kt) {
+                    const f32x4 rj = *reinterpret_cast<const f32x4*>(&d.r[kj]), lj = *reinterpret_cast<const f32x4*>(&d.rlo[kj]);
+                    const float ri = d.r[qi], li = d.rlo[qi];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = kj + e <= qi ? A[e] * (a.oscale * __builtin_amdgcn_exp2f((ri - rj[e]) + (li - lj[e]))) : 0.0f;
+                } else {
+                    w = A * d.row[qi] * *reinterpret_cast<const f32x4*>(&d.col[kj]);
+                }
+                *reinterpret_cast<f32x4*>(&s.p[qi][kj]) = w;
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) O[i] *= d.in[i * 16 + l16];
+            __syncthreads(); // the scores are written
+        }
+        float vf[2][4]; // v of column l16, tokens 16h + 4g .. +3
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) vf[h][e] = s.v[16 * h + 4 * g + e][wave * 16 + l16];
+        if constexpr (MODE != PART_STATE) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int h = 0; h <= i; ++h) {
+                    const f32x4 p = *reinterpret_cast<const f32x4*>(&s.p[i * 16 + l16][16 * h + 4 * g]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) O[i] = mfma_f32(vf[h][e], p[e], O[i]);
+                }
+            const uint32_t last = (uint32_t)(end - t0 < kWideChunk ? end - t0 : kWideChunk) - 1;
+            const Rsrc bo = wave_rsrc(op + t0 * a.os, last * o_row + cols * SIZE);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if constexpr (DT == DT_FP32) {
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[i]), bo, o_off + i * 16 * o_row, 0, 0);
+                } else {
+                    typedef T t4 __attribute__((ext_vector_type(4)));
+                    const t4 w = {(T)O[i].x, (T)O[i].y, (T)O[i].z, (T)O[i].w};
+                    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, w), bo, o_off + i * 16 * o_row, 0, 0);
+                }
+            }
+        }
+        if (MODE == PART_OUT && !more) break; // the next part has its own state
+        if constexpr (MODE != PART_STATE) {
+            const float keep = d.keep, change = d.change;
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) S[t][r] = __builtin_fmaf(S[t][r], change, S[t][r] * keep);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const f32x4 od = *reinterpret_cast<const f32x4*>(&d.out[16 * h + 4 * g]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float w = vf[h][e] * od[e];
+                const float* kr = &s.k[16 * h + 4 * g + e][8 * l16];
+                const f32x4 k0 = *reinterpret_cast<const f32x4*>(kr), k1 = *reinterpret_cast<const f32x4*>(kr + 4);
+#pragma unroll
+                for (int t = 0; t < 8; ++t) S[t] = mfma_f32(t < 4 ? k0[t & 3] : k1[t & 3], w, S[t]);
+            }
+        }
+        if (more) decays(buf ^ 1);
+    }
+    if constexpr (MODE != PART_OUT) {
+        if (have) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                f32x4 x;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = S[u % 2 * 4 + e][u / 2];
+                *reinterpret_cast<f32x4*>(rows + u * kStep) = x;
+            }
+        }
+    }
+    if constexpr (MODE == PART_STATE) {
+        if (wave == 3 && lane == 0 && p0 == 0) c.part_decay[(int64_t)work.item * a.H + head] = decay_of(after);
     }
 }
 
@@ -708,34 +946,33 @@ __global__ __launch_bounds__(256) void k_linattn_join(ChunkArgs c, int64_t units
 // launch
 // ---------------------------------------------------------------------------
 struct ChunkPlan {
-    int blocks, block_cols, pair;
+    int blocks;
+    bool pair;       // bf16: a block is two heads that share keys
     int part_tokens; // 0: sequences are not split
     int64_t nparts;
 };
 
-// The columns of a block: two heads of up to 64 columns where they share keys, else up to 128 of
-// one head.
-static ChunkPlan chunk_plan(int nseq, int64_t tokens, int H, int G, int P, int num_cus)
+// The columns of a block: 64 of a head for fp32 and fp16; for bf16 128, of two heads of up to 64
+// columns where they share keys, else of one.  Sequences are split where they and the blocks do not
+// give every compute unit a workgroup, into as many parts as there can be workgroups at once, of
+// two chunks at least.  (24 ragged prompts of 32 heads, 384 workgroups whole: 103 us, split 162 us;
+// three prompts of 32 heads of 128, 96 workgroups whole: 94 us split for two workgroups a unit,
+// 106 us for one.)
+static ChunkPlan chunk_plan(int dtype, int nseq, int64_t tokens, int H, int G, int P, int num_cus)
 {
     ChunkPlan p;
-    const int share = H / G;
-    if (P <= 64 && share > 1) {
-        p.pair = 2;
-        p.block_cols = P;
-        p.blocks = G * ((share + 1) / 2);
-    } else {
-        p.pair = 1;
-        p.block_cols = P < 128 ? P : 128;
-        p.blocks = H * ((P + 127) / 128);
-    }
+    const int share = H / G, chunk = dtype == DT_BF16 ? kChunk : kWideChunk;
+    p.pair = dtype == DT_BF16 && P <= 64 && share > 1;
+    if (p.pair) p.blocks = G * ((share + 1) / 2);
+    else p.blocks = H * (dtype == DT_BF16 ? (P + 127) / 128 : (P + 63) / 64);
     p.part_tokens = 0;
     p.nparts = 0;
-    const int64_t chunks = (tokens + kChunk - 1) / kChunk;
+    const int64_t chunks = (tokens + chunk - 1) / chunk;
     const int64_t slots = 2 * (int64_t)num_cus; // workgroups at once
-    if (chunks > 2 && nseq * (int64_t)p.blocks < slots) {
+    if (chunks > 2 && nseq * (int64_t)p.blocks < num_cus) {
         int64_t per = (chunks * p.blocks + slots - 1) / slots;
         if (per < 2) per = 2;
-        p.part_tokens = (int)(per * kChunk);
+        p.part_tokens = (int)(per * chunk);
         p.nparts = tokens / p.part_tokens + nseq;
     }
     return p;
@@ -743,15 +980,23 @@ static ChunkPlan chunk_plan(int nseq, int64_t tokens, int H, int G, int P, int n
 
 static size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
+static size_t parts_bytes(const ChunkPlan& p, int H, int P)
+{
+    return (size_t)p.nparts * H * P * 512 + align256((size_t)p.nparts * H * sizeof(float2));
+}
+
 size_t linattn_workspace(int fmt, int nseq, int64_t tokens, int H, int G, int P, int num_cus)
 {
-    const ChunkPlan p = chunk_plan(nseq, tokens, H, G, P, num_cus);
-    const size_t rows = (size_t)H * P;
-    return (fmt == FP32 ? 0 : (size_t)nseq * rows * 512) + p.nparts * rows * 512 + align256(p.nparts * H * sizeof(float2));
+    size_t parts = 0; // of the type that takes most
+    for (int dtype : {DT_FP32, DT_BF16, DT_FP16}) {
+        const size_t n = parts_bytes(chunk_plan(dtype, nseq, tokens, H, G, P, num_cus), H, P);
+        if (n > parts) parts = n;
+    }
+    return (fmt == FP32 ? 0 : (size_t)nseq * H * P * 512) + parts;
 }
 
 template <int MODE>
-static hipError_t launch_chunk(ChunkArgs c, int64_t items, hipStream_t st)
+static hipError_t launch_chunk(int dtype, bool pair, ChunkArgs c, int64_t items, hipStream_t st)
 {
     const LinArgs& a = c.a;
     // all the blocks of a key head, fewer where that would leave XCDs without work
@@ -763,39 +1008,41 @@ static hipError_t launch_chunk(ChunkArgs c, int64_t items, hipStream_t st)
     c.runs = (c.blocks + c.run - 1) / c.run;
     const int64_t blocks = (items * c.runs + 7) / 8 * 8 * c.run;
     if (blocks > kMaxBlocks) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)blocks);
-    const dim3 wg(256);
-    const bool wide = c.pair * c.block_cols > 64;
-    if (c.pair == 2) {
-        if (wide) hipLaunchKernelGGL((k_linattn_chunk<MODE, 2, 2>), grid, wg, 0, st, c);
+    const dim3 grid((unsigned)blocks), wg(256);
+    if (dtype == DT_FP32) {
+        hipLaunchKernelGGL((k_linattn_wide<MODE, DT_FP32>), grid, wg, 0, st, c);
+    } else if (dtype == DT_FP16) {
+        hipLaunchKernelGGL((k_linattn_wide<MODE, DT_FP16>), grid, wg, 0, st, c);
+    } else if (pair) {
+        c.block_cols = a.P;
+        if (a.P > 32) hipLaunchKernelGGL((k_linattn_chunk<MODE, 2, 2>), grid, wg, 0, st, c);
         else hipLaunchKernelGGL((k_linattn_chunk<MODE, 1, 2>), grid, wg, 0, st, c);
     } else {
-        if (wide) hipLaunchKernelGGL((k_linattn_chunk<MODE, 2, 1>), grid, wg, 0, st, c);
+        c.block_cols = a.P < 128 ? a.P : 128;
+        if (a.P > 64) hipLaunchKernelGGL((k_linattn_chunk<MODE, 2, 1>), grid, wg, 0, st, c);
         else hipLaunchKernelGGL((k_linattn_chunk<MODE, 1, 1>), grid, wg, 0, st, c);
     }
     return hipGetLastError();
 }
 
-static hipError_t launch_chunks(const LinArgs& a, void* ws, int num_cus, hipStream_t st)
+static hipError_t launch_chunks(int dtype, const LinArgs& a, void* ws, int num_cus, hipStream_t st)
 {
-    const ChunkPlan p = chunk_plan(a.nseq, a.tokens, a.H, a.G, a.P, num_cus);
+    const ChunkPlan p = chunk_plan(dtype, a.nseq, a.tokens, a.H, a.G, a.P, num_cus);
     ChunkArgs c{};
     c.a = a;
     c.blocks = p.blocks;
-    c.block_cols = p.block_cols;
-    c.pair = p.pair;
-    if (p.part_tokens == 0) return launch_chunk<WHOLE>(c, a.nseq, st);
+    if (p.part_tokens == 0) return launch_chunk<WHOLE>(dtype, p.pair, c, a.nseq, st);
     c.part_tokens = p.part_tokens;
     c.part_state = static_cast<float*>(ws);
     c.part_decay = reinterpret_cast<float2*>(c.part_state + p.nparts * a.H * a.P * 128);
-    hipError_t e = launch_chunk<PART_STATE>(c, p.nparts, st);
+    hipError_t e = launch_chunk<PART_STATE>(dtype, p.pair, c, p.nparts, st);
     if (e != hipSuccess) return e;
     const int64_t units = (int64_t)a.nseq * a.H * a.P * 32, blocks = (units + 255) / 256;
     if (blocks > kMaxBlocks) return hipErrorInvalidValue;
     hipLaunchKernelGGL(k_linattn_join, dim3((unsigned)blocks), dim3(256), 0, st, c, units);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    return launch_chunk<PART_OUT>(c, p.nparts, st);
+    return launch_chunk<PART_OUT>(dtype, p.pair, c, p.nparts, st);
 }
 
 template <int F>
@@ -832,16 +1079,7 @@ hipError_t launch_linattn_prefill(int fmt, int dtype, const LinArgs& args, void*
     }
     hipError_t e = state_rows(fmt, a, false, st);
     if (e != hipSuccess) return e;
-    const int64_t units = (int64_t)a.nseq * a.H * a.P / 4, blocks = (units + 3) / 4;
-    if (blocks > kMaxBlocks) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)blocks), wg(256);
-    switch (dtype) {
-    case DT_FP32: hipLaunchKernelGGL(k_linattn_scan<DT_FP32>, grid, wg, 0, st, a, units); break;
-    case DT_BF16: e = launch_chunks(a, ws, num_cus, st); break;
-    case DT_FP16: hipLaunchKernelGGL(k_linattn_scan<DT_FP16>, grid, wg, 0, st, a, units); break;
-    default: return hipErrorInvalidValue;
-    }
-    if (e == hipSuccess) e = hipGetLastError();
+    e = launch_chunks(dtype, a, ws, num_cus, st);
     if (e != hipSuccess) return e;
     return state_rows(fmt, a, true, st);
 }
