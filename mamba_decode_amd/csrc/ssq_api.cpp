@@ -552,8 +552,8 @@ static ssq_status fill_linattn(ssq_state* st, const ssq_linattn_io* io, int32_t 
 size_t ssq_linattn_workspace(const ssq_state* st, int32_t nseq, int64_t tokens)
 {
     if (!st || st->desc.kind != SSQ_MAMBA2 || nseq < 0 || tokens < 0) return (size_t)-1;
-    return ssq::linattn_workspace(st->desc.format, nseq, tokens, st->desc.nheads, st->desc.ngroups,
-                                  st->desc.rows_per_head, num_cus(st->device));
+    return ssq::linattn_workspace(st->desc.format, nseq, tokens, st->desc.nheads, st->desc.rows_per_head,
+                                  num_cus(st->device));
 }
 
 ssq_status ssq_linattn_prefill(ssq_state* st, const ssq_linattn_io* io, int32_t nseq, int64_t tokens,

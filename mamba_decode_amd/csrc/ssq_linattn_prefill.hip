@@ -1,6 +1,8 @@
 // ssq_linattn_prefill.hip -- linear attention with a decay for each head over ragged prompts,
 // gfx950: chunks of tokens on the matrix cores, bf16 products for bf16 tensors and fp32 products
 // for fp32 and fp16 ones.
+#include <cstddef>
+
 #include "ssq_ops_device.h"
 
 namespace ssq {
@@ -86,20 +88,20 @@ __device__ __forceinline__ float* seq_rows(const LinArgs& a, int seq, int slot)
 // With c_i the sum of a chunk's g up to token i, S the state before it:
 //   o_i = scale * (exp(c_i) S q_i + sum_{j<=i} exp(c_i - c_j) (q_i.k_j) v_j)
 //   S'  = exp(c_last) S + sum_j (exp(c_last - c_j) v_j) k_j^T
-// Every exponent is a difference that is not positive, so nothing overflows; the sums c are taken
-// in double and kept as two floats, so that the difference of two far-decayed tokens is exact.
+// Every exponent is a difference that is not positive, so nothing overflows; sums of g are taken
+// in double, since they are subtracted from each other.
 //
-// A workgroup of four waves runs one span of tokens for up to 128 value columns that share keys:
-// two heads of 64, or one of 128.  A wave owns columns in tiles of 16 and keeps their state,
-// 16 x 128 fp32, in registers, laid out as a matrix product leaves it: lane (g, c) = (lane/16,
-// lane%16) holds column c and the key entries 32g .. 32g+31, which is at once the operand of the
-// next S q (any order of the summed index serves, if both operands have it).  Scores are
-// computed once for the heads that share keys and meet the waves through LDS, decayed per head.
+// A workgroup of four waves runs one span of tokens for 64 columns of one head.  A wave owns 16
+// of them and keeps their state, 16 x 128 fp32, in registers, laid out as a matrix product leaves
+// it: lane (g, c) = (lane/16, lane%16) holds column c and the key entries 32g .. 32g+31, which is
+// at once the operand of the next S q (any order of the summed index serves, if both operands
+// have it).  Each wave also has the scores of 16 keys; they meet the other waves through LDS.
 constexpr int kChunk = 64;
-constexpr int kPitch = 136;  // bf16 of a row of 128 in LDS: 16-byte reads of 8 rows fall in different banks
-constexpr int kScorePitch = 72;
+constexpr int kCols = 64;
+constexpr int kPitch = 136;      // bf16 of a row of 128 in LDS: 16-byte reads of 16 rows fall in different banks
+constexpr int kColPitch = 72;    // the same of a row of 64 ...
+constexpr int kScorePitch = 40;  // ... and of 32
 constexpr double kLog2e = 1.4426950408889634;
-
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
@@ -135,22 +137,30 @@ __device__ __forceinline__ f32x2 from_bf16(bf16x2 v)
     return f32x2{__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u)};
 }
 
-// Decays of one head over a chunk.  r_i is the sum of g, in powers of two, over the tokens of i's
-// tile of 16 up to i, c_i the sum over the chunk.
-struct alignas(16) HeadDecay {
-    float r[kChunk];       // r_i: scores of a tile on the diagonal decay by exp2(r_i - r_j) ...
-    float row[kChunk];     // ... and off it by scale * exp2(r_i) ...
-    float col[3][kChunk];  // ... times exp2(c - c_j) with c before the tiles 1, 2 and 3
-    float in[kChunk];      // scale * exp2(c_i)
-    float out[kChunk];     // exp2(c_last - c_i)
-    float keep, change;    // exp2(c_last) x = keep*x + change*x, keep 0 or 1: exact near 1
+// Decays of a chunk.  r_i is the sum of g, in powers of two, over the tokens of i's tile of 16 up
+// to i, c_i the sum over the chunk.
+struct alignas(16) ReadDecay {
+    float r[kChunk];   // r_i: scores of a tile on the diagonal decay by exp2(r_i - r_j) ...
+    float row[kChunk]; // ... and off it by scale * exp2(r_i) ...
+    float col[96];     // ... times exp2(c - c_j) with c before the tile of i: 16 keys for tile 1, 32 for 2, 48 for 3
+    float in[kChunk];  // scale * exp2(c_i)
+};
+struct alignas(16) WriteDecay {
+    float out[kChunk];  // exp2(c_last - c_i)
+    float keep, change; // exp2(c_last) x = keep*x + change*x, keep 0 or 1: exact near 1
 };
 
+// 52,928 bytes: three workgroups on a compute unit
 struct alignas(16) ChunkLds {
-    __bf16 q[kChunk][kPitch], k[kChunk][kPitch], v[kChunk][kPitch];
-    __bf16 p[2][kChunk][kScorePitch]; // decayed scores, [query][key]
-    HeadDecay d[2][2]; // of this chunk and the next
+    __bf16 k[kChunk][kPitch];
+    __bf16 v[kChunk][kColPitch];
+    WriteDecay w[2]; // of this chunk and the next
+    __bf16 q[kChunk][kPitch];
+    __bf16 p01[32][kScorePitch]; // decayed scores, [query][key]: the queries 0 .. 31 have no later keys
+    __bf16 p23[32][kColPitch];
+    ReadDecay d;
 };
+constexpr size_t kStateLds = offsetof(ChunkLds, q); // what the parts' own states take
 
 // exp2 of the double x, rounded to a few units of fp32 for any size of x
 __device__ __forceinline__ float exp2_of(double x)
@@ -167,6 +177,13 @@ __device__ __forceinline__ double add_dpp(double x)
     const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xF, true);
     const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xF, true);
     return x + __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+__device__ __forceinline__ double readlane_d(double x, int lane)
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane), hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
 // A decay of 2^c as keep*x + change*x.  From 1/2 up the change, exp(y) - 1 of y = c ln 2, is
@@ -188,13 +205,6 @@ __device__ __forceinline__ float2 decay_of(double c)
     return make_float2(near ? 1.0f : 0.0f, near ? __builtin_fmaf(p * y, y, y) : exp2_of(c));
 }
 
-__device__ __forceinline__ double readlane_d(double x, int lane)
-{
-    const uint64_t u = __builtin_bit_cast(uint64_t, x);
-    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane), hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
-    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
-}
-
 // the log decay g in powers of two: 2^-184 is 0 in fp32, and so is all that passes such a token
 __device__ __forceinline__ double log2_decay(float g)
 {
@@ -214,32 +224,27 @@ __device__ __forceinline__ double wave_sums(double r)
     return add_dpp<0x143, 0xC>(r); // lane 31 to rows 2 and 3
 }
 
-// one wave, lane = token of the chunk: g the token's log decay (0 behind the span's end)
-__device__ __forceinline__ void chunk_decays(float g, float scale, int lane, HeadDecay& d)
+// One wave's share of a chunk's decays; lane = token, g its log decay (0 behind the span's end).
+__device__ __forceinline__ void chunk_decays(int wave, float g, float scale, int lane, ReadDecay& d, WriteDecay& w)
 {
     const double r = row_sums(log2_decay(g)), c = wave_sums(r);
-    const double last = readlane_d(c, 63);
-    d.r[lane] = (float)r;
-    d.row[lane] = scale * __builtin_amdgcn_exp2f((float)r); // scores are rounded to bf16: a few units of fp32 do
+    if (wave == 0) {
+        d.r[lane] = (float)r;
+        d.row[lane] = scale * __builtin_amdgcn_exp2f((float)r); // scores are rounded to bf16: a few units of fp32 do
+    } else if (wave == 1) {
 #pragma unroll
-    for (int i = 0; i < 3; ++i) // not positive for the tokens that use it
-        d.col[i][lane] = __builtin_amdgcn_exp2f(fminf((float)(readlane_d(c, 16 * i + 15) - c), 0.0f));
-    d.in[lane] = scale * exp2_of(c);
-    d.out[lane] = exp2_of(last - c);
-    if (lane == 63) {
-        const float2 e = decay_of(c);
-        d.keep = e.x;
-        d.change = e.y;
+        for (int i = 0; i < 3; ++i)
+            if (lane < 16 * (i + 1)) d.col[8 * i * (i + 1) + lane] = __builtin_amdgcn_exp2f((float)(readlane_d(c, 16 * i + 15) - c));
+    } else if (wave == 2) {
+        d.in[lane] = scale * exp2_of(c);
+        if (lane == 63) {
+            const float2 e = decay_of(c);
+            w.keep = e.x;
+            w.change = e.y;
+        }
+    } else {
+        w.out[lane] = exp2_of(readlane_d(c, 63) - c);
     }
-}
-
-// the same where only the writes count: exp2 of what follows the token in the chunk, and `after` it
-__device__ __forceinline__ void write_decays(float g, int lane, double& after, HeadDecay& d)
-{
-    const double c = wave_sums(row_sums(log2_decay(g)));
-    const double last = readlane_d(c, 63);
-    d.out[lane] = exp2_of(after + (last - c));
-    after += last;
 }
 
 enum { WHOLE = 0, PART_STATE = 1, PART_OUT = 2 };
@@ -253,13 +258,6 @@ constexpr int kReadTerms = 2;
 template <int MODE>
 constexpr int write_terms() { return MODE == PART_OUT ? 2 : 3; }
 
-// a descriptor of the wave's: without the readfirstlanes the compiler would loop over its lanes' values
-__device__ __forceinline__ Rsrc wave_rsrc(const void* base, uint32_t bytes)
-{
-    const uint64_t b = (uint64_t)base;
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)b), hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32));
-    return make_rsrc((const void*)(((uint64_t)hi << 32) | lo), (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes));
-}
 
 struct ChunkArgs {
     LinArgs a;
@@ -269,13 +267,20 @@ struct ChunkArgs {
     int items;          // sequences, or parts at most
     int blocks;         // column blocks
     int run, runs;      // blocks on an XCD together, and such runs in `blocks`
-    int block_cols;     // columns of a head in a block: P or 128
 };
 
 // the place of a sequence's first part among all parts: sequences follow each other, each ending in a part of its own
 __device__ __forceinline__ int64_t first_part(const ChunkArgs& c, int64_t begin, int seq)
 {
     return begin / c.part_tokens + seq;
+}
+
+// a descriptor of the wave's: without the readfirstlanes the compiler would loop over its lanes' values
+__device__ __forceinline__ Rsrc wave_rsrc(const void* base, uint32_t bytes)
+{
+    const uint64_t b = (uint64_t)base;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)b), hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32));
+    return make_rsrc((const void*)(((uint64_t)hi << 32) | lo), (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes));
 }
 
 // What a workgroup does: a block of columns of a sequence, or of a part of one.
@@ -321,11 +326,11 @@ __device__ __forceinline__ bool find_work(const ChunkArgs& c, Work& w)
     return true;
 }
 
-// NTW tiles of 16 columns a wave, HEADS heads at most (2: the blocks of a pair)
-template <int MODE, int NTW, int HEADS>
-__global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
+template <int MODE>
+__global__ __launch_bounds__(256, MODE == PART_STATE ? 4 : 3) void k_linattn_chunk(ChunkArgs c)
 {
-    __shared__ ChunkLds s;
+    __shared__ alignas(16) uint8_t lds[MODE == PART_STATE ? kStateLds : sizeof(ChunkLds)];
+    ChunkLds& s = *reinterpret_cast<ChunkLds*>(lds);
     const LinArgs& a = c.a;
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -333,306 +338,246 @@ __global__ __launch_bounds__(256, 2) void k_linattn_chunk(ChunkArgs c)
     if (!find_work<MODE>(c, work)) return;
     const int block = work.block, item = work.item, seq = work.seq;
     const int64_t begin = work.begin, end = work.end;
-    // columns: heads head0 .. head0 + nh - 1 from column p0 of each
-    const int share = a.H / a.G;
-    int head0, nh, p0;
-    if constexpr (HEADS == 2) {
-        const int per_group = (share + 1) / 2;
-        head0 = block / per_group * share + block % per_group * 2;
-        nh = min(2, share - (int)(block % per_group) * 2);
-        p0 = 0;
-    } else {
-        const int per_head = (a.P + c.block_cols - 1) / c.block_cols;
-        head0 = block / per_head;
-        nh = 1;
-        p0 = block % per_head * c.block_cols;
-    }
-    const int head_tiles = min(c.block_cols, a.P - p0) / 16, tiles = nh * head_tiles;
-    const int64_t col0 = (int64_t)head0 * a.P + p0; // of v and o, and the row of the state
-    const int kvh = head0 / share;
+    const int per_head = (a.P + kCols - 1) / kCols;
+    const int head = block / per_head, p0 = block % per_head * kCols;
+    const int cols = min(kCols, a.P - p0);                 // a multiple of 16
+    const int64_t col0 = (int64_t)head * a.P + p0;         // of v and o, and the row of the state
+    const int kvh = head / (a.H / a.G);
+    const bool have = wave * 16 < cols;                    // a wave without columns runs on zeros and stores nothing
 
     const __bf16* qp = static_cast<const __bf16*>(a.q) + kvh * 128;
     const __bf16* kp = static_cast<const __bf16*>(a.k) + kvh * 128;
     const __bf16* vp = static_cast<const __bf16*>(a.v) + col0;
     __bf16* op = static_cast<__bf16*>(a.o) + col0;
 
-    // This wave's tiles: NTW next to each other in one head, `head` of the block, the first at
-    // `col` of the block's columns.  A tile that the head does not have runs on another's values
-    // and is not stored.
-    const int waves_per_head = (head_tiles + NTW - 1) / NTW;
-    const int head = HEADS == 2 && wave >= waves_per_head ? 1 : 0;
-    const int tile0 = (wave - head * waves_per_head) * NTW;
-    const int col = min(head * head_tiles + tile0, 8 - NTW) * 16;
-    bool have[NTW];
-#pragma unroll
-    for (int x = 0; x < NTW; ++x) have[x] = head < nh && tile0 + x < head_tiles;
-
-    f32x4 S[NTW][8]; // n-tile t: entries 32g + 4t .. 32g + 4t + 3 of column l16
-    // A sequence's state is in rows, a part's as the registers hold it.
+    // n-tile t: entries 32g + 4t .. 32g + 4t + 3 of column l16.  A sequence's state is in rows, a
+    // part's as the registers hold it.
+    f32x4 S[8];
     float* rows = nullptr;
-    if constexpr (MODE == WHOLE) rows = seq_rows(a, seq, work.slot) + col0 * 128 + l16 * 128 + 32 * g;
-    else rows = c.part_state + ((int64_t)item * a.H * a.P + col0) * 128 + lane * 4;
+    if constexpr (MODE == WHOLE) rows = seq_rows(a, seq, work.slot) + (col0 + wave * 16 + l16) * 128 + 32 * g;
+    else rows = c.part_state + ((int64_t)item * a.H * a.P + col0 + wave * 16) * 128 + lane * 4;
     constexpr int kStep = MODE == WHOLE ? 4 : 256; // floats from one n-tile to the next
 #pragma unroll
-    for (int x = 0; x < NTW; ++x) {
+    for (int t = 0; t < 8; ++t) S[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (have && MODE != PART_STATE && !(MODE == WHOLE && work.fresh)) {
 #pragma unroll
-        for (int t = 0; t < 8; ++t) S[x][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        if (have[x] && MODE != PART_STATE && !(MODE == WHOLE && work.fresh)) {
-#pragma unroll
-            for (int t = 0; t < 8; ++t) S[x][t] = *reinterpret_cast<const f32x4*>(rows + (col / 16 + x) * 2048 + t * kStep);
-        }
+        for (int t = 0; t < 8; ++t) S[t] = *reinterpret_cast<const f32x4*>(rows + t * kStep);
     }
     if constexpr (MODE != PART_STATE) { // the scores above the diagonal's tiles stay zero
-        for (int i = tid; i < (int)sizeof(s.p) / 4; i += 256) reinterpret_cast<uint32_t*>(s.p)[i] = 0;
+        constexpr int words = (sizeof(s.p01) + sizeof(s.p23)) / 4;
+        for (int i = tid; i < words; i += 256) reinterpret_cast<uint32_t*>(s.p01)[i] = 0;
     }
 
     // Tiles come and go through buffer descriptors that end with the span: rows behind it read 0
-    // and are not written.  16 pieces of 16 bytes a row.
-    const uint32_t piece = tid & 15, prow = tid >> 4;
+    // and are not written.  16 pieces of 16 bytes a row of q and k, 8 of v.
+    const uint32_t piece = tid & 15, prow = tid >> 4, vpiece = tid & 7, vrow = tid >> 3;
     const uint32_t q_row = (uint32_t)a.qs * 2, k_row = (uint32_t)a.ks * 2, v_row = (uint32_t)a.vs * 2, o_row = (uint32_t)a.os * 2;
     const uint32_t q_off = prow * q_row + piece * 16, k_off = prow * k_row + piece * 16;
-    const uint32_t v_off = piece * 8 < (uint32_t)tiles * 16 ? prow * v_row + piece * 16 : 0x80000000u; // no such column: 0
-    uint32_t o_off[NTW];
+    constexpr uint32_t kNone = 0x80000000u; // behind every range
+    const uint32_t v_off = (int)vpiece * 8 < cols ? vrow * v_row + vpiece * 16 : kNone;
+    const uint32_t o_off = have ? l16 * o_row + wave * 32 + 8 * g : kNone;
+    u32x4 rq[4], rk[4], rv[2];
+    float rg = 0.0f;
+    // offsets are added up where they are used: kept for the whole loop they would cost the registers that it lacks
+    auto here = [](uint32_t x) {
+        asm volatile("" : "+v"(x));
+        return x;
+    };
+    auto rows_of = [&](int64_t t0) { return (uint32_t)(end - t0 < kChunk ? end - t0 : kChunk) - 1; };
+    auto fetch_q = [&](int64_t t0) {
+        const Rsrc bq = wave_rsrc(qp + t0 * a.qs, rows_of(t0) * q_row + 256);
+        const uint32_t at = here(q_off);
 #pragma unroll
-    for (int x = 0; x < NTW; ++x) o_off[x] = have[x] ? l16 * o_row + (col + x * 16) * 2 + 8 * g : 0x80000000u;
-    u32x4 rq[4], rk[4], rv[4];
+        for (int i = 0; i < 4; ++i)
+            if constexpr (MODE != PART_STATE) rq[i] = __builtin_amdgcn_raw_buffer_load_b128(bq, at + 16 * i * q_row, 0, 0);
+    };
     auto fetch = [&](int64_t t0) {
-        const uint32_t last = (uint32_t)(end - t0 < kChunk ? end - t0 : kChunk) - 1;
-        const Rsrc bq = wave_rsrc(qp + t0 * a.qs, last * q_row + 256);
-        const Rsrc bk = wave_rsrc(kp + t0 * a.ks, last * k_row + 256);
-        const Rsrc bv = wave_rsrc(vp + t0 * a.vs, last * v_row + tiles * 32);
+        const Rsrc bk = wave_rsrc(kp + t0 * a.ks, rows_of(t0) * k_row + 256);
+        const Rsrc bv = wave_rsrc(vp + t0 * a.vs, rows_of(t0) * v_row + cols * 2);
+        const uint32_t k_at = here(k_off), v_at = here(v_off);
+        rg = 0.0f;
+        if (a.g && t0 + lane < end) rg = a.g[(t0 + lane) * a.gs + head];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if constexpr (MODE != PART_STATE) rq[i] = __builtin_amdgcn_raw_buffer_load_b128(bq, q_off + 16 * i * q_row, 0, 0);
-            rk[i] = __builtin_amdgcn_raw_buffer_load_b128(bk, k_off + 16 * i * k_row, 0, 0);
-            rv[i] = __builtin_amdgcn_raw_buffer_load_b128(bv, v_off + 16 * i * v_row, 0, 0);
+            rk[i] = __builtin_amdgcn_raw_buffer_load_b128(bk, k_at + 16 * i * k_row, 0, 0);
+            if (i < 2) rv[i] = __builtin_amdgcn_raw_buffer_load_b128(bv, v_at + 32 * i * v_row, 0, 0);
         }
     };
-    // The last waves, which have the fewest scores, make the decays of a head each, a chunk's
-    // while the chunk before it is run.
-    const int dhead = 3 - wave; // this wave's head, if there is such a one
-    float rg = 0.0f;
-    auto fetch_decays = [&](int64_t t0) {
-        rg = 0.0f;
-        if (dhead < nh && a.g && t0 + lane < end) rg = a.g[(t0 + lane) * a.gs + head0 + dhead];
+    // PART_STATE runs from the last chunk to the first, so that what is summed need not decay:
+    // `after` is the decay of the chunks behind.
+    double after = 0.0;
+    auto decays = [&](int buf) {
+        if constexpr (MODE == PART_STATE) {
+            const double sum = wave_sums(row_sums(log2_decay(rg))), last = readlane_d(sum, 63);
+            if (wave == 0) s.w[buf].out[lane] = exp2_of(after + (last - sum));
+            after += last;
+        } else {
+            chunk_decays(wave, rg, a.oscale, lane, s.d, s.w[buf]);
+        }
     };
-    double after = 0.0; // PART_STATE: the decays of the chunks behind
-    auto make_decays = [&](int buf) {
-        if constexpr (MODE == PART_STATE) write_decays(rg, lane, after, s.d[buf][dhead]);
-        else chunk_decays(rg, a.oscale, lane, s.d[buf][dhead]);
-    };
-    // PART_STATE runs from the last chunk to the first, so that what is summed need not decay
     const int64_t chunks = (end - begin + kChunk - 1) / kChunk;
     auto start = [&](int64_t n) { return begin + (MODE == PART_STATE ? chunks - 1 - n : n) * kChunk; };
     if (chunks > 0) { // an empty sequence has no row that a descriptor could end with
         fetch(start(0));
-        if (dhead < HEADS) {
-            fetch_decays(start(0));
-            make_decays(0);
-            if (chunks > 1) fetch_decays(start(1));
-        }
+        fetch_q(start(0));
+        decays(0);
     }
     int buf = 0;
     for (int64_t n = 0; n < chunks; ++n, buf ^= 1) {
         const int64_t t0 = start(n);
-        const HeadDecay* const sd = s.d[buf];
+        const WriteDecay& sw = s.w[buf];
         __syncthreads(); // the previous chunk has been read
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int r = prow + 16 * i;
-            if constexpr (MODE != PART_STATE) *reinterpret_cast<u32x4*>(&s.q[r][piece * 8]) = rq[i];
-            *reinterpret_cast<u32x4*>(&s.k[r][piece * 8]) = rk[i];
-            *reinterpret_cast<u32x4*>(&s.v[r][piece * 8]) = rv[i];
+            if constexpr (MODE != PART_STATE) *reinterpret_cast<u32x4*>(&s.q[prow + 16 * i][piece * 8]) = rq[i];
+            *reinterpret_cast<u32x4*>(&s.k[prow + 16 * i][piece * 8]) = rk[i];
+            if (i < 2) *reinterpret_cast<u32x4*>(&s.v[vrow + 32 * i][vpiece * 8]) = rv[i];
         }
         __syncthreads();
         const bool more = n + 1 < chunks;
         if (more) fetch(start(n + 1));
-        if (dhead < HEADS && more) {
-            make_decays(buf ^ 1);
-            if (n + 2 < chunks) fetch_decays(start(n + 2));
-        }
 
-        f32x4 O[NTW][4]; // query tile i: columns of this tile 4g .. 4g+3, query l16
+        f32x4 O[4]; // query tile i: columns 4g .. 4g+3, query l16
         if constexpr (MODE != PART_STATE) {
-            // S q, the state as the sum of two bf16, and the scores of this wave's 16 keys, which use
-            // the same fragments of q (rows keys, columns queries; those above the diagonal for nothing)
+            // S q, the state as a sum of bf16, and the scores of this wave's 16 keys, which use the
+            // same fragments of q (rows keys, columns queries; those above the diagonal for nothing)
             f32x4 A[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                A[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int x = 0; x < NTW; ++x) O[x][i] = A[i];
-            }
-            bf16x8 qq[2][4], kk[2];
-            auto read_q = [&](int ks) {
-                kk[ks & 1] = *reinterpret_cast<const bf16x8*>(&s.k[wave * 16 + l16][g * 32 + ks * 8]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) qq[ks & 1][i] = *reinterpret_cast<const bf16x8*>(&s.q[i * 16 + l16][g * 32 + ks * 8]);
-            };
-            read_q(0);
+            for (int i = 0; i < 4; ++i) A[i] = O[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
-                if (ks < 3) read_q(ks + 1);
-                bf16x8 hi[NTW], lo[NTW];
+                __builtin_amdgcn_sched_barrier(0); // one step's fragments at a time: more would not fit the registers
+                const bf16x8 kk = *reinterpret_cast<const bf16x8*>(&s.k[wave * 16 + l16][g * 32 + ks * 8]);
+                bf16x8 qq[4];
 #pragma unroll
-                for (int x = 0; x < NTW; ++x)
-#pragma unroll
-                    for (int e = 0; e < 8; e += 2) {
-                        const float v0 = S[x][2 * ks + e / 4][e % 4], v1 = S[x][2 * ks + e / 4][e % 4 + 1];
-                        const bf16x2 h = to_bf16(v0, v1);
-                        const f32x2 f = from_bf16(h);
-                        const bf16x2 l = to_bf16(v0 - f.x, v1 - f.y);
-                        hi[x][e] = h.x;
-                        hi[x][e + 1] = h.y;
-                        lo[x][e] = l.x;
-                        lo[x][e + 1] = l.y;
-                    }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) A[i] = mfma(kk[ks & 1], qq[ks & 1][i], A[i]);
-#pragma unroll
-                for (int x = 0; x < NTW; ++x)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) O[x][i] = mfma(hi[x], qq[ks & 1][i], O[x][i]);
-                if constexpr (kReadTerms == 2)
-#pragma unroll
-                    for (int x = 0; x < NTW; ++x)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) O[x][i] = mfma(lo[x], qq[ks & 1][i], O[x][i]);
-            }
-            const int kj = wave * 16 + g * 4;
-#pragma unroll
-            for (int h = 0; h < HEADS; ++h)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int qi = i * 16 + l16;
-                    f32x4 w;
-                    if (i < wave) continue;
-                    if (i == wave) {
-                        const f32x4 rj = *reinterpret_cast<const f32x4*>(&sd[h].r[kj]);
-                        const float ri = sd[h].r[qi];
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            w[r] = A[i][r] * (a.oscale * __builtin_amdgcn_exp2f(kj + r <= qi ? ri - rj[r] : -1000.0f));
-                    } else {
-                        w = A[i] * sd[h].row[qi] * *reinterpret_cast<const f32x4*>(&sd[h].col[i == 0 ? 0 : i - 1][kj]);
-                    }
-                    const bf16x2 w01 = to_bf16(w.x, w.y), w23 = to_bf16(w.z, w.w);
-                    *reinterpret_cast<bf16x4*>(&s.p[h][qi][kj]) = __builtin_shufflevector(w01, w23, 0, 1, 2, 3);
-                }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float in = sd[head].in[i * 16 + l16];
-#pragma unroll
-                for (int x = 0; x < NTW; ++x) O[x][i] *= in;
-            }
-            __syncthreads(); // the scores are written
-        }
-        bf16x8 vf[NTW][2]; // this wave's columns of v: column l16, tokens 32*kb + 8g .. +7
-#pragma unroll
-        for (int x = 0; x < NTW; ++x)
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb) {
-                const int vcol = col + x * 16 + 4 * (l16 & 3);
-                const int row = kb * 32 + g * 8 + (l16 >> 2);
-                vf[x][kb] = join4(lds_read_tr(&s.v[row][vcol]), lds_read_tr(&s.v[row + 4][vcol]));
-            }
-        if constexpr (MODE != PART_STATE) {
-            const uint32_t last = (uint32_t)(end - t0 < kChunk ? end - t0 : kChunk) - 1;
-            const Rsrc bo = wave_rsrc(op + t0 * a.os, last * o_row + tiles * 32);
-            bf16x8 pf[6];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) pf[i] = *reinterpret_cast<const bf16x8*>(&s.p[head][i * 16 + l16][g * 8]);
-#pragma unroll
-            for (int i = 2; i < 4; ++i) pf[2 + i] = *reinterpret_cast<const bf16x8*>(&s.p[head][i * 16 + l16][32 + g * 8]);
-#pragma unroll
-            for (int x = 0; x < NTW; ++x)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) O[x][i] = mfma(vf[x][0], pf[i], O[x][i]);
-#pragma unroll
-            for (int x = 0; x < NTW; ++x)
-#pragma unroll
-                for (int i = 2; i < 4; ++i) O[x][i] = mfma(vf[x][1], pf[2 + i], O[x][i]);
-#pragma unroll
-            for (int x = 0; x < NTW; ++x)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const f32x4 w = O[x][i];
-                    const u32x2 w4 = {__builtin_bit_cast(uint32_t, to_bf16(w.x, w.y)), __builtin_bit_cast(uint32_t, to_bf16(w.z, w.w))};
-                    __builtin_amdgcn_raw_buffer_store_b64(w4, bo, o_off[x] + i * 16 * o_row, 0, 0);
-                }
-        }
-        // the state: decayed, and the chunk's writes with v's decay, as a sum of bf16
-        if (MODE == PART_OUT && !more) break; // the next part has its own
-        if constexpr (MODE != PART_STATE) {
-            const float change = sd[head].change;
-            if (__builtin_amdgcn_readfirstlane(__float_as_int(sd[head].keep)) != 0) {
-#pragma unroll
-                for (int x = 0; x < NTW; ++x)
-#pragma unroll
-                    for (int t = 0; t < 8; ++t)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) S[x][t][r] = __builtin_fmaf(S[x][t][r], change, S[x][t][r]);
-            } else {
-#pragma unroll
-                for (int x = 0; x < NTW; ++x)
-#pragma unroll
-                    for (int t = 0; t < 8; ++t) S[x][t] *= change;
-            }
-        }
-        const int krow = g * 8 + (l16 >> 2), kcol = (l16 & 3) * 32;
-        auto k_frag = [&](int kb, int t) {
-            const int row = kb * 32 + krow, n = kcol + t * 4;
-            return join4(lds_read_tr(&s.k[row][n]), lds_read_tr(&s.k[row + 4][n]));
-        };
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            bf16x8 w[NTW][write_terms<MODE>()];
-            const float* od = &sd[head].out[kb * 32 + g * 8];
-            const f32x4 o0 = *reinterpret_cast<const f32x4*>(od), o1 = *reinterpret_cast<const f32x4*>(od + 4);
-            const float oe[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
-#pragma unroll
-            for (int x = 0; x < NTW; ++x) {
+                for (int i = 0; i < 4; ++i) qq[i] = *reinterpret_cast<const bf16x8*>(&s.q[i * 16 + l16][g * 32 + ks * 8]);
+                bf16x8 term[kReadTerms];
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
-                    f32x2 v = from_bf16(bf16x2{vf[x][kb][e], vf[x][kb][e + 1]});
-                    v.x *= oe[e];
-                    v.y *= oe[e + 1];
+                    f32x2 v = {S[2 * ks + e / 4][e % 4], S[2 * ks + e / 4][e % 4 + 1]};
 #pragma unroll
-                    for (int j = 0; j < write_terms<MODE>(); ++j) {
+                    for (int j = 0; j < kReadTerms; ++j) {
                         const bf16x2 h = to_bf16(v.x, v.y);
                         const f32x2 f = from_bf16(h);
-                        w[x][j][e] = h.x;
-                        w[x][j][e + 1] = h.y;
+                        term[j][e] = h.x;
+                        term[j][e + 1] = h.y;
                         v.x -= f.x;
                         v.y -= f.y;
                     }
                 }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) A[i] = mfma(kk, qq[i], A[i]);
+#pragma unroll
+                for (int j = 0; j < kReadTerms; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) O[i] = mfma(term[j], qq[i], O[i]);
+            }
+            const int kj = wave * 16 + g * 4;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int qi = i * 16 + l16;
+                f32x4 w;
+                if (i < wave) continue;
+                if (i == wave) {
+                    const f32x4 rj = *reinterpret_cast<const f32x4*>(&s.d.r[kj]);
+                    const float ri = s.d.r[qi];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        w[r] = A[i][r] * (a.oscale * __builtin_amdgcn_exp2f(kj + r <= qi ? ri - rj[r] : -1000.0f));
+                } else {
+                    w = A[i] * s.d.row[qi] * *reinterpret_cast<const f32x4*>(&s.d.col[8 * i * (i - 1) + kj]);
+                }
+                const bf16x2 w01 = to_bf16(w.x, w.y), w23 = to_bf16(w.z, w.w);
+                __bf16* const p = i < 2 ? &s.p01[qi][kj] : &s.p23[qi - 32][kj];
+                *reinterpret_cast<bf16x4*>(p) = __builtin_shufflevector(w01, w23, 0, 1, 2, 3);
             }
 #pragma unroll
-            for (int t = 0; t < 8; t += 2) {
-                const bf16x8 kf[2] = {k_frag(kb, t), k_frag(kb, t + 1)};
+            for (int i = 0; i < 4; ++i) O[i] *= s.d.in[i * 16 + l16];
+            __syncthreads(); // the scores are written, and the decays that they took are read
+        }
+        if (more) fetch_q(start(n + 1)); // not sooner: its registers are S q's operands till here
+        bf16x8 vf[2]; // this wave's columns of v: column l16, tokens 32*kb + 8g .. +7
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            const int row = kb * 32 + g * 8 + (l16 >> 2), col = wave * 16 + 4 * (l16 & 3);
+            vf[kb] = join4(lds_read_tr(&s.v[row][col]), lds_read_tr(&s.v[row + 4][col]));
+        }
+        if constexpr (MODE != PART_STATE) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                O[i] = mfma(vf[0], *reinterpret_cast<const bf16x8*>(i < 2 ? &s.p01[i * 16 + l16][g * 8] : &s.p23[i * 16 - 32 + l16][g * 8]), O[i]);
+#pragma unroll
+            for (int i = 2; i < 4; ++i)
+                O[i] = mfma(vf[1], *reinterpret_cast<const bf16x8*>(&s.p23[i * 16 - 32 + l16][32 + g * 8]), O[i]);
+            const uint32_t last = (uint32_t)(end - t0 < kChunk ? end - t0 : kChunk) - 1;
+            const Rsrc bo = wave_rsrc(op + t0 * a.os, last * o_row + cols * 2);
+            const uint32_t o_at = here(o_off);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const u32x2 w4 = {__builtin_bit_cast(uint32_t, to_bf16(O[i].x, O[i].y)), __builtin_bit_cast(uint32_t, to_bf16(O[i].z, O[i].w))};
+                __builtin_amdgcn_raw_buffer_store_b64(w4, bo, o_at + i * 16 * o_row, 0, 0);
+            }
+        }
+        if (MODE == PART_OUT && !more) break; // the next part has its own state
+        // the state: decayed, and the chunk's writes with v's decay, as a sum of bf16
+        if constexpr (MODE != PART_STATE) {
+            const float change = sw.change;
+            if (__builtin_amdgcn_readfirstlane(__float_as_int(sw.keep)) != 0) {
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) S[t][r] = __builtin_fmaf(S[t][r], change, S[t][r]);
+            } else {
+#pragma unroll
+                for (int t = 0; t < 8; ++t) S[t] *= change;
+            }
+        }
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            const float* od = &sw.out[kb * 32 + g * 8];
+            const f32x4 o0 = *reinterpret_cast<const f32x4*>(od), o1 = *reinterpret_cast<const f32x4*>(od + 4);
+            const float oe[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
+            bf16x8 term[write_terms<MODE>()];
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                f32x2 v = from_bf16(bf16x2{vf[kb][e], vf[kb][e + 1]});
+                v.x *= oe[e];
+                v.y *= oe[e + 1];
+#pragma unroll
+                for (int j = 0; j < write_terms<MODE>(); ++j) {
+                    const bf16x2 h = to_bf16(v.x, v.y);
+                    const f32x2 f = from_bf16(h);
+                    term[j][e] = h.x;
+                    term[j][e + 1] = h.y;
+                    v.x -= f.x;
+                    v.y -= f.y;
+                }
+            }
+            const int row = kb * 32 + g * 8 + (l16 >> 2), col = (l16 & 3) * 32;
+#pragma unroll
+            for (int t = 0; t < 8; t += 4) {
+                bf16x8 kf[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    kf[u] = join4(lds_read_tr(&s.k[row][col + 4 * (t + u)]), lds_read_tr(&s.k[row + 4][col + 4 * (t + u)]));
 #pragma unroll
                 for (int j = 0; j < write_terms<MODE>(); ++j)
 #pragma unroll
-                    for (int u = 0; u < 2; ++u)
-#pragma unroll
-                        for (int x = 0; x < NTW; ++x) S[x][t + u] = mfma(kf[u], w[x][j], S[x][t + u]);
+                    for (int u = 0; u < 4; ++u) S[t + u] = mfma(kf[u], term[j], S[t + u]);
             }
         }
+        if (more) decays(buf ^ 1);
     }
     if constexpr (MODE != PART_OUT) {
+        if (have) {
 #pragma unroll
-        for (int x = 0; x < NTW; ++x)
-            if (have[x]) {
-#pragma unroll
-                for (int t = 0; t < 8; ++t) *reinterpret_cast<f32x4*>(rows + (col / 16 + x) * 2048 + t * kStep) = S[x][t];
-            }
+            for (int t = 0; t < 8; ++t) *reinterpret_cast<f32x4*>(rows + t * kStep) = S[t];
+        }
     }
     if constexpr (MODE == PART_STATE) {
-        if (dhead < nh && lane == 0 && p0 == 0) c.part_decay[(int64_t)item * a.H + head0 + dhead] = decay_of(after);
+        if (tid == 0 && p0 == 0) c.part_decay[(int64_t)item * a.H + head] = decay_of(after);
     }
 }
-
 
 // ---------------------------------------------------------------------------
 // fp32 and fp16: chunks of 32 tokens, every product on the fp32 matrix instruction
@@ -679,9 +624,9 @@ __global__ __launch_bounds__(256, 2) void k_linattn_wide(ChunkArgs c)
     const int64_t begin = work.begin, end = work.end;
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int per_head = (a.P + 63) / 64;
-    const int head = work.block / per_head, p0 = work.block % per_head * 64;
-    const int cols = min(64, a.P - p0);            // a multiple of 16
+    const int per_head = (a.P + kCols - 1) / kCols;
+    const int head = work.block / per_head, p0 = work.block % per_head * kCols;
+    const int cols = min(kCols, a.P - p0);         // a multiple of 16
     const bool have = wave * 16 < cols;            // a wave without columns runs on zeros and stores nothing
     const int64_t col0 = (int64_t)head * a.P + p0; // of v and o, and the row of the state
     const int kvh = head / (a.H / a.G);
@@ -946,29 +891,25 @@ __global__ __launch_bounds__(256) void k_linattn_join(ChunkArgs c, int64_t units
 // launch
 // ---------------------------------------------------------------------------
 struct ChunkPlan {
-    int blocks;
-    bool pair;       // bf16: a block is two heads that share keys
+    int blocks;      // of 64 columns of a head
     int part_tokens; // 0: sequences are not split
     int64_t nparts;
 };
 
-// The columns of a block: 64 of a head for fp32 and fp16; for bf16 128, of two heads of up to 64
-// columns where they share keys, else of one.  Sequences are split where they and the blocks do not
-// give every compute unit a workgroup, into as many parts as there can be workgroups at once, of
-// two chunks at least.  (24 ragged prompts of 32 heads, 384 workgroups whole: 103 us, split 162 us;
-// three prompts of 32 heads of 128, 96 workgroups whole: 94 us split for two workgroups a unit,
-// 106 us for one.)
-static ChunkPlan chunk_plan(int dtype, int nseq, int64_t tokens, int H, int G, int P, int num_cus)
+// Sequences are split where they and the blocks do not give every compute unit a workgroup, into
+// as many parts as there can be workgroups at once, of two chunks at least.  (24 ragged bf16
+// prompts of 32 heads, 768 workgroups whole: 88 us; as 384 workgroups of twice the columns 99 us
+// whole and 162 us split.  Three prompts of 32 heads of 128, 192 workgroups whole: 94 us split for
+// three workgroups a unit, 104 us for two.)
+static ChunkPlan chunk_plan(int dtype, int nseq, int64_t tokens, int H, int P, int num_cus)
 {
     ChunkPlan p;
-    const int share = H / G, chunk = dtype == DT_BF16 ? kChunk : kWideChunk;
-    p.pair = dtype == DT_BF16 && P <= 64 && share > 1;
-    if (p.pair) p.blocks = G * ((share + 1) / 2);
-    else p.blocks = H * (dtype == DT_BF16 ? (P + 127) / 128 : (P + 63) / 64);
+    const int chunk = dtype == DT_BF16 ? kChunk : kWideChunk;
+    p.blocks = H * ((P + kCols - 1) / kCols);
     p.part_tokens = 0;
     p.nparts = 0;
     const int64_t chunks = (tokens + chunk - 1) / chunk;
-    const int64_t slots = 2 * (int64_t)num_cus; // workgroups at once
+    const int64_t slots = (dtype == DT_BF16 ? 3 : 2) * (int64_t)num_cus; // workgroups at once
     if (chunks > 2 && nseq * (int64_t)p.blocks < num_cus) {
         int64_t per = (chunks * p.blocks + slots - 1) / slots;
         if (per < 2) per = 2;
@@ -985,18 +926,18 @@ static size_t parts_bytes(const ChunkPlan& p, int H, int P)
     return (size_t)p.nparts * H * P * 512 + align256((size_t)p.nparts * H * sizeof(float2));
 }
 
-size_t linattn_workspace(int fmt, int nseq, int64_t tokens, int H, int G, int P, int num_cus)
+size_t linattn_workspace(int fmt, int nseq, int64_t tokens, int H, int P, int num_cus)
 {
     size_t parts = 0; // of the type that takes most
     for (int dtype : {DT_FP32, DT_BF16, DT_FP16}) {
-        const size_t n = parts_bytes(chunk_plan(dtype, nseq, tokens, H, G, P, num_cus), H, P);
+        const size_t n = parts_bytes(chunk_plan(dtype, nseq, tokens, H, P, num_cus), H, P);
         if (n > parts) parts = n;
     }
     return (fmt == FP32 ? 0 : (size_t)nseq * H * P * 512) + parts;
 }
 
 template <int MODE>
-static hipError_t launch_chunk(int dtype, bool pair, ChunkArgs c, int64_t items, hipStream_t st)
+static hipError_t launch_chunk(int dtype, ChunkArgs c, int64_t items, hipStream_t st)
 {
     const LinArgs& a = c.a;
     // all the blocks of a key head, fewer where that would leave XCDs without work
@@ -1013,36 +954,30 @@ static hipError_t launch_chunk(int dtype, bool pair, ChunkArgs c, int64_t items,
         hipLaunchKernelGGL((k_linattn_wide<MODE, DT_FP32>), grid, wg, 0, st, c);
     } else if (dtype == DT_FP16) {
         hipLaunchKernelGGL((k_linattn_wide<MODE, DT_FP16>), grid, wg, 0, st, c);
-    } else if (pair) {
-        c.block_cols = a.P;
-        if (a.P > 32) hipLaunchKernelGGL((k_linattn_chunk<MODE, 2, 2>), grid, wg, 0, st, c);
-        else hipLaunchKernelGGL((k_linattn_chunk<MODE, 1, 2>), grid, wg, 0, st, c);
     } else {
-        c.block_cols = a.P < 128 ? a.P : 128;
-        if (a.P > 64) hipLaunchKernelGGL((k_linattn_chunk<MODE, 2, 1>), grid, wg, 0, st, c);
-        else hipLaunchKernelGGL((k_linattn_chunk<MODE, 1, 1>), grid, wg, 0, st, c);
+        hipLaunchKernelGGL(k_linattn_chunk<MODE>, grid, wg, 0, st, c);
     }
     return hipGetLastError();
 }
 
 static hipError_t launch_chunks(int dtype, const LinArgs& a, void* ws, int num_cus, hipStream_t st)
 {
-    const ChunkPlan p = chunk_plan(dtype, a.nseq, a.tokens, a.H, a.G, a.P, num_cus);
+    const ChunkPlan p = chunk_plan(dtype, a.nseq, a.tokens, a.H, a.P, num_cus);
     ChunkArgs c{};
     c.a = a;
     c.blocks = p.blocks;
-    if (p.part_tokens == 0) return launch_chunk<WHOLE>(dtype, p.pair, c, a.nseq, st);
+    if (p.part_tokens == 0) return launch_chunk<WHOLE>(dtype, c, a.nseq, st);
     c.part_tokens = p.part_tokens;
     c.part_state = static_cast<float*>(ws);
     c.part_decay = reinterpret_cast<float2*>(c.part_state + p.nparts * a.H * a.P * 128);
-    hipError_t e = launch_chunk<PART_STATE>(dtype, p.pair, c, p.nparts, st);
+    hipError_t e = launch_chunk<PART_STATE>(dtype, c, p.nparts, st);
     if (e != hipSuccess) return e;
     const int64_t units = (int64_t)a.nseq * a.H * a.P * 32, blocks = (units + 255) / 256;
     if (blocks > kMaxBlocks) return hipErrorInvalidValue;
     hipLaunchKernelGGL(k_linattn_join, dim3((unsigned)blocks), dim3(256), 0, st, c, units);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    return launch_chunk<PART_OUT>(dtype, p.pair, c, p.nparts, st);
+    return launch_chunk<PART_OUT>(dtype, c, p.nparts, st);
 }
 
 template <int F>

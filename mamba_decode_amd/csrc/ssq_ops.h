@@ -54,7 +54,7 @@ struct ReorderPart {
 };
 
 hipError_t launch_linattn_step(int fmt, int dtype, const LinArgs& a, bool pre, hipStream_t st);
-size_t linattn_workspace(int fmt, int nseq, int64_t tokens, int H, int G, int P, int num_cus);
+size_t linattn_workspace(int fmt, int nseq, int64_t tokens, int H, int P, int num_cus);
 hipError_t launch_linattn_prefill(int fmt, int dtype, const LinArgs& a, void* ws, int num_cus, hipStream_t st);
 size_t beam_workspace(int batch, int beams, int vocab, int nselect);
 hipError_t launch_beam_select(int dtype, const BeamArgs& a, hipStream_t st);
