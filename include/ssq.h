@@ -323,14 +323,19 @@ ssq_status ssq_stream_copy(void *dst, const void *src, size_t bytes, void *strea
  * (-infinity forgets the state; NULL: no decay), with a stride of its own (0:
  * the same decay at every token).  q, k, v and o and their strides in bytes
  * are multiples of 16, no stride but g's is shorter than a token's row, and
- * none exceeds 2^23 elements.  o overlaps no input.  The state, every sum and every decay
- * are fp32 or wider; o is rounded once to `dtype`.
+ * none exceeds 2^23 elements.  o overlaps no input.  The state, every sum and
+ * every decay are fp32 or wider; o is rounded once to `dtype`.
  *
  * slots: device int32 [nseq], the sequence of the state (0 .. batch-1) that
  * sequence i of the call is, each at most once (twice: the state and outputs
  * of those are unspecified); a slot out of range skips the sequence, of which
  * nothing is read or written.  NULL: i, and nseq <= batch.  Sequences of the
  * state that no slot names are left as they are.  nseq = 0 is an empty call.
+ *
+ * A value of q, k, v or g that is not finite (g = -infinity apart) leaves the
+ * outputs of its call and the state unspecified for its sequence and head (of
+ * q and k: for the heads that share it), earlier tokens included; every other
+ * sequence and head is computed as usual.
  * ------------------------------------------------------------------------ */
 typedef enum { SSQ_DTYPE_FP32 = 0, SSQ_DTYPE_BF16 = 1, SSQ_DTYPE_FP16 = 2 } ssq_dtype;
 
@@ -350,7 +355,8 @@ typedef struct {
 } ssq_linattn_io;
 
 /* Bytes of device workspace ssq_linattn_prefill needs for these sizes (0: none);
- * (size_t)-1 if the state is NULL or a delta state, or a size is negative. */
+ * (size_t)-1 if the state is NULL or a delta state, or a size is negative or
+ * more than ssq_linattn_prefill takes. */
 size_t ssq_linattn_workspace(const ssq_state *state, int32_t nseq, int64_t tokens);
 
 /* Prompts, one after the other in `tokens` rows: sequence i has the tokens
@@ -365,11 +371,12 @@ size_t ssq_linattn_workspace(const ssq_state *state, int32_t nseq, int64_t token
  * rounded once, at the end (as ssq_prefill with one chunk; a stochastic
  * rounding draws the uniforms of the state's next token and advances it by
  * one).  o is read from the fp32 recurrence.
- * The tokens of a sequence are taken 64 at a time: products among them and
- * with the state run on the matrix cores; where sequences and heads are too
+ * The tokens of a sequence are taken 64 at a time (bf16) or 32 (fp32, fp16):
+ * products among them and with the state run on the matrix cores; where sequences and heads are too
  * few to fill the card, a sequence is split and its parts are joined by their
  * decays.  Results do not depend on other sequences of the call, but may
  * differ in rounding with the call's sizes.
+ * A call takes fewer than 2^31 - 128 tokens and nseq*nheads*P up to 2^26.
  * workspace: device memory of at least ssq_linattn_workspace() bytes, 256-byte
  * aligned, used by this call alone until the stream has passed it. */
 ssq_status ssq_linattn_prefill(ssq_state *state, const ssq_linattn_io *io, int32_t nseq, int64_t tokens,
@@ -380,7 +387,8 @@ ssq_status ssq_linattn_prefill(ssq_state *state, const ssq_linattn_io *io, int32
  * lambda = fl32(exp(g)) (in double, rounded once), each entry
  * h'_n = fma(lambda, h_n, fl(v_p*k_n)) on the reconstructed entry; a quantized
  * row is then refit and rounded (nearest, or stochastically as in
- * ssq_decode_step), and o is read from the new codes or from h' (`readout`). */
+ * ssq_decode_step), and o is read from the new codes or from h' (`readout`).
+ * nseq*nheads*P is 2^29 at most. */
 ssq_status ssq_linattn_step(ssq_state *state, const ssq_linattn_io *io, int32_t nseq, const int32_t *slots,
                             int32_t readout, void *stream);
 
@@ -407,8 +415,8 @@ size_t ssq_beam_workspace(const ssq_beam_desc *desc);
  *   scores[beam] + (x - m) - log(sum exp(x - m)),  m the beam's largest logit,
  * compared in double.  Candidates are ordered by descending score, of equal
  * ones the lower beam first, and within a beam by descending logit, of equal
- * ones the lower token first; they are written as scores [batch][nselect] (fp32), tokens and parents (the beam in 0 ..
- * beams-1) int32.  A logit of -infinity is no candidate, nor is any token of a
+ * ones the lower token first; they are written as scores [batch][nselect]
+ * (fp32), tokens and parents (the beam in 0 .. beams-1) int32.  A logit of -infinity is no candidate, nor is any token of a
  * beam with the score -infinity or with nothing but -infinity; NaN logits
  * count as -infinity.  A beam with finished[beam] != 0 (device uint8
  * [batch][beams]; NULL: none) has one candidate, pad_token with the beam's
@@ -417,7 +425,7 @@ size_t ssq_beam_workspace(const ssq_beam_desc *desc);
  * (place mod beams).  Scores or logits of +infinity and scores that are NaN
  * leave that request's outputs unspecified (parents stay in range).
  * logits: aligned to their element; the rest as named; workspace as for
- * ssq_linattn_prefill.  The outputs overlap no input. */
+ * ssq_linattn_prefill.  The outputs overlap no input; batch*beams < 2^24. */
 ssq_status ssq_beam_select(const ssq_beam_desc *desc, const void *logits, const float *scores,
                            const uint8_t *finished, float *out_scores, int32_t *out_tokens,
                            int32_t *out_parents, void *workspace, size_t workspace_bytes, void *stream);
@@ -427,8 +435,9 @@ ssq_status ssq_beam_select(const ssq_beam_desc *desc, const void *logits, const 
  * parents[r*beams + j] (0 .. beams-1, device int32 [batch]) of the group was;
  * a parent out of range leaves sequence j.  In place, for `nstates` different
  * states (the layers of a model; any kinds and formats, all of one batch that
- * `beams` divides) at once.  Rounding modes and token counters stay.  Bytes
- * move unchanged. */
+ * `beams` divides, each with less than 4 KiB * 2^24 / batch of codes or fp32
+ * entries for `beams` sequences) at once.  Rounding modes and token counters
+ * stay.  Bytes move unchanged. */
 ssq_status ssq_state_reorder(ssq_state *const *states, int32_t nstates, const int32_t *parents, int32_t beams,
                              void *stream);
 

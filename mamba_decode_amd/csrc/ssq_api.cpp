@@ -495,15 +495,19 @@ ssq_status ssq_stream_copy(void* dst, const void* src, size_t bytes, void* strea
 // ---------------------------------------------------------------------------
 // linear attention
 // ---------------------------------------------------------------------------
+constexpr int64_t kMostTokens = 0x7FFFFF80 - 1; // of a prompt call
+
 static bool dtype_valid(int d) { return d >= SSQ_DTYPE_FP32 && d <= SSQ_DTYPE_FP16; }
 
 static ssq_status fill_linattn(ssq_state* st, const ssq_linattn_io* io, int32_t nseq, int64_t tokens,
-                               const int32_t* slots, ssq::LinArgs* a)
+                               const int32_t* slots, int64_t most_rows, ssq::LinArgs* a)
 {
     SSQ_REQUIRE(st && io, SSQ_ERR_INVALID_ARG, "state or io is NULL");
     SSQ_REQUIRE(st->desc.kind == SSQ_MAMBA2, SSQ_ERR_KIND_MISMATCH, "linear attention runs on an SSQ_MAMBA2 state");
     SSQ_REQUIRE(dtype_valid(io->dtype), SSQ_ERR_INVALID_ARG, "unknown dtype");
     SSQ_REQUIRE(nseq >= 0 && tokens >= 0, SSQ_ERR_INVALID_ARG, "nseq and tokens must not be negative");
+    SSQ_REQUIRE(nseq <= most_rows / ((int64_t)st->desc.nheads * st->desc.rows_per_head), SSQ_ERR_UNSUPPORTED,
+                "the call covers too many state rows");
     SSQ_REQUIRE(slots || nseq <= st->desc.batch, SSQ_ERR_INVALID_ARG, "without slots nseq must not exceed the batch");
     SSQ_REQUIRE(tokens == 0 || (io->q && io->k && io->v && io->o), SSQ_ERR_INVALID_ARG,
                 "an input or output pointer is NULL");
@@ -551,7 +555,9 @@ static ssq_status fill_linattn(ssq_state* st, const ssq_linattn_io* io, int32_t 
 
 size_t ssq_linattn_workspace(const ssq_state* st, int32_t nseq, int64_t tokens)
 {
-    if (!st || st->desc.kind != SSQ_MAMBA2 || nseq < 0 || tokens < 0) return (size_t)-1;
+    if (!st || st->desc.kind != SSQ_MAMBA2 || nseq < 0 || tokens < 0 || tokens > kMostTokens ||
+        nseq > ssq::kMaxPrefillRows / ((int64_t)st->desc.nheads * st->desc.rows_per_head))
+        return (size_t)-1;
     return ssq::linattn_workspace(st->desc.format, nseq, tokens, st->desc.nheads, st->desc.rows_per_head,
                                   num_cus(st->device));
 }
@@ -561,11 +567,11 @@ ssq_status ssq_linattn_prefill(ssq_state* st, const ssq_linattn_io* io, int32_t 
                                size_t workspace_bytes, void* stream)
 {
     ssq::LinArgs a;
-    ssq_status s = fill_linattn(st, io, nseq, tokens, slots, &a);
+    ssq_status s = fill_linattn(st, io, nseq, tokens, slots, ssq::kMaxPrefillRows, &a);
     if (s != SSQ_OK) return s;
     SSQ_REQUIRE(nseq == 0 || cu_seqlens, SSQ_ERR_INVALID_ARG, "cu_seqlens is NULL");
     SSQ_REQUIRE(aligned(cu_seqlens, 4), SSQ_ERR_INVALID_ARG, "cu_seqlens must be 4-byte aligned");
-    SSQ_REQUIRE(tokens < 0x7FFFFF80, SSQ_ERR_UNSUPPORTED, "a call takes up to 2^31-128 tokens");
+    SSQ_REQUIRE(tokens <= kMostTokens, SSQ_ERR_UNSUPPORTED, "a call takes fewer than 2^31-128 tokens");
     const size_t need = ssq_linattn_workspace(st, nseq, tokens);
     SSQ_REQUIRE(need == 0 || (workspace && workspace_bytes >= need), SSQ_ERR_INVALID_ARG, "the workspace is too small");
     SSQ_REQUIRE(aligned(workspace, 256), SSQ_ERR_INVALID_ARG, "the workspace must be 256-byte aligned");
@@ -582,7 +588,7 @@ ssq_status ssq_linattn_step(ssq_state* st, const ssq_linattn_io* io, int32_t nse
                             int32_t readout, void* stream)
 {
     ssq::LinArgs a;
-    ssq_status s = fill_linattn(st, io, nseq, nseq, slots, &a);
+    ssq_status s = fill_linattn(st, io, nseq, nseq, slots, ssq::kMaxStepRows, &a);
     if (s != SSQ_OK) return s;
     SSQ_REQUIRE(readout == SSQ_READ_POST_QUANT || readout == SSQ_READ_PRE_QUANT, SSQ_ERR_INVALID_ARG,
                 "unknown readout");
@@ -606,6 +612,7 @@ static ssq_status check_beam(const ssq_beam_desc* d)
     SSQ_REQUIRE(d->pad_token >= 0 && d->pad_token < d->vocab, SSQ_ERR_INVALID_ARG, "pad_token must be 0 .. vocab-1");
     SSQ_REQUIRE(d->row_stride >= d->vocab, SSQ_ERR_INVALID_ARG, "row_stride must be at least vocab");
     const int64_t rows = (int64_t)d->batch * d->beams;
+    SSQ_REQUIRE(rows <= ssq::kMaxBlocks, SSQ_ERR_UNSUPPORTED, "batch * beams must be below 2^24");
     SSQ_REQUIRE(d->row_stride <= ((int64_t)1 << 59) / (rows > 0 ? rows : 1), SSQ_ERR_INVALID_ARG,
                 "row_stride is too large");
     return SSQ_OK;
@@ -681,6 +688,8 @@ ssq_status ssq_state_reorder(ssq_state* const* states, int32_t nstates, const in
         if (scale_ptr(st)) parts[n++] = {(uint8_t*)scale_ptr(st), low * 4};
         if (zero_ptr(st)) parts[n++] = {(uint8_t*)zero_ptr(st), low * 4};
         if (hi_ptr(st)) parts[n++] = {(uint8_t*)hi_ptr(st), (rows - low) * 256};
+        SSQ_REQUIRE(ssq::reorder_blocks(rows * (int64_t)st->lay.row_bytes, st->desc.batch / beams) <= ssq::kMaxBlocks,
+                    SSQ_ERR_UNSUPPORTED, "a state has too many bytes for each beam");
     }
     if (beams == 1) return ok();
     return from_hip(ssq::launch_reorder(parts, n, parents, beams, states[0]->desc.batch / beams, (hipStream_t)stream),

@@ -24,10 +24,7 @@
 namespace ssq {
 
 constexpr int kBeamMaxShares = 16; // workgroups per row at most
-#ifndef SSQ_BEAM_VPL
-#define SSQ_BEAM_VPL 32
-#endif
-constexpr int kBeamLane = SSQ_BEAM_VPL; // elements a lane holds at once
+constexpr int kBeamLane = 32; // elements a lane holds at once
 constexpr int kBeamPiece = 16;
 
 struct BeamShare {
@@ -388,16 +385,13 @@ __global__ __launch_bounds__(1024) void k_beam_join(BeamArgs a, const BeamShare*
 // ---------------------------------------------------------------------------
 // launch
 // ---------------------------------------------------------------------------
-// Workgroups of a row: enough of all rows to fill the card (2048), no more than there are tiles of
+// Workgroups of a row: enough of all rows to fill the card (1024), no more than there are tiles of
 // four waves, nor than the join takes.
 static int beam_shares(int64_t rows, int vocab)
 {
-#ifndef SSQ_BEAM_WGS
-#define SSQ_BEAM_WGS 1024
-#endif
     const int tile = 256 * kBeamLane;
     const int64_t tiles = ((int64_t)vocab + 7 + tile - 1) / tile;
-    int64_t shares = (SSQ_BEAM_WGS + rows - 1) / (rows > 0 ? rows : 1);
+    int64_t shares = (1024 + rows - 1) / (rows > 0 ? rows : 1);
     if (shares > tiles) shares = tiles;
     return (int)(shares < kBeamMaxShares ? shares : kBeamMaxShares);
 }
@@ -412,7 +406,6 @@ template <int DT>
 static hipError_t launch_rows_of(const BeamArgs& a, BeamShare* shares, uint64_t* best, int nshares, hipStream_t st)
 {
     const int64_t blocks = (int64_t)a.batch * a.beams * nshares;
-    if (blocks > kMaxBlocks) return hipErrorInvalidValue;
     const size_t lds = 4 * (size_t)beam_wave_keys(a.nselect) * sizeof(uint64_t); // 34 KiB at most
     hipLaunchKernelGGL(k_beam_rows<DT>, dim3((unsigned)blocks), dim3(256), lds, st, a, shares, best, nshares);
     return hipGetLastError();

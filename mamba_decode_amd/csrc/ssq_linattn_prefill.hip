@@ -150,7 +150,7 @@ struct alignas(16) WriteDecay {
     float keep, change; // exp2(c_last) x = keep*x + change*x, keep 0 or 1: exact near 1
 };
 
-// 52,928 bytes: three workgroups on a compute unit
+// 52,896 bytes: three workgroups on a compute unit
 struct alignas(16) ChunkLds {
     __bf16 k[kChunk][kPitch];
     __bf16 v[kChunk][kColPitch];
@@ -257,7 +257,6 @@ enum { WHOLE = 0, PART_STATE = 1, PART_OUT = 2 };
 constexpr int kReadTerms = 2;
 template <int MODE>
 constexpr int write_terms() { return MODE == PART_OUT ? 2 : 3; }
-
 
 struct ChunkArgs {
     LinArgs a;
@@ -483,7 +482,7 @@ __global__ __launch_bounds__(256, MODE == PART_STATE ? 4 : 3) void k_linattn_chu
                     const float ri = s.d.r[qi];
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        w[r] = A[i][r] * (a.oscale * __builtin_amdgcn_exp2f(kj + r <= qi ? ri - rj[r] : -1000.0f));
+                        w[r] = kj + r <= qi ? A[i][r] * (a.oscale * __builtin_amdgcn_exp2f(ri - rj[r])) : 0.0f;
                 } else {
                     w = A[i] * s.d.row[qi] * *reinterpret_cast<const f32x4*>(&s.d.col[8 * i * (i - 1) + kj]);
                 }
@@ -896,11 +895,12 @@ struct ChunkPlan {
     int64_t nparts;
 };
 
-// Sequences are split where they and the blocks do not give every compute unit a workgroup, into
-// as many parts as there can be workgroups at once, of two chunks at least.  (24 ragged bf16
-// prompts of 32 heads, 768 workgroups whole: 88 us; as 384 workgroups of twice the columns 99 us
-// whole and 162 us split.  Three prompts of 32 heads of 128, 192 workgroups whole: 94 us split for
-// three workgroups a unit, 104 us for two.)
+// Sequences are split where they and the blocks do not give every compute unit a workgroup (24
+// ragged bf16 prompts of 32 heads, 768 workgroups whole: 84 us; as 384 workgroups of twice the
+// columns 99 us whole and 162 us split), into as many parts as there can be workgroups at once (of
+// three prompts of 32 heads of 128, bf16: 94 us for three workgroups a unit, 104 us for two), of
+// three chunks at least (2048 tokens of 24 heads: the three kernels take 32.4 us, 35.3 in parts
+// of two and 34.3 of four: shorter parts give the join more states to move).
 static ChunkPlan chunk_plan(int dtype, int nseq, int64_t tokens, int H, int P, int num_cus)
 {
     ChunkPlan p;
@@ -910,9 +910,9 @@ static ChunkPlan chunk_plan(int dtype, int nseq, int64_t tokens, int H, int P, i
     p.nparts = 0;
     const int64_t chunks = (tokens + chunk - 1) / chunk;
     const int64_t slots = (dtype == DT_BF16 ? 3 : 2) * (int64_t)num_cus; // workgroups at once
-    if (chunks > 2 && nseq * (int64_t)p.blocks < num_cus) {
+    if (nseq > 0 && chunks > 2 && nseq * (int64_t)p.blocks < num_cus) {
         int64_t per = (chunks * p.blocks + slots - 1) / slots;
-        if (per < 2) per = 2;
+        if (per < 3) per = 3;
         p.part_tokens = (int)(per * chunk);
         p.nparts = tokens / p.part_tokens + nseq;
     }
@@ -948,7 +948,6 @@ static hipError_t launch_chunk(int dtype, ChunkArgs c, int64_t items, hipStream_
     c.run = (share + cut - 1) / cut;
     c.runs = (c.blocks + c.run - 1) / c.run;
     const int64_t blocks = (items * c.runs + 7) / 8 * 8 * c.run;
-    if (blocks > kMaxBlocks) return hipErrorInvalidValue;
     const dim3 grid((unsigned)blocks), wg(256);
     if (dtype == DT_FP32) {
         hipLaunchKernelGGL((k_linattn_wide<MODE, DT_FP32>), grid, wg, 0, st, c);
@@ -973,7 +972,6 @@ static hipError_t launch_chunks(int dtype, const LinArgs& a, void* ws, int num_c
     hipError_t e = launch_chunk<PART_STATE>(dtype, c, p.nparts, st);
     if (e != hipSuccess) return e;
     const int64_t units = (int64_t)a.nseq * a.H * a.P * 32, blocks = (units + 255) / 256;
-    if (blocks > kMaxBlocks) return hipErrorInvalidValue;
     hipLaunchKernelGGL(k_linattn_join, dim3((unsigned)blocks), dim3(256), 0, st, c, units);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -985,7 +983,6 @@ static hipError_t launch_state_rows(const LinArgs& a, bool store, hipStream_t st
 {
     constexpr int RPW = Traits<F>::bits == 8 ? 8 : 16;
     const int64_t units = (int64_t)a.nseq * a.H * a.P / RPW, blocks = (units + 3) / 4;
-    if (blocks > kMaxBlocks) return hipErrorInvalidValue;
     if (a.sr.on) hipLaunchKernelGGL((k_linattn_rows<F, true>), dim3((unsigned)blocks), dim3(256), 0, st, a, units, store);
     else hipLaunchKernelGGL((k_linattn_rows<F, false>), dim3((unsigned)blocks), dim3(256), 0, st, a, units, store);
     return hipGetLastError();

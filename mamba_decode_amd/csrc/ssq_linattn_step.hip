@@ -145,7 +145,6 @@ static hipError_t launch_step_rows(const LinArgs& a, bool pre, hipStream_t st)
 {
     const int64_t units = (int64_t)a.nseq * a.H * (a.P / ROWS);
     const int64_t blocks = (units + 3) / 4;
-    if (blocks > kMaxBlocks) return hipErrorInvalidValue;
     const dim3 grid((unsigned)blocks), wg(256);
     if constexpr (F == FP32) {
         hipLaunchKernelGGL((k_linattn_step<F, DT, ROWS, true, false>), grid, wg, 0, st, a, units);

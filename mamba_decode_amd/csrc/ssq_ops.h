@@ -33,7 +33,13 @@ struct LinArgs {
 };
 
 constexpr int kMaxBeams = 32;
-constexpr int64_t kMaxBlocks = (1 << 24) - 1; // workgroups of 256: a launch has fewer than 2^32 work-items
+
+// Sizes are refused before anything is enqueued where a launch would have 2^32 work-items or more:
+// workgroups of 256, state rows of a token step (16 a wave) and of a prompt (16 a column block, and
+// the blocks' runs rounded up at no more than 2.3 blocks for each).
+constexpr int64_t kMaxBlocks = (1 << 24) - 1;
+constexpr int64_t kMaxStepRows = (int64_t)1 << 29;
+constexpr int64_t kMaxPrefillRows = (int64_t)1 << 26;
 
 struct BeamArgs {
     const void* logits;
@@ -52,6 +58,8 @@ struct ReorderPart {
     uint8_t* p;
     int64_t bytes;
 };
+constexpr int64_t kColumnBytes = 256 * 16; // what a workgroup moves of each sequence of a group
+constexpr int64_t reorder_blocks(int64_t bytes, int64_t groups) { return (bytes + kColumnBytes - 1) / kColumnBytes * groups; }
 
 hipError_t launch_linattn_step(int fmt, int dtype, const LinArgs& a, bool pre, hipStream_t st);
 size_t linattn_workspace(int fmt, int nseq, int64_t tokens, int H, int P, int num_cus);

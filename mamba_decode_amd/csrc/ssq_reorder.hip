@@ -20,8 +20,6 @@ struct ReorderArgs {
     int nparts, beams, groups;
 };
 
-constexpr int64_t kColumnBytes = 256 * 16; // a workgroup's columns
-
 template <int BMAX>
 __global__ __launch_bounds__(256) void k_reorder(ReorderArgs a)
 {
@@ -67,8 +65,7 @@ hipError_t launch_reorder(const ReorderPart* parts, int nparts, const int32_t* p
         a.nparts = 0;
         int64_t blocks = 0;
         while (at < nparts && a.nparts < kMaxParts) {
-            const int64_t n = (parts[at].bytes + kColumnBytes - 1) / kColumnBytes * groups;
-            if (n > kMaxBlocks) return hipErrorInvalidValue;
+            const int64_t n = reorder_blocks(parts[at].bytes, groups); // kMaxBlocks at most
             if (blocks + n > kMaxBlocks) break;
             a.part[a.nparts] = parts[at];
             a.first[a.nparts] = (uint32_t)blocks;

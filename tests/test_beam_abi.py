@@ -28,6 +28,15 @@ def test_beam_descriptions(kw):
     assert ssq.ssq_last_error()
 
 
+def test_beam_rows_of_one_launch():
+    d = desc(batch=1 << 22)
+    assert ssq.ssq_beam_workspace(d) == 0
+    vp = ctypes.c_void_p
+    assert L.ssq_beam_select(ctypes.byref(d), vp(4096), vp(4096), None, vp(4096), vp(4096), vp(4096), vp(4096), 1 << 40,
+                             None) == ssq.SSQ_ERR_UNSUPPORTED
+    assert ssq.ssq_beam_workspace(desc(batch=(1 << 22) - 1)) > 0
+
+
 def test_beam_arguments():
     vp = ctypes.c_void_p
     d = desc()

@@ -490,5 +490,79 @@ def test_refusals():
     refused(ssq.SsqError, step, delta, q[:2], q[:2], v[:2], g[:2], o[:2])
     quant = state_of(torch.zeros(2, 4, 32, 128), 2, "int8_sym")
     refused(ssq.SsqError, run, quant, q, q, v, g, o, cu, workspace=t(256, d=torch.uint8))
+    # more state rows, or more tokens, than one launch covers: refused whatever the slots say
+    io = ssq._linattn_io(st, q, q, v, g, o, 1.0, 6, torch.cuda.current_device())
+    slots = torch.full((8,), -1, dtype=torch.int32, device="cuda")
+    ws = t(256, d=torch.uint8)
+    for n, T in (((1 << 26) // 128 + 1, 6), (1, 0x7FFFFF80), (1, 1 << 40)):
+        assert ssq.lib.ssq_linattn_workspace(st.handle, n, T) == ssq._SIZE_MAX
+        assert ssq.lib.ssq_linattn_prefill(st.handle, io, n, T, cu.data_ptr(), slots.data_ptr(), None, ws.data_ptr(), 256,
+                                           None) == ssq.SSQ_ERR_UNSUPPORTED
+    assert ssq.lib.ssq_linattn_step(st.handle, io, (1 << 29) // 128 + 1, slots.data_ptr(), 0, None) == ssq.SSQ_ERR_UNSUPPORTED
+    assert ssq.ssq_linattn_workspace(st, 0, 0x7FFFFF7F) == 0
     torch.cuda.synchronize()
     assert torch.equal(st.storage, before)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+@pytest.mark.parametrize("fmt", ["fp32", "int8_asym"])
+def test_nothing_is_read_that_is_not_asked_for(dtype, fmt):
+    """NaN in the rows before, between and behind the sequences, in the states of fresh and unnamed
+    slots and in one sequence: every other sequence has the result of a clean call."""
+    say("NaN around", dtype, fmt)
+    gen = torch.Generator().manual_seed(20)
+    H, G, P, T = 4, 2, 48, 400
+    q, k, v, g = (x.cuda() for x in ref.inputs(gen, T, H, G, P, dtype))
+    start = torch.randn(5, H, P, 128, generator=gen)
+    # tokens 10..100, 100..101 (the bad one), 101..330; 0..10 and 330..400 are padding
+    cu = torch.tensor([10, 100, 101, 330], dtype=torch.int32, device="cuda")
+    slots = torch.tensor([2, 4, 0], dtype=torch.int32, device="cuda")
+    fresh = torch.tensor([1, 0, 0], dtype=torch.uint8, device="cuda")
+    clean, dirty = state_of(start, G, fmt), state_of(start, G, fmt)
+    want, got = torch.zeros_like(v), torch.zeros_like(v)
+    ssq.ssq_linattn_prefill(clean, q, k, v, g, want, cu, slots=slots, fresh=fresh)
+    for x in (q, k, v, g):
+        x[:10] = x[330:] = x[100:101] = torch.nan
+    for part in (dirty.regions()[0] if fmt == "fp32" else dirty.regions()[1],):
+        rows = part.view(torch.float32).view(5, -1)
+        rows[1] = rows[2] = rows[3] = torch.nan
+    ssq.ssq_linattn_prefill(dirty, q, k, v, g, got, cu, slots=slots, fresh=fresh)
+    keep = torch.ones(T, dtype=torch.bool, device="cuda")
+    keep[100] = False
+    assert torch.equal(got[keep], want[keep])
+    a, b = values_of(clean), values_of(dirty)
+    assert torch.equal(a[[0, 2]], b[[0, 2]])
+    assert b[[1, 3]].isnan().all()
+
+
+def test_two_calls_at_once():
+    """Two prompts and a token on three states and streams, each with its own workspace."""
+    say("two at once")
+    gen = torch.Generator().manual_seed(21)
+    H, P, T = 8, 64, 1500
+    cases = []
+    for dtype in (BF, F32, BF):
+        q, k, v, g = (x.cuda() for x in ref.inputs(gen, T, H, 1, P, dtype))
+        start = torch.randn(1, H, P, 128, generator=gen)
+        cases.append((q, k, v, g, start))
+    cu = cu_of([T])
+
+    def run(i, st, o, stream=None):
+        q, k, v, g, _ = cases[i]
+        for _ in range(3):
+            ssq.ssq_linattn_prefill(st, q, k, v, g, o, cu, stream=stream)
+            ssq.ssq_linattn_step(st, q[:1], k[:1], v[:1], g[:1], o[:1], stream=stream)
+
+    want = []
+    for i, c in enumerate(cases):
+        st, o = state_of(c[4], 1), torch.zeros_like(c[2])
+        run(i, st, o)
+        want.append((values_of(st), o.cpu()))
+    streams = [torch.cuda.Stream() for _ in cases]
+    states, outs = [state_of(c[4], 1) for c in cases], [torch.zeros_like(c[2]) for c in cases]
+    torch.cuda.synchronize()
+    for i, s in enumerate(streams):
+        run(i, states[i], outs[i], stream=s)
+    torch.cuda.synchronize()
+    for w, st, o in zip(want, states, outs):
+        assert torch.equal(w[0], values_of(st)) and torch.equal(w[1], o.cpu())
