@@ -24,7 +24,6 @@
 namespace ssq {
 
 constexpr int kBeamMaxShares = 16; // workgroups per row at most
-constexpr int kBeamLane = 32; // elements a lane holds at once
 constexpr int kBeamPiece = 16;
 
 struct BeamShare {
@@ -86,6 +85,97 @@ __device__ __forceinline__ uint64_t wave_nth(uint64_t key, int n, uint64_t* room
     return at ? shfl_u64(key, __builtin_ctzll(at)) : 0;
 }
 
+// key of lane ^ D
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t x)
+{
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xF, 0xF, true);
+}
+template <int D>
+__device__ __forceinline__ uint32_t xor_u32(uint32_t x)
+{
+    if constexpr (D == 1) return dpp_u32<0xB1>(x);
+    else if constexpr (D == 2) return dpp_u32<0x4E>(x);
+    else if constexpr (D == 3) return dpp_u32<0x1B>(x);
+    else if constexpr (D == 4) return dpp_u32<0x141>(dpp_u32<0x1B>(x));
+    else if constexpr (D == 7) return dpp_u32<0x141>(x);
+    else if constexpr (D == 8) return dpp_u32<0x128>(x);
+    else if constexpr (D == 15) return dpp_u32<0x140>(x);
+    else if constexpr (D == 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false); // rows 0 0 2 2 and 1 1 3 3
+        return threadIdx.x & 16 ? r[0] : r[1];
+    } else if constexpr (D == 32) {
+        const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false); // the low half twice, the high half twice
+        return threadIdx.x & 32 ? r[0] : r[1];
+    } else if constexpr (D == 31) return xor_u32<16>(xor_u32<15>(x));
+    else return xor_u32<32>(xor_u32<31>(x));
+}
+
+// What is sorted: a key, or a candidate of which one with an equal score comes first by its place.
+struct BeamTop {
+    uint64_t score; // order bits of the double, 0: none
+    uint32_t place; // beam, and rank in the beam's list
+};
+__device__ __forceinline__ bool before(uint64_t a, uint64_t b) { return a > b; }
+__device__ __forceinline__ bool before(BeamTop a, BeamTop b)
+{
+    return a.score > b.score || (a.score == b.score && a.place < b.place);
+}
+template <int D>
+__device__ __forceinline__ uint64_t other_lane(uint64_t v)
+{
+    return ((uint64_t)xor_u32<D>((uint32_t)(v >> 32)) << 32) | xor_u32<D>((uint32_t)v);
+}
+template <int D>
+__device__ __forceinline__ BeamTop other_lane(BeamTop v)
+{
+    return {other_lane<D>(v.score), xor_u32<D>(v.place)};
+}
+
+// One step of a sorting network over the wave's lanes: of lane and lane ^ D the one without bit
+// UPPER keeps what comes first.
+template <int D, int UPPER, typename K>
+__device__ __forceinline__ void exchange(K& v)
+{
+    const K o = other_lane<D>(v);
+    if (before(o, v) != ((threadIdx.x & UPPER) != 0)) v = o;
+}
+// lanes that first rise and then fall, or the other way round, into order
+template <int N, typename K>
+__device__ __forceinline__ void settle(K& v)
+{
+    if constexpr (N >= 32) exchange<32, 32>(v);
+    if constexpr (N >= 16) exchange<16, 16>(v);
+    if constexpr (N >= 8) exchange<8, 8>(v);
+    if constexpr (N >= 4) exchange<4, 4>(v);
+    if constexpr (N >= 2) exchange<2, 2>(v);
+    if constexpr (N >= 1) exchange<1, 1>(v);
+}
+// the wave's keys in descending order
+__device__ __forceinline__ uint64_t wave_sort(uint64_t v)
+{
+    exchange<1, 1>(v);
+    exchange<3, 2>(v);
+    settle<1>(v);
+    exchange<7, 4>(v);
+    settle<2>(v);
+    exchange<15, 8>(v);
+    settle<4>(v);
+    exchange<31, 16>(v);
+    settle<8>(v);
+    exchange<63, 32>(v);
+    settle<16>(v);
+    return v;
+}
+// the 64 first of two lists, one in descending order and one in ascending order, in descending order
+template <typename K>
+__device__ __forceinline__ K wave_merge(K v, K ascending)
+{
+    if (before(ascending, v)) v = ascending;
+    settle<32>(v);
+    return v;
+}
+
 // keys larger than `key` among list[0 .. count)
 __device__ __forceinline__ int keys_above(const uint64_t* list, int count, uint64_t key)
 {
@@ -122,16 +212,14 @@ __device__ __forceinline__ float wave_threshold(float v, int n)
     return order_value(lo);
 }
 
-template <int DT>
+template <int DT, int VPL>
 __global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a, BeamShare* shares, uint64_t* best, int nshares)
 {
-    constexpr int VPL = kBeamLane;
     constexpr int VE = DT == DT_FP32 ? 4 : 8; // elements in 16 bytes
     constexpr int NV = VPL / VE;
     constexpr int TILE = 64 * VPL;            // elements of a wave's tile
     extern __shared__ __align__(16) uint64_t lds[];
     __shared__ BeamShare wave_share[4];
-    __shared__ int wave_kept[4];
     const int n = a.nselect;
     const int row = blockIdx.x / nshares, share = blockIdx.x % nshares;
     const int tid = threadIdx.x, lane = tid & 63;
@@ -154,16 +242,22 @@ __global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a, BeamShare* shares
     float last = -INFINITY;        // the n-th best so far; -inf while there are fewer
     auto merge = [&](int c) { // the new keys and the kept ones: the best n are kept
         wave_lds_sync();
+        if (nkept + c > 64) {
+            uint64_t top = lane < nkept ? kept[lane] : 0;
+            for (int i = 0; i < c; i += 64) top = wave_merge(top, ~wave_sort(i + lane < c ? ~fresh[i + lane] : ~0ull));
+            if (lane < n) kept[lane] = top;
+        } else {
         for (int i = lane; i < nkept + c; i += 64) {
             const uint64_t key = i < nkept ? kept[i] : fresh[i - nkept];
             const int rank = keys_above(kept, nkept, key) + keys_above(fresh, c, key);
             if (rank < n) next[rank] = key;
         }
-        wave_lds_sync();
-        nkept = min(n, nkept + c);
         uint64_t* const swap = kept;
         kept = next;
         next = swap;
+        }
+        wave_lds_sync();
+        nkept = min(n, nkept + c);
         if (nkept == n) last = order_value((uint32_t)(kept[n - 1] >> 32));
     };
     for (int64_t t = share * 4 + wave; t < tiles; t += 4 * nshares) {
@@ -237,30 +331,18 @@ __global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a, BeamShare* shares
             merge(c);
         }
     }
-    // the four waves' lists, each copied to its place at the front of the wave's LDS
+    // the four waves' lists, each at the front of the wave's LDS, 0 behind its last key
     const float wm = wave_max(m);
     s = wave_sum(m > -INFINITY ? s * __expf(m - wm) : 0.0f);
-    if (kept != mine) {
-        for (int i = lane; i < nkept; i += 64) mine[i] = kept[i];
-    }
-    if (lane == 0) {
-        wave_share[wave] = {wm, s};
-        wave_kept[wave] = nkept;
-    }
+    wave_lds_sync();
+    uint64_t top = lane < nkept ? kept[lane] : 0;
+    wave_lds_sync();
+    if (lane < n) mine[lane] = top;
+    if (lane == 0) wave_share[wave] = {wm, s};
     __syncthreads();
-    uint64_t* out_best = best + ((int64_t)row * nshares + share) * n;
-    int found = 0;
-    for (int w = 0; w < 4; ++w) found += wave_kept[w];
-    for (int i = tid; i < 4 * n; i += 256) {
-        const int w = i / n, r = i % n;
-        if (r >= wave_kept[w]) continue;
-        const uint64_t key = lds[w * beam_wave_keys(n) + r];
-        int rank = r;
-        for (int o = 0; o < 4; ++o)
-            if (o != w) rank += keys_above(lds + o * beam_wave_keys(n), wave_kept[o], key);
-        if (rank < n) out_best[rank] = key;
-    }
-    for (int i = found + tid; i < n; i += 256) out_best[i] = 0;
+    if (wave != 0) return;
+    for (int w = 1; w < 4; ++w) top = wave_merge(top, 63 - lane < n ? lds[w * beam_wave_keys(n) + 63 - lane] : 0);
+    if (lane < n) best[((int64_t)row * nshares + share) * n + lane] = top;
     if (tid == 0) {
         float M = -INFINITY, sum = 0.0f;
         for (int i = 0; i < 4; ++i) M = fmaxf(M, wave_share[i].m);
@@ -273,158 +355,160 @@ __global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a, BeamShare* shares
 // ---------------------------------------------------------------------------
 // the shares of each beam, then the beams of each request
 // ---------------------------------------------------------------------------
-// a wave's work list: the keys of all shares, and at least the 64 of wave_nth
-__host__ __device__ constexpr int beam_join_keys(int nshares, int n) { return nshares * n > 64 ? nshares * n : 64; }
+// order bits of a double, and the double
+__device__ __forceinline__ uint64_t order_bits64(double x)
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, x + 0.0);
+    return u ^ ((u >> 63) ? ~0ull : 1ull << 63);
+}
+__device__ __forceinline__ double order_value64(uint64_t o)
+{
+    return __builtin_bit_cast(double, (o >> 63) ? o ^ (1ull << 63) : ~o);
+}
 
-struct BeamCand {
-    double score;
-    uint32_t beam, token;
-};
+// LDS of the join: each wave's list [n], scores and places, and the tokens of all beams [beams][n]
+__host__ __device__ constexpr size_t beam_join_lds(int waves, int beams, int n)
+{
+    return (size_t)waves * n * (sizeof(uint64_t) + sizeof(uint32_t)) + (size_t)beams * n * sizeof(uint32_t);
+}
 
-// a wave for each beam, up to 16
+// A workgroup of a request, a wave of a beam (of two from 17 beams up).  A wave sorts the keys of
+// its beam's shares, 64 at a time, into the beam's candidates, a lane each, and joins its beams;
+// then the waves' lists are joined in pairs.
 __global__ __launch_bounds__(1024) void k_beam_join(BeamArgs a, const BeamShare* shares, const uint64_t* best, int nshares)
 {
-    // LDS: a work list of each wave, the best [n], the beams' lists [beams][n]: scores, tokens
     extern __shared__ __align__(16) uint64_t lds[];
-    __shared__ int counts[kMaxBeams];
     const int n = a.nselect, beams = a.beams;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int waves = blockDim.x >> 6, room = beam_join_keys(nshares, n);
-    uint64_t* work = lds + wave * room;
-    BeamCand* top = reinterpret_cast<BeamCand*>(lds + waves * room);
-    double* cand = reinterpret_cast<double*>(top + n);
-    uint32_t* tokens = reinterpret_cast<uint32_t*>(cand + beams * n);
+    const int tid = threadIdx.x, lane = tid & 63, waves = blockDim.x >> 6;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    uint64_t* const scores = lds;
+    uint32_t* const places = reinterpret_cast<uint32_t*>(lds + waves * n);
+    uint32_t* const tokens = places + waves * n;
     const int64_t request = blockIdx.x;
 
+    BeamTop top = {0, 0};
     for (int b = wave; b < beams; b += waves) {
         const int64_t row = request * beams + b;
         const float score = a.scores[row];
-        const int total = nshares * n; // at most 16 for each lane
-        const uint64_t* keys = best + row * total;
-        BeamShare sh = {-INFINITY, 0.0f};
-        if (lane < nshares) sh = shares[row * nshares + lane];
-        uint64_t k[kBeamMaxShares], mine = 0; // of a dead or finished beam never written, and not used
+        const bool finished = a.finished && a.finished[row];
+        if (!(score > -INFINITY)) continue;
+        BeamTop mine = {0, (uint32_t)(b * n + lane)};
+        uint32_t token = (uint32_t)a.pad;
+        if (finished) {
+            if (lane == 0) mine.score = order_bits64((double)score);
+        } else {
+            const int total = nshares * n;
+            const uint64_t* keys = best + row * total;
+            BeamShare sh = {-INFINITY, 0.0f};
+            if (lane < nshares) sh = shares[row * nshares + lane];
+            uint64_t k[kBeamMaxShares];
+            uint64_t key;
+            if (n > 16) { // each share's list, in order, by itself
 #pragma unroll
-        for (int i = 0; i < kBeamMaxShares; ++i) {
-            k[i] = lane + 64 * i < total ? keys[lane + 64 * i] : 0;
-            mine = k[i] > mine ? k[i] : mine;
-        }
-        if (!(score > -INFINITY)) {
-            if (lane == 0) counts[b] = 0;
-            continue;
-        }
-        if (a.finished && a.finished[row]) {
-            if (lane == 0) {
-                counts[b] = 1;
-                cand[b * n] = (double)score;
-                tokens[b * n] = (uint32_t)a.pad;
+                for (int i = 0; i < kBeamMaxShares; ++i) {
+                    const int r = i == 0 ? lane : 63 - lane; // the first from its front, the others from their ends
+                    k[i] = i < nshares && r < n ? keys[i * n + r] : 0;
+                }
+                key = k[0];
+#pragma unroll
+                for (int i = 1; i < kBeamMaxShares; ++i)
+                    if (i < nshares) key = wave_merge(key, k[i]);
+            } else { // 64 keys of several shares at a time, at most four times
+#pragma unroll
+                for (int i = 0; i < 4; ++i) k[i] = lane + 64 * i < total ? keys[lane + 64 * i] : 0;
+                key = wave_sort(k[0]);
+#pragma unroll
+                for (int i = 1; i < 4; ++i)
+                    if (64 * i < total) key = wave_merge(key, ~wave_sort(~k[i]));
             }
-            continue;
-        }
-        const float M = wave_max(sh.m);
-        if (!(M > -INFINITY)) {
-            if (lane == 0) counts[b] = 0;
-            continue;
-        }
-        const double logz = log((double)wave_sum(sh.m > -INFINITY ? sh.sum * __expf(sh.m - M) : 0.0f));
-        const uint64_t nth = wave_nth(mine, n, work);
-        const uint64_t low = nth ? nth : 1;
-        int c = 0;
-#pragma unroll
-        for (int i = 0; i < kBeamMaxShares; ++i) {
-            const uint64_t have = __ballot(k[i] >= low);
-            if (k[i] >= low) work[c + __popcll(have & ((1ull << lane) - 1))] = k[i];
-            c += __popcll(have);
-        }
-        wave_lds_sync();
-        for (int i = lane; i < c; i += 64) {
-            const uint64_t key = work[i];
-            const int rank = keys_above(work, c, key);
-            if (rank < n) {
+            const float M = wave_max(sh.m);
+            if (!(M > -INFINITY)) continue;
+            const double logz = log((double)wave_sum(sh.m > -INFINITY ? sh.sum * __expf(sh.m - M) : 0.0f));
+            if (key && lane < n) {
                 const double x = (double)order_value((uint32_t)(key >> 32));
-                cand[b * n + rank] = (double)score + ((x - (double)M) - logz);
-                tokens[b * n + rank] = ~(uint32_t)key;
+                mine.score = order_bits64((double)score + ((x - (double)M) - logz));
+                token = ~(uint32_t)key;
             }
         }
-        if (lane == 0) counts[b] = min(c, n);
-        wave_lds_sync(); // the list is read before the next beam's is written
+        if (lane < n) tokens[b * n + lane] = token;
+        // this list from its end: its places are above those of the wave's beams before it
+        const BeamTop end = other_lane<63>(mine);
+        top = b == wave ? mine : wave_merge(top, end);
     }
-    __syncthreads();
-    // A candidate's rank: its place in its own beam's list, and the candidates before it in the
-    // others', which are sorted: found by halving.  Of equal scores the lower beam is first.
-    int found = 0;
-    for (int b = 0; b < beams; ++b) found += counts[b];
-    for (int i = tid; i < beams * n; i += blockDim.x) {
-        const int b = i / n, r = i % n;
-        if (r >= counts[b]) continue;
-        const double me = cand[i];
-        int rank = r;
-        for (int o = 0; o < beams && rank < n; ++o) {
-            if (o == b) continue;
-            int lo = 0, hi = counts[o];
-            while (lo < hi) {
-                const int mid = (lo + hi) >> 1;
-                const double other = cand[o * n + mid];
-                if (other > me || (other == me && o < b)) lo = mid + 1;
-                else hi = mid;
-            }
-            rank += lo;
+    auto leave = [&]() {
+        if (lane < n) {
+            scores[wave * n + lane] = top.score;
+            places[wave * n + lane] = top.place;
         }
-        if (rank < n) top[rank] = {me, (uint32_t)b, tokens[i]};
+    };
+    leave();
+    for (int step = 1; step < waves; step *= 2) {
+        __syncthreads();
+        if (wave % (2 * step) == 0 && wave + step < waves) {
+            BeamTop end = {0, 0};
+            if (63 - lane < n) end = {scores[(wave + step) * n + 63 - lane], places[(wave + step) * n + 63 - lane]};
+            top = wave_merge(top, end);
+            leave();
+        }
     }
     __syncthreads();
-    for (int j = tid; j < n; j += blockDim.x) {
-        const bool have = j < found;
-        const int64_t at = request * n + j;
-        a.out_scores[at] = have ? (float)top[j].score : -INFINITY;
-        a.out_tokens[at] = have ? (int32_t)top[j].token : -1;
-        a.out_parents[at] = have ? (int32_t)top[j].beam : j % beams;
+    if (wave == 0 && lane < n) {
+        const int64_t at = request * n + lane;
+        const bool have = top.score != 0;
+        a.out_scores[at] = have ? (float)order_value64(top.score) : -INFINITY;
+        a.out_tokens[at] = have ? (int32_t)tokens[top.place] : -1;
+        a.out_parents[at] = have ? (int32_t)(top.place / n) : lane % beams;
     }
 }
 
 // ---------------------------------------------------------------------------
 // launch
 // ---------------------------------------------------------------------------
-// Workgroups of a row: enough of all rows to fill the card (1024), no more than there are tiles of
-// four waves, nor than the join takes.
-static int beam_shares(int64_t rows, int vocab)
+// Elements a lane holds at once: 32, or 16 where all of the logits are in flight at once that way
+// and the card is not full (4 x 50280 bf16: 12.9 us against 13.8; 64 x 50280 fp32 15.9 against 15.1,
+// 8 x 131071 bf16 22.7 against 21.5, 256 x 131071 fp32 45 against 40; 64 of them: 15.5 and 48).
+// Workgroups of a row: enough of all rows to fill the card (1024: of 256 x 131071 40 us, 48 for
+// 512 and 43 for 2048), no more than there are tiles of four waves, nor than the join takes.
+struct BeamPlan {
+    int lane, shares;
+};
+static BeamPlan beam_plan(int64_t rows, int vocab)
 {
-    const int tile = 256 * kBeamLane;
-    const int64_t tiles = ((int64_t)vocab + 7 + tile - 1) / tile;
+    auto tiles = [&](int lane) { return ((int64_t)vocab + 7 + 256 * lane - 1) / (256 * lane); };
+    if (tiles(16) <= kBeamMaxShares && rows * tiles(16) <= 512) return {16, (int)tiles(16)};
     int64_t shares = (1024 + rows - 1) / (rows > 0 ? rows : 1);
-    if (shares > tiles) shares = tiles;
-    return (int)(shares < kBeamMaxShares ? shares : kBeamMaxShares);
+    if (shares > tiles(32)) shares = tiles(32);
+    return {32, (int)(shares < kBeamMaxShares ? shares : kBeamMaxShares)};
 }
 
 size_t beam_workspace(int batch, int beams, int vocab, int nselect)
 {
-    const size_t shares = (size_t)batch * beams * beam_shares((int64_t)batch * beams, vocab);
+    const size_t shares = (size_t)batch * beams * beam_plan((int64_t)batch * beams, vocab).shares;
     return (shares * sizeof(BeamShare) + 255) / 256 * 256 + shares * nselect * sizeof(uint64_t);
 }
 
-template <int DT>
+template <int DT, int VPL>
 static hipError_t launch_rows_of(const BeamArgs& a, BeamShare* shares, uint64_t* best, int nshares, hipStream_t st)
 {
     const int64_t blocks = (int64_t)a.batch * a.beams * nshares;
     const size_t lds = 4 * (size_t)beam_wave_keys(a.nselect) * sizeof(uint64_t); // 34 KiB at most
-    hipLaunchKernelGGL(k_beam_rows<DT>, dim3((unsigned)blocks), dim3(256), lds, st, a, shares, best, nshares);
+    hipLaunchKernelGGL((k_beam_rows<DT, VPL>), dim3((unsigned)blocks), dim3(256), lds, st, a, shares, best, nshares);
     return hipGetLastError();
 }
 
 template <int DT>
 static hipError_t launch_beam_dt(const BeamArgs& a, hipStream_t st)
 {
-    const int nshares = beam_shares((int64_t)a.batch * a.beams, a.vocab);
+    const BeamPlan plan = beam_plan((int64_t)a.batch * a.beams, a.vocab);
+    const int nshares = plan.shares;
     const size_t rows = (size_t)a.batch * a.beams * nshares;
     BeamShare* shares = static_cast<BeamShare*>(a.ws);
     uint64_t* best = reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(a.ws) + (rows * sizeof(BeamShare) + 255) / 256 * 256);
-    const hipError_t e = launch_rows_of<DT>(a, shares, best, nshares, st);
+    const hipError_t e = plan.lane == 16 ? launch_rows_of<DT, 16>(a, shares, best, nshares, st)
+                                         : launch_rows_of<DT, 32>(a, shares, best, nshares, st);
     if (e != hipSuccess) return e;
-    // the waves' lists within 32 KiB, at most 26 KiB of candidates
-    const size_t list = (size_t)beam_join_keys(nshares, a.nselect) * sizeof(uint64_t);
-    int waves = a.beams < 16 ? a.beams : 16;
-    while (waves * list > 32768) --waves;
-    const size_t lds = waves * list + (size_t)a.nselect * (sizeof(BeamCand) + a.beams * (sizeof(double) + sizeof(uint32_t)));
+    const int waves = a.beams < 16 ? a.beams : 16;
+    const size_t lds = beam_join_lds(waves, a.beams, a.nselect); // 20 KiB at most
     hipLaunchKernelGGL(k_beam_join, dim3((unsigned)a.batch), dim3(64 * waves), lds, st, a, shares, best, nshares);
     return hipGetLastError();
 }
