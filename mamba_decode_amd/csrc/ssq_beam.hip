@@ -15,10 +15,17 @@
 // of its row with the best nselect keys so far in LDS, and looks further at a tile only where a
 // lane's maximum passes the last of them.  The elements that do, or in a first tile those that
 // reach the nselect-th largest of the lanes' maxima (found to a few thousandths of their range by
-// halving: any value that nselect lanes reach serves), go into a short list; the list and the
-// kept keys are ranked together.  Where the list runs over (rows in order, or many equal logits),
+// halving: any value that nselect lanes reach serves), go into a short list, and the list and the
+// kept keys together give the kept ones: ranked by counting up to 64 of them, else sorted across
+// the lanes and merged, 64 at a time (counting costs their square: 32 x 32 beams of 32000 with
+// nselect 64 took 351 us that way, 44 so).  Where the list runs over (rows in order, or many equal logits),
 // the tile is taken in pieces of 16 elements a lane with an exact threshold, which bounds the list
 // whatever the values are.
+//
+// What bounds it: 32 x 8 beams of 131071 in fp32 (134 MB) take 28 us, 4.8 TB/s, in the pass and 6
+// us in the join; a wave's loads of 2048 elements wait for the tile before (fetched a tile ahead
+// they need 32 registers more, three waves a SIMD for four: 40 us in fp32; 3% gained in bf16).
+// 4 x 50280 take 6.6 and 5.5 us, mostly the latency of two launches.
 #include "ssq_ops_device.h"
 
 namespace ssq {
@@ -212,6 +219,24 @@ __device__ __forceinline__ float wave_threshold(float v, int n)
     return order_value(lo);
 }
 
+// 16 bytes of logits, aligned to their element
+template <int DT>
+__device__ __forceinline__ void load_piece(const typename Elem<DT>::T* p, float* v)
+{
+    u32x4 w;
+    __builtin_memcpy(&w, p, sizeof(w));
+    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (DT == DT_FP32) {
+            v[j] = __uint_as_float(ws[j]);
+        } else {
+            v[2 * j] = to_f32<DT>(ws[j] & 0xFFFFu);
+            v[2 * j + 1] = to_f32<DT>(ws[j] >> 16);
+        }
+    }
+}
+
 template <int DT, int VPL>
 __global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a, BeamShare* shares, uint64_t* best, int nshares)
 {
@@ -232,9 +257,8 @@ __global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a, BeamShare* shares
     uint64_t* const fresh = mine + 2 * n;
     using T = typename Elem<DT>::T;
     const T* x = static_cast<const T*>(a.logits) + (int64_t)row * a.row_stride;
-    // 16-byte pieces from the row's first aligned address down: `off` elements of piece 0 lie before the row
-    const int off = (int)(((uintptr_t)x & 15) / sizeof(T));
-    const int64_t pieces = ((int64_t)a.vocab + off + VE - 1) / VE;
+    // 16-byte pieces from the row's start, whatever its alignment: rows of equal logits have equal sums
+    const int64_t pieces = ((int64_t)a.vocab + VE - 1) / VE;
     const int64_t tiles = (pieces + TILE / VE - 1) / (TILE / VE);
 
     float m = -INFINITY, s = 0.0f; // of this lane's elements
@@ -247,14 +271,12 @@ __global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a, BeamShare* shares
             for (int i = 0; i < c; i += 64) top = wave_merge(top, ~wave_sort(i + lane < c ? ~fresh[i + lane] : ~0ull));
             if (lane < n) kept[lane] = top;
         } else {
-        for (int i = lane; i < nkept + c; i += 64) {
-            const uint64_t key = i < nkept ? kept[i] : fresh[i - nkept];
+            const uint64_t key = lane < nkept ? kept[lane] : lane < nkept + c ? fresh[lane - nkept] : 0;
             const int rank = keys_above(kept, nkept, key) + keys_above(fresh, c, key);
-            if (rank < n) next[rank] = key;
-        }
-        uint64_t* const swap = kept;
-        kept = next;
-        next = swap;
+            if (key && rank < n) next[rank] = key;
+            uint64_t* const swap = kept;
+            kept = next;
+            next = swap;
         }
         wave_lds_sync();
         nkept = min(n, nkept + c);
@@ -263,16 +285,16 @@ __global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a, BeamShare* shares
     for (int64_t t = share * 4 + wave; t < tiles; t += 4 * nshares) {
         float v[VPL];
         const int64_t p0 = t * (TILE / VE) + lane;
-        auto token = [&](int i) { return (uint32_t)((p0 + (i / VE) * 64) * VE - off + i % VE); };
+        auto token = [&](int i) { return (uint32_t)((p0 + (i / VE) * 64) * VE + i % VE); };
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int64_t e0 = (p0 + i * 64) * VE - off; // the piece's first element
-            if (e0 >= 0 && e0 + VE <= a.vocab) {
-                load_elems<DT, VE>(x + e0, v + i * VE);
+            const int64_t e0 = (p0 + i * 64) * VE; // the piece's first element
+            if (e0 + VE <= a.vocab) {
+                load_piece<DT>(x + e0, v + i * VE);
             } else {
 #pragma unroll
                 for (int j = 0; j < VE; ++j)
-                    v[i * VE + j] = e0 + j >= 0 && e0 + j < a.vocab ? (float)x[e0 + j] : -INFINITY;
+                    v[i * VE + j] = e0 + j < a.vocab ? (float)x[e0 + j] : -INFINITY;
             }
         }
         float lm = -INFINITY;
@@ -372,9 +394,11 @@ __host__ __device__ constexpr size_t beam_join_lds(int waves, int beams, int n)
     return (size_t)waves * n * (sizeof(uint64_t) + sizeof(uint32_t)) + (size_t)beams * n * sizeof(uint32_t);
 }
 
-// A workgroup of a request, a wave of a beam (of two from 17 beams up).  A wave sorts the keys of
-// its beam's shares, 64 at a time, into the beam's candidates, a lane each, and joins its beams;
-// then the waves' lists are joined in pairs.
+// A workgroup of a request, a wave of a beam (of two from 17 beams up).  A wave joins the lists of
+// its beam's shares into the beam's candidates, a lane each, and its beams into one list; then the
+// waves' lists are joined in pairs.  Lists of up to 16 are sorted, 64 keys of several shares at a
+// time; longer ones are merged one by one (28 steps of a network for 64 keys, or 7 for a share:
+// 32 beams of 131071 with nselect 64, 16 shares each, take 21 us, 55 sorted).
 __global__ __launch_bounds__(1024) void k_beam_join(BeamArgs a, const BeamShare* shares, const uint64_t* best, int nshares)
 {
     extern __shared__ __align__(16) uint64_t lds[];
@@ -474,7 +498,7 @@ struct BeamPlan {
 };
 static BeamPlan beam_plan(int64_t rows, int vocab)
 {
-    auto tiles = [&](int lane) { return ((int64_t)vocab + 7 + 256 * lane - 1) / (256 * lane); };
+    auto tiles = [&](int lane) { return ((int64_t)vocab + 256 * lane - 1) / (256 * lane); };
     if (tiles(16) <= kBeamMaxShares && rows * tiles(16) <= 512) return {16, (int)tiles(16)};
     int64_t shares = (1024 + rows - 1) / (rows > 0 ? rows : 1);
     if (shares > tiles(32)) shares = tiles(32);

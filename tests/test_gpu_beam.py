@@ -279,3 +279,23 @@ def test_reorder_refusals():
             call()
     torch.cuda.synchronize()
     assert torch.equal(st.storage, before)
+
+
+@pytest.mark.parametrize("m,v,n", [(32, 131071, 64), (32, 70000, 17), (20, 40000, 33), (17, 9000, 34), (16, 300, 32), (32, 5, 64)])
+def test_many_beams(m, v, n):
+    """Waves with two beams, lists longer than 16, dead and finished beams among them, and ties."""
+    say("many beams", m, v, n)
+    gen = torch.Generator().manual_seed(m + v)
+    logits, scores = draw(gen, 2, m, v, BF)
+    logits[1] = torch.randint(-2, 3, (m, v), generator=gen).to(BF).cuda()  # ties between tokens
+    logits[1, 3:] = logits[1, 2]                                           # and between beams
+    scores[1] = -1.5
+    for dead in (m - 1, 0, m // 2):
+        scores[0, dead] = -math.inf
+        finished = torch.zeros(2, m, dtype=torch.bool, device="cuda")
+        finished[:, 1::5] = True
+        check(logits, scores, n)
+        check(logits, scores, n, finished, pad=4)
+    scores[0] = -math.inf
+    scores[0, m - 2] = 0.0
+    check(logits, scores, n)
