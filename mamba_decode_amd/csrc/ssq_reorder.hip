@@ -5,8 +5,8 @@
 // another one comes from, then writes the sequences that change.  No other thread touches the
 // column, so the move needs no second buffer, no order among threads and each byte is read at
 // most once and written at most once; sequences that keep their place are not touched.  Bytes
-// bound it: 48 int4 layers of 8 x 4 beams (301 MB) take 52-55 us with the non-temporal hint on
-// loads and stores, 5.5-5.8 TB/s, 61-65 us without it on either.
+// bound it: 48 int4 layers of 8 x 4 beams (301 MB) take 50-58 us with the non-temporal hint on
+// loads and stores, 5.2-6.0 TB/s, 61-65 us without it on either.
 #include "ssq_ops_device.h"
 
 namespace ssq {
