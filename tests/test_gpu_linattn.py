@@ -566,3 +566,19 @@ def test_two_calls_at_once():
     torch.cuda.synchronize()
     for w, st, o in zip(want, states, outs):
         assert torch.equal(w[0], values_of(st)) and torch.equal(w[1], o.cpu())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,H,G", [(2, 140, 2), (7, 40, 8), (31, 12, 1), (64, 5, 5), (65, 4, 2), (130, 3, 1)])
+def test_sequences_of_every_length_that_fill_the_card(dtype, n, H, G):
+    """Whole sequences, taken in the order of their lengths up to 64 of them: equal lengths, empty
+    ones, ones that are skipped, the longest anywhere."""
+    say("order of lengths", dtype, n, H)
+    gen = torch.Generator().manual_seed(n)
+    lens = [(0, 1, 64, 65, 5)[i % 5] if i % 2 else int(torch.randint(0, 130, (1,), generator=gen)) for i in range(n)]
+    lens[n // 2] = 200
+    slots = torch.randperm(n + 2, generator=gen)[:n].tolist()
+    if n > 2:
+        slots[1] = -1
+        slots[n - 1] = n + 2
+    prefill_case(dtype, H, G, 16, lens, tail=3, slots=slots, fresh=[i % 3 == 0 for i in range(n)], seed=n, batch=n + 2)
