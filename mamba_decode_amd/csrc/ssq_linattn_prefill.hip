@@ -98,7 +98,7 @@ __device__ __forceinline__ float* seq_rows(const LinArgs& a, int seq, int slot)
 // have it).  Each wave also has the scores of 16 keys; they meet the other waves through LDS.
 //
 // What bounds it: what the waves can issue.  One prompt of 8192 tokens on 128 heads of 64 takes
-// 191 us: 63 for the parts' own states, 12 to join them, 117-127 for the outputs (the
+// 185 us: 62 for the parts' own states, 125 for the outputs, which join them (the
 // 310 MB that have to move take 47 us as a copy, the 47 GFLOP 37 us as a large matrix product).  Of
 // the cycles that a compute unit is busy in the last the matrix pipes take 37%, and a vector instruction every 4 cycles another
 // 48%: decays, roundings to bf16 and their remainders, addresses.  Three workgroups of 64 columns
@@ -269,9 +269,11 @@ constexpr int write_terms() { return MODE == PART_OUT ? 2 : 3; }
 
 struct ChunkArgs {
     LinArgs a;
-    float* part_state;  // [parts][H*P][128]
+    float* part_state;  // [parts][H*P][128], with `fold` also [nseq]: the states before the call
     float2* part_decay; // [parts][H]: keep, change
+    int64_t parts;      // places of parts
     int part_tokens;    // a multiple of kChunk
+    int fold;           // the parts' outputs join the states themselves
     int items;          // sequences, or parts at most
     int blocks;         // column blocks
     int run, runs;      // blocks on an XCD together, and such runs in `blocks`
@@ -295,7 +297,8 @@ __device__ __forceinline__ Rsrc wave_rsrc(const void* base, uint32_t bytes)
 // What a workgroup does: a block of columns of a sequence, or of a part of one.
 struct Work {
     int block, item, seq, slot;
-    bool fresh;
+    bool fresh, last;   // last, part: of a sequence's parts
+    int64_t part;
     int64_t begin, end; // tokens
 };
 
@@ -352,10 +355,99 @@ __device__ __forceinline__ bool find_work(const ChunkArgs& c, Work& w)
     w.end = span.end;
     if constexpr (MODE == WHOLE) return w.begin < w.end || w.fresh;
     const int64_t part = (int64_t)w.item - first_part(c, span.begin, w.seq);
+    w.part = part;
+    w.last = true;
+    if (MODE == PART_OUT && c.fold && part == 0 && w.begin == w.end) return w.fresh; // its state is zeroed
     w.begin += part * c.part_tokens;
     if (part < 0 || w.begin >= w.end) return false; // a place of no part
-    if (w.end > w.begin + c.part_tokens) w.end = w.begin + c.part_tokens;
+    if (w.end > w.begin + c.part_tokens) {
+        w.end = w.begin + c.part_tokens;
+        w.last = false;
+    }
     return true;
+}
+
+// A wave's 16 columns of a state are 8 vectors a lane, vector u the entries 32g + 4u .. 32g + 4u + 3
+// of column l16: in rows in a state, one vector after the other in a part's.
+struct Tile {
+    float* rows; // + 4 floats a vector
+    float* part; // of place 0, + 256 floats a vector
+    int64_t place; // floats from one place to the next
+    const float2* decay; // of place 0, + H
+};
+__device__ __forceinline__ Tile tile_of(const ChunkArgs& c, const Work& w, int head, int64_t col, int lane)
+{
+    const LinArgs& a = c.a;
+    Tile t;
+    t.rows = seq_rows(a, w.seq, w.slot) + (col + (lane & 15)) * 128 + 32 * (lane >> 4);
+    t.part = c.part_state + col * 128 + lane * 4;
+    t.place = (int64_t)a.H * a.P * 128;
+    t.decay = c.part_decay + head;
+    return t;
+}
+__device__ __forceinline__ void load_tile(const float* p, int step, f32x4 (&x)[8])
+{
+#pragma unroll
+    for (int u = 0; u < 8; ++u) x[u] = *reinterpret_cast<const f32x4*>(p + u * step);
+}
+__device__ __forceinline__ void store_tile(float* p, int step, const f32x4 (&x)[8])
+{
+#pragma unroll
+    for (int u = 0; u < 8; ++u) *reinterpret_cast<f32x4*>(p + u * step) = x[u];
+}
+// the state x behind a part with this decay and this own state
+__device__ __forceinline__ f32x4 pass_part(f32x4 x, float2 d, f32x4 own)
+{
+#pragma unroll
+    for (int r = 0; r < 4; ++r) x[r] = __builtin_fmaf(x[r], d.y, x[r] * d.x) + own[r];
+    return x;
+}
+
+// The state that a workgroup starts from.  With `fold` the parts' own states are joined here, part 0's
+// already with the sequence's state before the call, and the last part leaves the state behind them.
+template <int MODE>
+__device__ __forceinline__ void first_state(const ChunkArgs& c, const Work& w, const Tile& t, f32x4 (&x)[8])
+{
+    if constexpr (MODE == WHOLE) {
+        if (!w.fresh) load_tile(t.rows, 4, x);
+        return;
+    }
+    // the join's state, the state before the call, or part 0's
+    const int64_t first = w.item - w.part;
+    const int64_t from = !c.fold ? w.item : w.part == 0 ? c.parts + w.seq : first;
+    if (!(c.fold && w.part == 0 && w.fresh)) load_tile(t.part + from * t.place, 256, x);
+    if (!c.fold) return;
+    for (int64_t p = first + 1; p < w.item; ++p) {
+        f32x4 own[8];
+        load_tile(t.part + p * t.place, 256, own);
+        const float2 d = t.decay[p * c.a.H];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) x[u] = pass_part(x[u], d, own[u]);
+    }
+    if (!w.last) return;
+    if (w.begin == w.end) { // an empty sequence, which is fresh
+#pragma unroll
+        for (int u = 0; u < 8; ++u) *reinterpret_cast<f32x4*>(t.rows + 4 * u) = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        return;
+    }
+    f32x4 own[8];
+    load_tile(t.part + w.item * t.place, 256, own);
+    const float2 d = w.part > 0 ? t.decay[w.item * c.a.H] : float2{0.0f, 0.0f}; // part 0 has the state before it
+#pragma unroll
+    for (int u = 0; u < 8; ++u) *reinterpret_cast<f32x4*>(t.rows + 4 * u) = pass_part(x[u], d, own[u]);
+}
+// what PART_STATE leaves: its own state, part 0's with the state before the call, which is kept aside
+__device__ __forceinline__ void leave_part(const ChunkArgs& c, const Work& w, const Tile& t, float2 d, f32x4 (&x)[8])
+{
+    if (c.fold && w.part == 0 && !w.fresh) {
+        f32x4 s0[8];
+        load_tile(t.rows, 4, s0);
+        store_tile(t.part + (c.parts + w.seq) * t.place, 256, s0);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) *reinterpret_cast<f32x4*>(t.part + w.item * t.place + u * 256) = pass_part(s0[u], d, x[u]);
+    } else {
+        store_tile(t.part + w.item * t.place, 256, x);
+    }
 }
 
 template <int MODE>
@@ -385,15 +477,9 @@ __global__ __launch_bounds__(256, MODE == PART_STATE ? 4 : 3) void k_linattn_chu
     // n-tile t: entries 32g + 4t .. 32g + 4t + 3 of column l16.  A sequence's state is in rows, a
     // part's as the registers hold it.
     f32x4 S[8];
-    float* const tile = (MODE == WHOLE ? seq_rows(a, seq, work.slot) : c.part_state + (int64_t)item * a.H * a.P * 128) + (col0 + wave * 16) * 128;
-    auto state_of = [&](uint32_t l) { return tile + (MODE == WHOLE ? (l & 15) * 128 + (l >> 4) * 32 : l * 4); };
-    constexpr int kStep = MODE == WHOLE ? 4 : 256; // floats from one n-tile to the next
 #pragma unroll
     for (int t = 0; t < 8; ++t) S[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    if (have && MODE != PART_STATE && !(MODE == WHOLE && work.fresh)) {
-#pragma unroll
-        for (int t = 0; t < 8; ++t) S[t] = *reinterpret_cast<const f32x4*>(state_of(lane) + t * kStep);
-    }
+    if (have && MODE != PART_STATE) first_state<MODE>(c, work, tile_of(c, work, head, col0 + wave * 16, lane), S);
     if constexpr (MODE != PART_STATE) { // the scores above the diagonal's tiles stay zero
         constexpr int words = (sizeof(s.p01) + sizeof(s.p23)) / 4;
         for (int i = tid; i < words; i += 256) reinterpret_cast<uint32_t*>(s.p01)[i] = 0;
@@ -599,12 +685,10 @@ __global__ __launch_bounds__(256, MODE == PART_STATE ? 4 : 3) void k_linattn_chu
         }
         if (more) decays(buf ^ 1);
     }
-    if constexpr (MODE != PART_OUT) {
-        if (have) {
-            float* const rows = state_of(here(lane)); // not an address kept through the loop
-#pragma unroll
-            for (int t = 0; t < 8; ++t) *reinterpret_cast<f32x4*>(rows + t * kStep) = S[t];
-        }
+    if (have && MODE != PART_OUT) {
+        const Tile tile = tile_of(c, work, head, col0 + wave * 16, here(lane)); // not addresses kept through the loop
+        if constexpr (MODE == WHOLE) store_tile(tile.rows, 4, S);
+        else leave_part(c, work, tile, decay_of(after), S);
     }
     if constexpr (MODE == PART_STATE) {
         if (tid == 0 && p0 == 0) c.part_decay[(int64_t)item * a.H + head] = decay_of(after);
@@ -650,6 +734,7 @@ __global__ __launch_bounds__(256, 2) void k_linattn_wide(ChunkArgs c)
     using T = typename Elem<DT>::T;
     constexpr int SIZE = sizeof(T), PER = 16 / SIZE; // elements in 16 bytes
     __shared__ WideLds s;
+    __shared__ float2 part_decay;
     const LinArgs& a = c.a;
     Work work;
     if (!find_work<MODE>(c, work)) return;
@@ -668,19 +753,15 @@ __global__ __launch_bounds__(256, 2) void k_linattn_wide(ChunkArgs c)
     T* op = static_cast<T*>(a.o) + col0;
 
     f32x4 S[8]; // S[t][r]: entry 32g + 8r + t of column l16
-    float* rows = nullptr;
-    if constexpr (MODE == WHOLE) rows = seq_rows(a, work.seq, work.slot) + (col0 + wave * 16 + l16) * 128 + 32 * g;
-    else rows = c.part_state + ((int64_t)work.item * a.H * a.P + col0 + wave * 16) * 128 + lane * 4;
-    constexpr int kStep = MODE == WHOLE ? 4 : 256; // floats from four entries to the next four
 #pragma unroll
     for (int t = 0; t < 8; ++t) S[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    if (have && MODE != PART_STATE && !(MODE == WHOLE && work.fresh)) {
+    if (have && MODE != PART_STATE) {
+        f32x4 x[8] = {};
+        first_state<MODE>(c, work, tile_of(c, work, head, col0 + wave * 16, lane), x);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const f32x4 x = *reinterpret_cast<const f32x4*>(rows + u * kStep);
+        for (int u = 0; u < 8; ++u)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) S[u % 2 * 4 + e][u / 2] = x[e];
-        }
+            for (int e = 0; e < 4; ++e) S[u % 2 * 4 + e][u / 2] = x[u][e];
     }
 
     // rows of 128 (q, k) and of 64 (v) in pieces of 16 bytes
@@ -858,19 +939,22 @@ __global__ __launch_bounds__(256, 2) void k_linattn_wide(ChunkArgs c)
         }
         if (more) decays(buf ^ 1);
     }
-    if constexpr (MODE != PART_OUT) {
-        if (have) {
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                f32x4 x;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = S[u % 2 * 4 + e][u / 2];
-                *reinterpret_cast<f32x4*>(rows + u * kStep) = x;
-            }
+    if constexpr (MODE == PART_STATE) { // the part's decay, which wave 3 has
+        if (wave == 3 && lane == 0) {
+            part_decay = decay_of(after);
+            if (p0 == 0) c.part_decay[(int64_t)work.item * a.H + head] = part_decay;
         }
+        __syncthreads();
     }
-    if constexpr (MODE == PART_STATE) {
-        if (wave == 3 && lane == 0 && p0 == 0) c.part_decay[(int64_t)work.item * a.H + head] = decay_of(after);
+    if (have && MODE != PART_OUT) {
+        f32x4 x[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[u][e] = S[u % 2 * 4 + e][u / 2];
+        const Tile tile = tile_of(c, work, head, col0 + wave * 16, lane);
+        if constexpr (MODE == WHOLE) store_tile(tile.rows, 4, x);
+        else leave_part(c, work, tile, part_decay, x);
     }
 }
 
@@ -926,14 +1010,19 @@ struct ChunkPlan {
     int blocks;      // of 64 columns of a head
     int part_tokens; // 0: sequences are not split
     int64_t nparts;
+    bool fold;       // the parts' outputs join the states
 };
 
 // Sequences are split where they and the blocks do not give every compute unit a workgroup (24
-// ragged bf16 prompts of 32 heads, 768 workgroups whole: 84 us; as 384 workgroups of twice the
-// columns 99 us whole and 162 us split), into as many parts as there can be workgroups at once (of
-// three prompts of 32 heads of 128, bf16: 94 us for three workgroups a unit, 104 us for two), of
-// three chunks at least (2048 tokens of 24 heads: the three kernels take 32.4 us, 35.3 in parts
-// of two and 34.3 of four: shorter parts give the join more states to move).
+// ragged bf16 prompts of 32 heads, 768 workgroups whole: 82 us in the order of the call; as 384
+// workgroups of twice the columns 99 us whole and 162 us split), into as many parts as there can be
+// workgroups at once (three prompts of 32 heads of 128, bf16, by a join of its own: 94 us for three
+// workgroups a unit, 104 us for two), of three chunks at least (2048 tokens of 24 heads: 32.2 us,
+// 32.3 in parts of two, 30.0 of four; 512 tokens 18.4, 23.4 of four).
+// Few parts are joined by those who need them, each from the parts before it, more by a launch of
+// its own: 512 tokens of 24 heads 18.4 us against 23.6, three prompts of 32 heads of 128 83 against
+// 93; but 16000 tokens, 32 parts, 107 against 85.  Only the sum of the parts is known here: where
+// four sequences or more share it, 32 are few (five fp32 prompts, 21 parts, 51 us against 57).
 static ChunkPlan chunk_plan(int dtype, int nseq, int64_t tokens, int H, int P, int num_cus)
 {
     ChunkPlan p;
@@ -941,6 +1030,7 @@ static ChunkPlan chunk_plan(int dtype, int nseq, int64_t tokens, int H, int P, i
     p.blocks = H * ((P + kCols - 1) / kCols);
     p.part_tokens = 0;
     p.nparts = 0;
+    p.fold = false;
     const int64_t chunks = (tokens + chunk - 1) / chunk;
     const int64_t slots = (dtype == DT_BF16 ? 3 : 2) * (int64_t)num_cus; // workgroups at once
     if (nseq > 0 && chunks > 2 && nseq * (int64_t)p.blocks < num_cus) {
@@ -948,22 +1038,25 @@ static ChunkPlan chunk_plan(int dtype, int nseq, int64_t tokens, int H, int P, i
         if (per < 3) per = 3;
         p.part_tokens = (int)(per * chunk);
         p.nparts = tokens / p.part_tokens + nseq;
+        p.fold = (tokens + p.part_tokens - 1) / p.part_tokens <= (nseq < 4 ? 16 : 32);
     }
     return p;
 }
 
 static size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-static size_t parts_bytes(const ChunkPlan& p, int H, int P)
+static int64_t part_places(const ChunkPlan& p, int nseq) { return p.nparts + (p.fold ? nseq : 0); }
+
+static size_t parts_bytes(const ChunkPlan& p, int nseq, int H, int P)
 {
-    return (size_t)p.nparts * H * P * 512 + align256((size_t)p.nparts * H * sizeof(float2));
+    return (size_t)part_places(p, nseq) * H * P * 512 + align256((size_t)p.nparts * H * sizeof(float2));
 }
 
 size_t linattn_workspace(int fmt, int nseq, int64_t tokens, int H, int P, int num_cus)
 {
     size_t parts = 0; // of the type that takes most
     for (int dtype : {DT_FP32, DT_BF16, DT_FP16}) {
-        const size_t n = parts_bytes(chunk_plan(dtype, nseq, tokens, H, P, num_cus), H, P);
+        const size_t n = parts_bytes(chunk_plan(dtype, nseq, tokens, H, P, num_cus), nseq, H, P);
         if (n > parts) parts = n;
     }
     return (fmt == FP32 ? 0 : (size_t)nseq * H * P * 512) + parts;
@@ -1003,13 +1096,17 @@ static hipError_t launch_chunks(int dtype, const LinArgs& a, void* ws, int num_c
     if (p.part_tokens == 0) return launch_chunk<WHOLE>(dtype, c, a.nseq, num_cus, st);
     c.part_tokens = p.part_tokens;
     c.part_state = static_cast<float*>(ws);
-    c.part_decay = reinterpret_cast<float2*>(c.part_state + p.nparts * a.H * a.P * 128);
+    c.part_decay = reinterpret_cast<float2*>(c.part_state + part_places(p, a.nseq) * a.H * a.P * 128);
+    c.parts = p.nparts;
+    c.fold = p.fold;
     hipError_t e = launch_chunk<PART_STATE>(dtype, c, p.nparts, num_cus, st);
     if (e != hipSuccess) return e;
-    const int64_t units = (int64_t)a.nseq * a.H * a.P * 32, blocks = (units + 255) / 256;
-    hipLaunchKernelGGL(k_linattn_join, dim3((unsigned)blocks), dim3(256), 0, st, c, units);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (!p.fold) {
+        const int64_t units = (int64_t)a.nseq * a.H * a.P * 32, blocks = (units + 255) / 256;
+        hipLaunchKernelGGL(k_linattn_join, dim3((unsigned)blocks), dim3(256), 0, st, c, units);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
     return launch_chunk<PART_OUT>(dtype, c, p.nparts, num_cus, st);
 }
 

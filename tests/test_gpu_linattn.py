@@ -582,3 +582,14 @@ def test_sequences_of_every_length_that_fill_the_card(dtype, n, H, G):
         slots[1] = -1
         slots[n - 1] = n + 2
     prefill_case(dtype, H, G, 16, lens, tail=3, slots=slots, fresh=[i % 3 == 0 for i in range(n)], seed=n, batch=n + 2)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("lens", [[1025], [0, 700, 0], [0], [193, 192, 191], [0, 5, 900, 64, 0], [3, 4000], [2600, 0, 0, 0, 1],
+                                  [8000, 10, 0, 200, 1]])
+def test_parts_joined_by_those_who_need_them_and_by_a_launch(dtype, lens):
+    """Sequences of few heads, in one part, a few and many, with empty ones, fresh and not."""
+    say("parts", dtype, lens)
+    n = len(lens)
+    for fresh in ([0] * n, [1] * n, [i % 2 for i in range(n)]):
+        prefill_case(dtype, 2, 1, 32, lens, tail=2, slots=list(range(n, 0, -1)), fresh=fresh, seed=sum(lens), batch=n + 1)
