@@ -332,10 +332,10 @@ ssq_status ssq_stream_copy(void *dst, const void *src, size_t bytes, void *strea
  * nothing is read or written.  NULL: i, and nseq <= batch.  Sequences of the
  * state that no slot names are left as they are.  nseq = 0 is an empty call.
  *
- * A value of q, k, v or g that is not finite (g = -infinity apart) leaves the
- * outputs of its call and the state unspecified for its sequence and head (of
- * q and k: for the heads that share it), earlier tokens included; every other
- * sequence and head is computed as usual.
+ * A value of q, k, v, g or the state that is not finite (g = -infinity apart)
+ * leaves the outputs of its call and the state unspecified for its sequence and
+ * head (of q and k: for the heads that share it), earlier tokens included;
+ * every other sequence and head is computed as usual.
  * ------------------------------------------------------------------------ */
 typedef enum { SSQ_DTYPE_FP32 = 0, SSQ_DTYPE_BF16 = 1, SSQ_DTYPE_FP16 = 2 } ssq_dtype;
 
@@ -356,7 +356,8 @@ typedef struct {
 
 /* Bytes of device workspace ssq_linattn_prefill needs for these sizes (0: none);
  * (size_t)-1 if the state is NULL or a delta state, or a size is negative or
- * more than ssq_linattn_prefill takes. */
+ * more than ssq_linattn_prefill takes.  It does not always grow with them: a
+ * workspace for several sizes is as large as the largest of their answers. */
 size_t ssq_linattn_workspace(const ssq_state *state, int32_t nseq, int64_t tokens);
 
 /* Prompts, one after the other in `tokens` rows: sequence i has the tokens

@@ -97,14 +97,15 @@ __device__ __forceinline__ float* seq_rows(const LinArgs& a, int seq, int slot)
 // at once the operand of the next S q (any order of the summed index serves, if both operands
 // have it).  Each wave also has the scores of 16 keys; they meet the other waves through LDS.
 //
-// What bounds it: what the waves can issue.  One prompt of 8192 tokens on 128 heads of 64 takes
-// 185 us: 62 for the parts' own states, 125 for the outputs, which join them (the
-// 310 MB that have to move take 47 us as a copy, the 47 GFLOP 37 us as a large matrix product).  Of
-// the cycles that a compute unit is busy in the last the matrix pipes take 37%, and a vector instruction every 4 cycles another
-// 48%: decays, roundings to bf16 and their remainders, addresses.  Three workgroups of 64 columns
-// on a compute unit, 12 waves, against two of 128 columns (two tiles a wave, each fragment of q and k
-// read once for both): 24 ragged prompts of 32 heads 84 us against 99, since what one wave waits for
-// the others fill.  HBM is not a bound: those prompts move 125 MB, 1.5 TB/s.
+// What bounds it: the chain of each wave and what the waves of a SIMD can issue.  One prompt of 8192
+// tokens on 128 heads of 64 takes 185 us: 62 for the parts' own states, 125 for the outputs, which
+// join them (the 310 MB that have to move take 47 us as a copy, the 47 GFLOP 37 us as a large matrix
+// product).  In the last the matrix pipes are busy 31% of the cycles and vector instructions (decays,
+// roundings to bf16 and their remainders, addresses), at 4 cycles each, take 40%; in the rest the
+// three waves of a SIMD wait for LDS and at barriers.  Three workgroups of 64 columns on a compute
+// unit, 12 waves, against two of 128 columns (two tiles a wave, each fragment of q and k read once for
+// both): 24 ragged prompts of 32 heads 84 us against 99, since what one wave waits for the others
+// fill.  HBM is not a bound: those prompts move 125 MB in 70 us.
 constexpr int kChunk = 64;
 constexpr int kCols = 64;
 constexpr int kPitch = 136;      // bf16 of a row of 128 in LDS: 16-byte reads of 16 rows fall in different banks
