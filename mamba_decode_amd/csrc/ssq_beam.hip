@@ -92,12 +92,12 @@ __device__ __forceinline__ uint64_t wave_nth(uint64_t key, int n, uint64_t* room
     return at ? shfl_u64(key, __builtin_ctzll(at)) : 0;
 }
 
-// key of lane ^ D
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_u32(uint32_t x)
 {
     return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xF, 0xF, true);
 }
+// the value of lane ^ D
 template <int D>
 __device__ __forceinline__ uint32_t xor_u32(uint32_t x)
 {

@@ -461,7 +461,7 @@ __global__ __launch_bounds__(256, MODE == PART_STATE ? 4 : 3) void k_linattn_chu
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     Work work;
     if (!find_work<MODE>(c, work)) return;
-    const int block = work.block, item = work.item, seq = work.seq;
+    const int block = work.block, item = work.item;
     const int64_t begin = work.begin, end = work.end;
     const int per_head = (a.P + kCols - 1) / kCols;
     const int head = block / per_head, p0 = block % per_head * kCols;

@@ -32,7 +32,6 @@ struct LinArgs {
     SrArgs sr;
 };
 
-constexpr int kMaxBeams = 32;
 
 // Sizes are refused before anything is enqueued where a launch would have 2^32 work-items or more:
 // workgroups of 256, state rows of a token step (16 a wave) and of a prompt (16 a column block, and
