@@ -95,7 +95,11 @@ __device__ __forceinline__ float* seq_rows(const LinArgs& a, int seq, int slot)
 // of them and keeps their state, 16 x 128 fp32, in registers, laid out as a matrix product leaves
 // it: lane (g, c) = (lane/16, lane%16) holds column c and the key entries 32g .. 32g+31, which is
 // at once the operand of the next S q (any order of the summed index serves, if both operands
-// have it).  Each wave also has the scores of 16 keys; they meet the other waves through LDS.
+// have it).  Each wave also has the scores of 16 keys; they meet the other waves through LDS, the
+// first terms in a place of their own and the second ones, once q has been read, in q's: room for
+// both would cost the third workgroup of a compute unit.  The barrier between is behind the state's
+// products, so that few waves wait there (ragged prompts 76 us, 79 with it in front of them; 69 with
+// one term).
 //
 // What bounds it: the chain of each wave and what the waves of a SIMD can issue.  One prompt of 8192
 // tokens on 128 heads of 64 takes 185 us: 62 for the parts' own states, 125 for the outputs, which
@@ -165,7 +169,10 @@ struct alignas(16) ChunkLds {
     __bf16 k[kChunk][kPitch];
     __bf16 v[kChunk][kColPitch];
     WriteDecay w[2]; // of this chunk and the next
-    __bf16 q[kChunk][kPitch];
+    union {
+        __bf16 q[kChunk][kPitch];
+        __bf16 low[kChunk][kColPitch]; // once q has been read: what p01 and p23 leave of the scores
+    };
     __bf16 p01[32][kScorePitch]; // decayed scores, [query][key]: the queries 0 .. 31 have no later keys
     __bf16 p23[32][kColPitch];
     ReadDecay d;
@@ -240,7 +247,7 @@ __device__ __forceinline__ void chunk_decays(int wave, float g, float scale, int
     const double r = row_sums(log2_decay(g)), c = wave_sums(r);
     if (wave == 0) {
         d.r[lane] = (float)r;
-        d.row[lane] = scale * __builtin_amdgcn_exp2f((float)r); // scores are rounded to bf16: a few units of fp32 do
+        d.row[lane] = scale * __builtin_amdgcn_exp2f((float)r); // scores stand as two terms of bf16: a few units of fp32 do
     } else if (wave == 1) {
 #pragma unroll
         for (int i = 0; i < 3; ++i)
@@ -259,8 +266,10 @@ __device__ __forceinline__ void chunk_decays(int wave, float g, float scale, int
 
 enum { WHOLE = 0, PART_STATE = 1, PART_OUT = 2 };
 
-// Terms of bf16 that stand for an fp32 operand.  The state as S q reads it, where o is rounded to
-// bf16 in the end: two (one would add an error as large as that rounding).  The decayed values that
+// Terms of bf16 that stand for an fp32 operand, each leaving 2^-8 of what the one before left.  The
+// state as S q reads it and the decayed scores as v meets them: two, off by 2^-16 of each term of an
+// output, so that o is exact to its own rounding (one term would add an error as large as that
+// rounding, and many times it where the terms of an output cancel).  The decayed values that
 // are added to a state which is kept: three, all 24 bits (two leave 2e-6 of the state, as much as
 // a chain of fp32 sums; 128 heads x 8192 tokens take 7% less time with them); two where the state
 // only serves to the end of a part.
@@ -489,7 +498,7 @@ __global__ __launch_bounds__(256, MODE == PART_STATE ? 4 : 3) void k_linattn_chu
     // Tiles come and go through buffer descriptors that end with the span: rows behind it read 0
     // and are not written.  16 pieces of 16 bytes a row of q and k, 8 of v.
     const uint32_t piece = tid & 15, prow = tid >> 4, vpiece = tid & 7, vrow = tid >> 3;
-    const uint32_t q_row = (uint32_t)a.qs * 2, k_row = (uint32_t)a.ks * 2, v_row = (uint32_t)a.vs * 2, o_row = (uint32_t)a.os * 2;
+    const uint32_t q_row = (uint32_t)a.qs * 2, k_row = (uint32_t)a.ks * 2, v_row = (uint32_t)a.vs * 2, o_row = (uint32_t)a.os * 2, g_row = (uint32_t)a.gs * 4;
     const uint32_t q_off = prow * q_row + piece * 16, k_off = prow * k_row + piece * 16;
     constexpr uint32_t kNone = 0x80000000u; // behind every range
     const uint32_t v_off = (int)vpiece * 8 < cols ? vrow * v_row + vpiece * 16 : kNone;
@@ -513,8 +522,9 @@ __global__ __launch_bounds__(256, MODE == PART_STATE ? 4 : 3) void k_linattn_chu
         const Rsrc bk = wave_rsrc(kp + t0 * a.ks, rows_of(t0) * k_row + 256);
         const Rsrc bv = wave_rsrc(vp + t0 * a.vs, rows_of(t0) * v_row + cols * 2);
         const uint32_t k_at = here(k_off), v_at = here(v_off);
-        rg = 0.0f;
-        if (a.g && t0 + lane < end) rg = a.g[(t0 + lane) * a.gs + head];
+        const Rsrc bg = a.g ? wave_rsrc(a.g + t0 * a.gs + head, rows_of(t0) * g_row + 4) : wave_rsrc(nullptr, 0);
+        const uint32_t g_at = (uint32_t)lane <= rows_of(t0) ? lane * g_row : kNone; // a stride of 0 has no row behind the span
+        rg = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(bg, g_at, 0, 0));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             rk[i] = __builtin_amdgcn_raw_buffer_load_b128(bk, k_at + 16 * i * k_row, 0, 0);
@@ -591,10 +601,12 @@ __global__ __launch_bounds__(256, MODE == PART_STATE ? 4 : 3) void k_linattn_chu
                     for (int i = 0; i < 4; ++i) O[i] = mfma(term[j], qq[i], O[i]);
             }
             const int kj = wave * 16 + g * 4;
+            bf16x4 low[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int qi = i * 16 + l16;
                 f32x4 w;
+                low[i] = bf16x4{};
                 if (i < wave) continue;
                 if (i == wave) {
                     const f32x4 rj = *reinterpret_cast<const f32x4*>(&s.d.r[kj]);
@@ -608,10 +620,15 @@ __global__ __launch_bounds__(256, MODE == PART_STATE ? 4 : 3) void k_linattn_chu
                 const bf16x2 w01 = to_bf16(w.x, w.y), w23 = to_bf16(w.z, w.w);
                 __bf16* const p = i < 2 ? &s.p01[qi][kj] : &s.p23[qi - 32][kj];
                 *reinterpret_cast<bf16x4*>(p) = __builtin_shufflevector(w01, w23, 0, 1, 2, 3);
+                const f32x2 f01 = from_bf16(w01), f23 = from_bf16(w23);
+                low[i] = __builtin_shufflevector(to_bf16(w.x - f01.x, w.y - f01.y), to_bf16(w.z - f23.x, w.w - f23.y), 0, 1, 2, 3);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) O[i] *= s.d.in[i * 16 + l16];
-            __syncthreads(); // the scores are written, and the decays that they took are read
+            __syncthreads(); // the scores are written, q and the decays that they took are read
+#pragma unroll
+            for (int i = 0; i < 4; ++i) // a tile above the diagonal that shares a product with one on it is zero
+                if (i >= (wave & ~1)) *reinterpret_cast<bf16x4*>(&s.low[i * 16 + l16][kj]) = low[i];
         }
         if (more) fetch_q(start(n + 1)); // not sooner: its registers are S q's operands till here
         bf16x8 vf[2]; // this wave's columns of v: column l16, tokens 32*kb + 8g .. +7
@@ -627,6 +644,62 @@ __global__ __launch_bounds__(256, MODE == PART_STATE ? 4 : 3) void k_linattn_chu
 #pragma unroll
             for (int i = 2; i < 4; ++i)
                 O[i] = mfma(vf[1], *reinterpret_cast<const bf16x8*>(&s.p23[i * 16 - 32 + l16][32 + g * 8]), O[i]);
+        }
+        if (MODE != PART_OUT || more) { // the next part has its own state
+            // the state: decayed, and the chunk's writes with v's decay, as a sum of bf16
+            if constexpr (MODE != PART_STATE) {
+                const float change = sw.change;
+                if (__builtin_amdgcn_readfirstlane(__float_as_int(sw.keep)) != 0) {
+#pragma unroll
+                    for (int t = 0; t < 8; ++t)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) S[t][r] = __builtin_fmaf(S[t][r], change, S[t][r]);
+                } else {
+#pragma unroll
+                    for (int t = 0; t < 8; ++t) S[t] *= change;
+                }
+            }
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                const float* od = &sw.out[kb * 32 + g * 8];
+                const f32x4 o0 = *reinterpret_cast<const f32x4*>(od), o1 = *reinterpret_cast<const f32x4*>(od + 4);
+                const float oe[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
+                bf16x8 term[write_terms<MODE>()];
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    f32x2 v = from_bf16(bf16x2{vf[kb][e], vf[kb][e + 1]});
+                    v.x *= oe[e];
+                    v.y *= oe[e + 1];
+#pragma unroll
+                    for (int j = 0; j < write_terms<MODE>(); ++j) {
+                        const bf16x2 h = to_bf16(v.x, v.y);
+                        const f32x2 f = from_bf16(h);
+                        term[j][e] = h.x;
+                        term[j][e + 1] = h.y;
+                        v.x -= f.x;
+                        v.y -= f.y;
+                    }
+                }
+                const int row = kb * 32 + g * 8 + (l16 >> 2), col = (l16 & 3) * 32;
+#pragma unroll
+                for (int t = 0; t < 8; t += 4) {
+                    bf16x8 kf[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        kf[u] = join4(lds_read_tr(&s.k[row][col + 4 * (t + u)]), lds_read_tr(&s.k[row + 4][col + 4 * (t + u)]));
+#pragma unroll
+                    for (int j = 0; j < write_terms<MODE>(); ++j)
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) S[t + u] = mfma(kf[u], term[j], S[t + u]);
+                }
+            }
+        }
+        if constexpr (MODE != PART_STATE) {
+            __syncthreads(); // the scores' second terms are written
+#pragma unroll
+            for (int i = 0; i < 4; ++i) O[i] = mfma(vf[0], *reinterpret_cast<const bf16x8*>(&s.low[i * 16 + l16][g * 8]), O[i]);
+#pragma unroll
+            for (int i = 2; i < 4; ++i) O[i] = mfma(vf[1], *reinterpret_cast<const bf16x8*>(&s.low[i * 16 + l16][32 + g * 8]), O[i]);
             const uint32_t last = (uint32_t)(end - t0 < kChunk ? end - t0 : kChunk) - 1;
             const Rsrc bo = wave_rsrc(op + t0 * a.os, last * o_row + cols * 2);
             const uint32_t o_at = here(o_off);
@@ -634,54 +707,6 @@ __global__ __launch_bounds__(256, MODE == PART_STATE ? 4 : 3) void k_linattn_chu
             for (int i = 0; i < 4; ++i) {
                 const u32x2 w4 = {__builtin_bit_cast(uint32_t, to_bf16(O[i].x, O[i].y)), __builtin_bit_cast(uint32_t, to_bf16(O[i].z, O[i].w))};
                 __builtin_amdgcn_raw_buffer_store_b64(w4, bo, o_at + i * 16 * o_row, 0, 0);
-            }
-        }
-        if (MODE == PART_OUT && !more) break; // the next part has its own state
-        // the state: decayed, and the chunk's writes with v's decay, as a sum of bf16
-        if constexpr (MODE != PART_STATE) {
-            const float change = sw.change;
-            if (__builtin_amdgcn_readfirstlane(__float_as_int(sw.keep)) != 0) {
-#pragma unroll
-                for (int t = 0; t < 8; ++t)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) S[t][r] = __builtin_fmaf(S[t][r], change, S[t][r]);
-            } else {
-#pragma unroll
-                for (int t = 0; t < 8; ++t) S[t] *= change;
-            }
-        }
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            const float* od = &sw.out[kb * 32 + g * 8];
-            const f32x4 o0 = *reinterpret_cast<const f32x4*>(od), o1 = *reinterpret_cast<const f32x4*>(od + 4);
-            const float oe[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
-            bf16x8 term[write_terms<MODE>()];
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                f32x2 v = from_bf16(bf16x2{vf[kb][e], vf[kb][e + 1]});
-                v.x *= oe[e];
-                v.y *= oe[e + 1];
-#pragma unroll
-                for (int j = 0; j < write_terms<MODE>(); ++j) {
-                    const bf16x2 h = to_bf16(v.x, v.y);
-                    const f32x2 f = from_bf16(h);
-                    term[j][e] = h.x;
-                    term[j][e + 1] = h.y;
-                    v.x -= f.x;
-                    v.y -= f.y;
-                }
-            }
-            const int row = kb * 32 + g * 8 + (l16 >> 2), col = (l16 & 3) * 32;
-#pragma unroll
-            for (int t = 0; t < 8; t += 4) {
-                bf16x8 kf[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    kf[u] = join4(lds_read_tr(&s.k[row][col + 4 * (t + u)]), lds_read_tr(&s.k[row + 4][col + 4 * (t + u)]));
-#pragma unroll
-                for (int j = 0; j < write_terms<MODE>(); ++j)
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) S[t + u] = mfma(kf[u], term[j], S[t + u]);
             }
         }
         if (more) decays(buf ^ 1);

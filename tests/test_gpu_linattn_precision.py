@@ -1,0 +1,63 @@
+"""GPU: how exact linear attention on prompts is, beyond what its other tests ask.
+
+Bounds, each relative to the sum of the absolute values of a result's terms, which the reference
+computes beside it.  A product's operand that stands as two bf16 terms is off by 2^-16: 2^-8 of it is
+left by the first rounding, and 2^-8 of that by the second.  An output meets that three times at
+most: the decayed scores as v meets them or the state as q reads it, and what a part of a split
+sequence writes into its own state.  Sums and decays are fp32 or wider, by ``sum_bound``.  The
+output is rounded once to its type, half a step of the value."""
+import math
+import sys
+
+import pytest
+import torch
+
+from tests import linattn_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import mamba_decode_amd as ssq
+    from tests.test_gpu_linattn import BF, F32, HF, cu_of, state_of, sum_bound, values_of
+
+
+def say(*a):
+    print(*a, file=sys.stderr, flush=True)
+
+
+def run(q, k, v, g, lens, G, start, scale):
+    st = state_of(start, G)
+    o = torch.zeros_like(v).cuda()
+    ssq.ssq_linattn_prefill(st, q.cuda(), k.cuda(), v.cuda(), g.cuda(), o, cu_of(lens), scale=scale)
+    o, state, at, want = o.cpu(), values_of(st), 0, []
+    for i, n in enumerate(lens):
+        want.append(ref.recurrence(*(x[at:at + n] for x in (q, k, v, g)), start[i], scale))
+        at += n
+    return o, state, want
+
+
+def check_rounded_once(o, wo, om, T, where):
+    tol = om * (3 * 2.0 ** -16 + sum_bound(T)) * 1.01 + wo.abs() * (torch.finfo(o.dtype).eps / 2) + torch.finfo(o.dtype).tiny
+    off = (o.double() - wo).abs() / tol
+    assert (off <= 1).all(), f"{where}: {int((off > 1).sum())} of {off.numel()} outputs off, the worst {off.max():.1f} times its bound"
+
+
+@pytest.mark.parametrize("H,G,P,lens", [(24, 1, 64, [300, 77]), (2, 2, 128, [2000]), (40, 4, 48, [64, 130, 1, 65, 200, 90, 16]),
+                                        (1, 1, 16, [1000, 33])])
+def test_outputs_of_bf16_prompts_are_rounded_once(H, G, P, lens):
+    """Scores that meet v in bf16 alone are off by 2^-8 each, many steps of an output whose terms cancel."""
+    say("rounded once", H, G, P, lens)
+    gen = torch.Generator().manual_seed(H + P)
+    q, k, v, g = ref.inputs(gen, sum(lens), H, G, P, BF)
+    o, _, want = run(q, k, v, g, lens, G, torch.randn(len(lens), H, P, 128, generator=gen), 0.3)
+    at, off, once, norm = 0, 0.0, 0.0, 0.0
+    for n, (wo, _, om, _) in zip(lens, want):
+        check_rounded_once(o[at:at + n], wo, om, n, f"{n} tokens")
+        off += (o[at:at + n].double() - wo).square().sum().item()
+        once += (wo.to(BF).double() - wo).square().sum().item()
+        norm += wo.square().sum().item()
+        at += n
+    # what comes before the rounding adds to it in squares: 2^-16 of terms whose sum of absolute values is some
+    # 10 times the result, against 2^-9.2 of the result itself, is less than 1% of it
+    say(f"  off by {math.sqrt(off / norm):.6f}, one rounding {math.sqrt(once / norm):.6f}")
+    assert math.sqrt(off) <= 1.02 * math.sqrt(once)
