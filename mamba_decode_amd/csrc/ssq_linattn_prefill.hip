@@ -154,7 +154,8 @@ __device__ __forceinline__ f32x2 from_bf16(bf16x2 v)
 // Decays of a chunk.  r_i is the sum of g, in powers of two, over the tokens of i's tile of 16 up
 // to i, c_i the sum over the chunk.
 struct alignas(16) ReadDecay {
-    float r[kChunk];   // r_i: scores of a tile on the diagonal decay by exp2(r_i - r_j) ...
+    float r[kChunk], rlo[kChunk]; // r_i as two floats (behind tokens that forget it is some -2000, and
+                                  // one would be off by 2^-13): scores on the diagonal decay by exp2(r_i - r_j) ...
     float row[kChunk]; // ... and off it by scale * exp2(r_i) ...
     float col[96];     // ... times exp2(c - c_j) with c before the tile of i: 16 keys for tile 1, 32 for 2, 48 for 3
     float in[kChunk];  // scale * exp2(c_i)
@@ -164,7 +165,7 @@ struct alignas(16) WriteDecay {
     float keep, change; // exp2(c_last) x = keep*x + change*x, keep 0 or 1: exact near 1
 };
 
-// 52,896 bytes: three workgroups on a compute unit
+// 53,152 bytes: three workgroups on a compute unit
 struct alignas(16) ChunkLds {
     __bf16 k[kChunk][kPitch];
     __bf16 v[kChunk][kColPitch];
@@ -246,12 +247,14 @@ __device__ __forceinline__ void chunk_decays(int wave, float g, float scale, int
 {
     const double r = row_sums(log2_decay(g)), c = wave_sums(r);
     if (wave == 0) {
-        d.r[lane] = (float)r;
-        d.row[lane] = scale * __builtin_amdgcn_exp2f((float)r); // scores stand as two terms of bf16: a few units of fp32 do
+        const float hi = (float)r;
+        d.r[lane] = hi;
+        d.rlo[lane] = (float)(r - (double)hi);
+        d.row[lane] = scale * exp2_of(r);
     } else if (wave == 1) {
 #pragma unroll
         for (int i = 0; i < 3; ++i)
-            if (lane < 16 * (i + 1)) d.col[8 * i * (i + 1) + lane] = __builtin_amdgcn_exp2f((float)(readlane_d(c, 16 * i + 15) - c));
+            if (lane < 16 * (i + 1)) d.col[8 * i * (i + 1) + lane] = exp2_of(readlane_d(c, 16 * i + 15) - c);
     } else if (wave == 2) {
         d.in[lane] = scale * exp2_of(c);
         if (lane == 63) {
@@ -609,11 +612,11 @@ __global__ __launch_bounds__(256, MODE == PART_STATE ? 4 : 3) void k_linattn_chu
                 low[i] = bf16x4{};
                 if (i < wave) continue;
                 if (i == wave) {
-                    const f32x4 rj = *reinterpret_cast<const f32x4*>(&s.d.r[kj]);
-                    const float ri = s.d.r[qi];
+                    const f32x4 rj = *reinterpret_cast<const f32x4*>(&s.d.r[kj]), lj = *reinterpret_cast<const f32x4*>(&s.d.rlo[kj]);
+                    const float ri = s.d.r[qi], li = s.d.rlo[qi];
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        w[r] = kj + r <= qi ? A[i][r] * (a.oscale * __builtin_amdgcn_exp2f(ri - rj[r])) : 0.0f;
+                        w[r] = kj + r <= qi ? A[i][r] * (a.oscale * __builtin_amdgcn_exp2f((ri - rj[r]) + (li - lj[r]))) : 0.0f;
                 } else {
                     w = A[i] * s.d.row[qi] * *reinterpret_cast<const f32x4*>(&s.d.col[8 * i * (i - 1) + kj]);
                 }

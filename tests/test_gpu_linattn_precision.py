@@ -36,8 +36,8 @@ def run(q, k, v, g, lens, G, start, scale):
     return o, state, want
 
 
-def check_rounded_once(o, wo, om, T, where):
-    tol = om * (3 * 2.0 ** -16 + sum_bound(T)) * 1.01 + wo.abs() * (torch.finfo(o.dtype).eps / 2) + torch.finfo(o.dtype).tiny
+def check_rounded_once(o, wo, om, T, where, pairs=3):
+    tol = om * (pairs * 2.0 ** -16 + sum_bound(T)) * 1.01 + wo.abs() * (torch.finfo(o.dtype).eps / 2) + torch.finfo(o.dtype).tiny
     off = (o.double() - wo).abs() / tol
     assert (off <= 1).all(), f"{where}: {int((off > 1).sum())} of {off.numel()} outputs off, the worst {off.max():.1f} times its bound"
 
@@ -61,3 +61,30 @@ def test_outputs_of_bf16_prompts_are_rounded_once(H, G, P, lens):
     # 10 times the result, against 2^-9.2 of the result itself, is less than 1% of it
     say(f"  off by {math.sqrt(off / norm):.6f}, one rounding {math.sqrt(once / norm):.6f}")
     assert math.sqrt(off) <= 1.02 * math.sqrt(once)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+@pytest.mark.parametrize("T", [16, 47, 300])
+def test_decays_behind_tokens_that_forget(dtype, T):
+    """A decay between two tokens is the difference of two sums of log decays.  Behind 13 tokens that
+    forget all (e^-128 is 0) these are some -2400 in powers of two: rounded to fp32 each is off by up
+    to 2^-13, and the decay by as much of itself, where 2^-22 is asked.  Of the three tokens that
+    follow each writes the opposite of the one before it, so that an output is little but the
+    difference of their decays.  Nothing comes through a state: scores alone stand as two terms."""
+    say("behind tokens that forget", dtype, T)
+    gen = torch.Generator().manual_seed(T)
+    H, G, P = 12, 2, 64
+    q, _, v, _ = ref.inputs(gen, T, H, G, P, dtype)
+    q[:] = q[:1]
+    t = torch.arange(T)
+    for i in (14, 15):
+        v[t % 16 == i] = -v[t % 16 == i - 1][: int((t % 16 == i).sum())]
+    g = -0.01 * torch.rand(T, H, generator=gen)
+    g[t % 16 < 13] -= 150.0
+    o, _, want = run(q, q, v, g, [T], G, torch.zeros(1, H, P, 128), 1.0)
+    wo, _, om, _ = want[0]
+    if dtype == F32:
+        off = (o.double() - wo).abs() / (sum_bound(T) * om)
+        assert (off <= 1).all(), f"the worst {off.max():.1f} times its bound"
+    else:
+        check_rounded_once(o, wo, om, T, "behind tokens that forget", pairs=1)
