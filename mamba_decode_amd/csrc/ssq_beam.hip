@@ -261,7 +261,10 @@ __global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a, BeamShare* shares
     const int64_t pieces = ((int64_t)a.vocab + VE - 1) / VE;
     const int64_t tiles = (pieces + TILE / VE - 1) / (TILE / VE);
 
-    float m = -INFINITY, s = 0.0f; // of this lane's elements
+    // of this lane's elements; the sum over tiles is a double: a lane of the longest rows has thousands of
+    // them, and one rounding to fp32 after the other, of alike addends, has a drift (2e-5 at 2^28 tokens)
+    float m = -INFINITY;
+    double s = 0.0;
     int nkept = 0;
     float last = -INFINITY;        // the n-th best so far; -inf while there are fewer
     auto merge = [&](int c) { // the new keys and the kept ones: the best n are kept
@@ -307,7 +310,7 @@ __global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a, BeamShare* shares
         float part = 0.0f;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) part += __expf(v[i] - shift);
-        s = s * __expf(m - shift) + part;
+        s = s * (double)__expf(m - shift) + (double)part;
         m = wm;
         // tiles come in the order of their tokens: an element equal to the last kept one comes behind it
         if (!__ballot(lm > last)) continue;
@@ -355,12 +358,12 @@ __global__ __launch_bounds__(256) void k_beam_rows(BeamArgs a, BeamShare* shares
     }
     // the four waves' lists, each at the front of the wave's LDS, 0 behind its last key
     const float wm = wave_max(m);
-    s = wave_sum(m > -INFINITY ? s * __expf(m - wm) : 0.0f);
+    const float of_wave = wave_sum(m > -INFINITY ? (float)s * __expf(m - wm) : 0.0f);
     wave_lds_sync();
     uint64_t top = lane < nkept ? kept[lane] : 0;
     wave_lds_sync();
     if (lane < n) mine[lane] = top;
-    if (lane == 0) wave_share[wave] = {wm, s};
+    if (lane == 0) wave_share[wave] = {wm, of_wave};
     __syncthreads();
     if (wave != 0) return;
     for (int w = 1; w < 4; ++w) top = wave_merge(top, 63 - lane < n ? lds[w * beam_wave_keys(n) + 63 - lane] : 0);
