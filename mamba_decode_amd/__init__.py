@@ -417,6 +417,13 @@ def _workspace(given, need: int, stream, dev: int):
     return ws, ws.data_ptr(), need
 
 
+def _int32(x, name: str) -> int:
+    """A number that ctypes would otherwise take modulo 2^32."""
+    if not -0x80000000 <= x <= 0x7FFFFFFF:
+        raise ValueError(f"{name} is {x}, which 32 bits do not hold")
+    return x
+
+
 def _linattn_io(state: State, q, k, v, g, o, scale: float, tokens: int, dev: int):
     d = state.desc
     if d.kind != SSQ_MAMBA2:
@@ -438,7 +445,9 @@ def _linattn_io(state: State, q, k, v, g, o, scale: float, tokens: int, dev: int
 
 def ssq_linattn_workspace(state: State, nseq: int, tokens: int) -> int:
     """Bytes of workspace ``ssq_linattn_prefill`` needs for these sizes."""
-    n = lib.ssq_linattn_workspace(state.handle, nseq, tokens)
+    if tokens >= 1 << 63:
+        raise ValueError("tokens is more than 63 bits hold")
+    n = lib.ssq_linattn_workspace(state.handle, _int32(nseq, "nseq"), tokens)
     if n == _SIZE_MAX:
         raise ValueError("linear attention runs on an SSQ_MAMBA2 state, sizes must not be negative")
     return n
@@ -477,7 +486,8 @@ def ssq_linattn_step(state: State, q, k, v, g, o, slots=None, scale: float = 1.0
     nseq = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() else 0
     io = _linattn_io(state, q, k, v, g, o, scale, nseq, dev)
     sp = None if slots is None else _ptr(slots, "slots", torch.int32, (nseq,), dev)
-    _check(lib.ssq_linattn_step(state.handle, io, nseq, sp, readout, _stream_ptr(stream, dev)), "ssq_linattn_step")
+    _check(lib.ssq_linattn_step(state.handle, io, _int32(nseq, "nseq"), sp, _int32(readout, "readout"),
+                                _stream_ptr(stream, dev)), "ssq_linattn_step")
 
 
 def ssq_beam_workspace(desc: ssq_beam_desc) -> int:
@@ -510,7 +520,8 @@ def ssq_beam_select(logits, scores, out_scores, out_tokens, out_parents, finishe
     osp = _ptr(out_scores, "out_scores", torch.float32, (b, n), dev)
     otp = _ptr(out_tokens, "out_tokens", torch.int32, (b, n), dev)
     opp = _ptr(out_parents, "out_parents", torch.int32, (b, n), dev)
-    d = ssq_beam_desc(_DTYPES[logits.dtype], b, m, v, n, pad_token, row)
+    d = ssq_beam_desc(_DTYPES[logits.dtype], _int32(b, "batch"), _int32(m, "beams"), _int32(v, "vocab"),
+                      _int32(n, "nselect"), _int32(pad_token, "pad_token"), row)
     ws, wp, wn = _workspace(workspace, lib.ssq_beam_workspace(d), stream, dev)
     _check(lib.ssq_beam_select(d, logits.data_ptr(), sp, fp, osp, otp, opp, wp, wn, _stream_ptr(stream, dev)),
            "ssq_beam_select")
