@@ -359,7 +359,11 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 def _stream_ptr(stream, dev: int) -> int:
     if stream is None:
         return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if not hasattr(stream, "cuda_stream"):
+        return int(stream)
+    if getattr(getattr(stream, "device", None), "index", dev) != dev:  # its kernels would run there, on this device's memory
+        raise ValueError("stream must be one of the current CUDA device")
+    return stream.cuda_stream
 
 
 def _refuse(t, name: str, dtype, shape, dev: int):
@@ -473,9 +477,9 @@ def ssq_linattn_prefill(state: State, q, k, v, g, o, cu_seqlens, slots=None, fre
     cu = _ptr(cu_seqlens, "cu_seqlens", torch.int32, (nseq + 1,), dev)
     sp = None if slots is None else _ptr(slots, "slots", torch.int32, (nseq,), dev)
     fp = _flags(fresh, "fresh", (nseq,), dev)
+    on = _stream_ptr(stream, dev)
     ws, wp, wn = _workspace(workspace, ssq_linattn_workspace(state, nseq, tokens), stream, dev)
-    _check(lib.ssq_linattn_prefill(state.handle, io, nseq, tokens, cu, sp, fp, wp, wn, _stream_ptr(stream, dev)),
-           "ssq_linattn_prefill")
+    _check(lib.ssq_linattn_prefill(state.handle, io, nseq, tokens, cu, sp, fp, wp, wn, on), "ssq_linattn_prefill")
 
 
 def ssq_linattn_step(state: State, q, k, v, g, o, slots=None, scale: float = 1.0, readout: int = SSQ_READ_POST_QUANT,
@@ -522,9 +526,9 @@ def ssq_beam_select(logits, scores, out_scores, out_tokens, out_parents, finishe
     opp = _ptr(out_parents, "out_parents", torch.int32, (b, n), dev)
     d = ssq_beam_desc(_DTYPES[logits.dtype], _int32(b, "batch"), _int32(m, "beams"), _int32(v, "vocab"),
                       _int32(n, "nselect"), _int32(pad_token, "pad_token"), row)
+    on = _stream_ptr(stream, dev)
     ws, wp, wn = _workspace(workspace, lib.ssq_beam_workspace(d), stream, dev)
-    _check(lib.ssq_beam_select(d, logits.data_ptr(), sp, fp, osp, otp, opp, wp, wn, _stream_ptr(stream, dev)),
-           "ssq_beam_select")
+    _check(lib.ssq_beam_select(d, logits.data_ptr(), sp, fp, osp, otp, opp, wp, wn, on), "ssq_beam_select")
 
 
 def ssq_state_reorder(states, parents, stream=None):

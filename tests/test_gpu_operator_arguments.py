@@ -43,3 +43,25 @@ def test_linear_attention():
         with pytest.raises(ValueError):
             ssq.ssq_linattn_workspace(st, nseq, tokens)
     assert ssq.ssq_linattn_workspace(st, 1, 100) >= 0
+
+
+class StreamElsewhere:
+    """What a stream of a second device looks like to a call; its handle is this device's default stream."""
+    cuda_stream = 0
+    device = torch.device("cuda", 1)
+
+
+def test_a_stream_of_another_device():
+    """Its kernels would run there, on this device's memory, and a workspace would come from there."""
+    there = StreamElsewhere()
+    st = ssq.ssq_alloc_state(ssq.make_desc(ssq.SSQ_MAMBA2, "int8_sym", 2, 2, 16))
+    q, v = torch.zeros(2, 1, 128, device="cuda"), torch.zeros(2, 2, 16, device="cuda")
+    cu = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    parents = torch.zeros(1, 2, dtype=torch.int32, device="cuda")
+    for call in (lambda: ssq.ssq_linattn_prefill(st, q, q, v, None, torch.empty_like(v), cu, stream=there),
+                 lambda: ssq.ssq_linattn_step(st, q, q, v, None, torch.empty_like(v), stream=there),
+                 lambda: ssq.ssq_state_reorder(st, parents, stream=there), lambda: selection(8, stream=there)):
+        with pytest.raises(ValueError, match="stream"):
+            call()
+    ssq.ssq_state_reorder(st, parents, stream=torch.cuda.Stream())
+    torch.cuda.synchronize()
