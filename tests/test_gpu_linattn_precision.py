@@ -88,3 +88,30 @@ def test_decays_behind_tokens_that_forget(dtype, T):
         assert (off <= 1).all(), f"the worst {off.max():.1f} times its bound"
     else:
         check_rounded_once(o, wo, om, T, "behind tokens that forget", pairs=1)
+
+
+def off_by(got, want):
+    return ((got.double() - want).norm() / want.norm()).item()
+
+
+@pytest.mark.parametrize("H,G,P,T", [(24, 1, 64, 700), (3, 1, 32, 2000), (60, 4, 64, 320)])
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+def test_norms(dtype, H, G, P, T):
+    """Errors of many roundings, in the 2-norm.  A chain of n fp32 additions is off by 2^-24 * sqrt(n/3)
+    of its running value; a state takes some 8 a chunk, whose weights its decay bounds to the last
+    hundred or so, a score or S q 32, an output twice that: 2e-7 for 40, 3e-7 for 80, and twice it
+    taken.  A state that is written as two bf16 terms would be off by 2.6e-6 (the rms of a rounding
+    to bf16 is 0.0016 of a value, and the second term's is that of 0.0023/1.4 of it)."""
+    gen = torch.Generator().manual_seed(T)
+    q, k, v, g = ref.inputs(gen, T, H, G, P, dtype)
+    n = 5 if H == 60 else 1
+    lens = [T // n] * n
+    o, state, want = run(q, k, v, g, lens, G, torch.randn(n, H, P, 128, generator=gen), 0.3)
+    ws, wo = torch.stack([w[1] for w in want]), torch.cat([w[0] for w in want])
+    so, oo = off_by(state, ws), off_by(o, wo)
+    say("norms", dtype, H, G, P, T, f"state {so:.2e}, o {oo:.2e}")
+    assert so <= 4e-7
+    if dtype == F32:
+        assert oo <= 6e-7
+    else:
+        assert oo <= 1.02 * off_by(wo.to(dtype), wo)
