@@ -107,3 +107,39 @@ def test_abi_host_tests_pass_with_the_host_side_sanitized(tmp_path):
     assert r.returncode == 0, out[-4000:]
     assert "runtime error" not in out and "AddressSanitizer" not in out, out[-4000:]
     assert " passed" in out
+
+
+def test_operators_host_tests_pass_with_the_host_side_sanitized(tmp_path):
+    """The same of what checks the arguments of linear attention, beam selection and reordering, and of the
+    files of the last two's kernels, whose host code sizes workspaces and launches."""
+    if os.environ.get("LD_PRELOAD"):
+        pytest.skip("a library is already preloaded; the sanitizer runtime has to come first")
+    import glob
+    found = glob.glob("/opt/rocm/llvm/lib/clang/*/lib/linux/libclang_rt.asan-x86_64.so")
+    if not found:
+        pytest.skip("no clang AddressSanitizer runtime here")
+    libbuild, objs = _hip_objects(tmp_path)
+    own = ["ssq_api.cpp", "ssq_beam.hip", "ssq_reorder.hip"]
+    objs = [o for o in objs if not any(n.rsplit(".", 1)[0] in os.path.basename(o) for n in own)]
+    host_san = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
+                "-Xarch_host", "-fno-sanitize-recover=all", "-Xarch_host", "-fno-omit-frame-pointer"]
+    flags = [f for f in libbuild.FLAGS if not f.startswith("-O")] + ["-O1", "-g"]
+    for src in own:
+        objs.append(str(tmp_path / (src + "_san.o")))
+        subprocess.check_call([libbuild.HIPCC, *flags, *host_san, "-c", os.path.join(libbuild.CSRC, src), "-o", objs[-1]],
+                              stdout=subprocess.DEVNULL, stderr=subprocess.DEVNULL)
+    so = str(tmp_path / "libssq_san.so")
+    subprocess.check_call([libbuild.HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", so])
+    env = dict(os.environ, SSQ_LIBRARY=so, LD_PRELOAD=found[0], ASAN_OPTIONS="detect_leaks=0",
+               UBSAN_OPTIONS="print_stacktrace=1")
+    probe = "import mamba_decode_amd as m; print(m.LIB_PATH, m.lib._name)"
+    r = subprocess.run([sys.executable, "-c", probe], cwd=ROOT, env=env, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    assert r.stdout.split() == [so, so], r.stdout
+    r = subprocess.run([sys.executable, "-m", "pytest", "-x", "-q", "-m", "not gpu", "-p", "no:cacheprovider",
+                        "--capture=sys", os.path.join(ROOT, "tests", "test_beam_abi.py")],
+                       cwd=ROOT, env=env, capture_output=True, text=True, timeout=600)
+    out = r.stdout + r.stderr
+    assert r.returncode == 0, out[-4000:]
+    assert "runtime error" not in out and "AddressSanitizer" not in out, out[-4000:]
+    assert " passed" in out
