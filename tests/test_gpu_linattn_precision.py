@@ -115,3 +115,20 @@ def test_norms(dtype, H, G, P, T):
         assert oo <= 6e-7
     else:
         assert oo <= 1.02 * off_by(wo.to(dtype), wo)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+@pytest.mark.parametrize("H,lens", [(3, [900, 1, 70]), (90, [65, 0, 130, 1]), (2, [5])])
+def test_log_decays_in_a_wider_row(dtype, H, lens):
+    """g as a slice of a wider tensor, whose other columns and rows behind the last sequence are NaN."""
+    say("wide decays", dtype, H, lens)
+    gen = torch.Generator().manual_seed(H)
+    T, P = sum(lens), 16
+    q, k, v, g = ref.inputs(gen, T, H, 1, P, dtype)
+    start = torch.randn(len(lens), H, P, 128, generator=gen)
+    want, same = run(q, k, v, g, lens, 1, start, 0.3)[:2]
+    wide = torch.full((T + 9, H + 7), math.nan, device="cuda")
+    wide[:T, 3:H + 3] = g.cuda()
+    st, o = state_of(start, 1), torch.zeros_like(v).cuda()
+    ssq.ssq_linattn_prefill(st, q.cuda(), k.cuda(), v.cuda(), wide[:T, 3:H + 3], o, cu_of(lens), scale=0.3)
+    assert torch.equal(o.cpu(), want) and torch.equal(values_of(st), same)
