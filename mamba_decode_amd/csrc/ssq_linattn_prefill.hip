@@ -525,7 +525,8 @@ __global__ __launch_bounds__(256, MODE == PART_STATE ? 4 : 3) void k_linattn_chu
         const Rsrc bk = wave_rsrc(kp + t0 * a.ks, rows_of(t0) * k_row + 256);
         const Rsrc bv = wave_rsrc(vp + t0 * a.vs, rows_of(t0) * v_row + cols * 2);
         const uint32_t k_at = here(k_off), v_at = here(v_off);
-        const Rsrc bg = a.g ? wave_rsrc(a.g + t0 * a.gs + head, rows_of(t0) * g_row + 4) : wave_rsrc(nullptr, 0);
+        // without g an empty range, which reads 0 (two descriptors to choose from would cost 3% of ragged prompts)
+        const Rsrc bg = wave_rsrc((const void*)((uint64_t)a.g + (uint64_t)(t0 * a.gs + head) * 4), a.g ? rows_of(t0) * g_row + 4 : 0);
         const uint32_t g_at = (uint32_t)lane <= rows_of(t0) ? lane * g_row : kNone; // a stride of 0 has no row behind the span
         rg = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(bg, g_at, 0, 0));
 #pragma unroll
