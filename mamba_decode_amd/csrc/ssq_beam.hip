@@ -31,6 +31,7 @@
 namespace ssq {
 
 constexpr int kBeamMaxShares = 16; // workgroups per row at most
+constexpr int kMaxBeams = 32;      // SSQ_MAX_BEAMS
 constexpr int kBeamPiece = 16;
 
 struct BeamShare {
@@ -518,7 +519,8 @@ template <int DT, int VPL>
 static hipError_t launch_rows_of(const BeamArgs& a, BeamShare* shares, uint64_t* best, int nshares, hipStream_t st)
 {
     const int64_t blocks = (int64_t)a.batch * a.beams * nshares;
-    const size_t lds = 4 * (size_t)beam_wave_keys(a.nselect) * sizeof(uint64_t); // 34 KiB at most
+    const size_t lds = 4 * (size_t)beam_wave_keys(a.nselect) * sizeof(uint64_t); // 36 KiB at most
+    static_assert(4 * beam_wave_keys(2 * kMaxBeams) * sizeof(uint64_t) == 36 * 1024, "a launch takes up to 64 KiB");
     hipLaunchKernelGGL((k_beam_rows<DT, VPL>), dim3((unsigned)blocks), dim3(256), lds, st, a, shares, best, nshares);
     return hipGetLastError();
 }
@@ -536,6 +538,7 @@ static hipError_t launch_beam_dt(const BeamArgs& a, hipStream_t st)
     if (e != hipSuccess) return e;
     const int waves = a.beams < 16 ? a.beams : 16;
     const size_t lds = beam_join_lds(waves, a.beams, a.nselect); // 20 KiB at most
+    static_assert(beam_join_lds(16, kMaxBeams, 2 * kMaxBeams) == 20 * 1024, "a launch takes up to 64 KiB");
     hipLaunchKernelGGL(k_beam_join, dim3((unsigned)a.batch), dim3(64 * waves), lds, st, a, shares, best, nshares);
     return hipGetLastError();
 }
