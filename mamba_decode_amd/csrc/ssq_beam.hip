@@ -22,10 +22,10 @@
 // the tile is taken in pieces of 16 elements a lane with an exact threshold, which bounds the list
 // whatever the values are.
 //
-// What bounds it: 32 x 8 beams of 131071 in fp32 (134 MB) take 28 us, 4.8 TB/s, in the pass and 6
+// What bounds it: 32 x 8 beams of 131071 in fp32 (134 MB) take 27 us, 5.0 TB/s, in the pass and 6
 // us in the join; a wave's loads of 2048 elements wait for the tile before (fetched a tile ahead
 // they need 32 registers more, three waves a SIMD for four: 40 us in fp32; 3% gained in bf16).
-// 4 x 50280 take 6.6 and 5.5 us, mostly the latency of two launches.
+// 4 x 50280 take 6.4 and 4.6 us, mostly the latency of two launches.
 #include "ssq_ops_device.h"
 
 namespace ssq {

@@ -98,18 +98,18 @@ __device__ __forceinline__ float* seq_rows(const LinArgs& a, int seq, int slot)
 // have it).  Each wave also has the scores of 16 keys; they meet the other waves through LDS, the
 // first terms in a place of their own and the second ones, once q has been read, in q's: room for
 // both would cost the third workgroup of a compute unit.  The barrier between is behind the state's
-// products, so that few waves wait there (ragged prompts 76 us, 79 with it in front of them; 69 with
-// one term).
+// products, so that few waves wait there (24 ragged prompts of 32 heads 80 us, 84 with it in front of
+// them; 72 with one term, and outputs off by as much again as their rounding).
 //
 // What bounds it: the chain of each wave and what the waves of a SIMD can issue.  One prompt of 8192
-// tokens on 128 heads of 64 takes 185 us: 62 for the parts' own states, 125 for the outputs, which
+// tokens on 128 heads of 64 takes 203 us: 63 for the parts' own states, 140 for the outputs, which
 // join them (the 310 MB that have to move take 47 us as a copy, the 47 GFLOP 37 us as a large matrix
-// product).  In the last the matrix pipes are busy 31% of the cycles and vector instructions (decays,
-// roundings to bf16 and their remainders, addresses), at 4 cycles each, take 40%; in the rest the
+// product).  In the last the matrix pipes are busy 30% of the cycles and vector instructions (decays,
+// roundings to bf16 and their remainders, addresses), at 4 cycles each, take 41%; in the rest the
 // three waves of a SIMD wait for LDS and at barriers.  Three workgroups of 64 columns on a compute
 // unit, 12 waves, against two of 128 columns (two tiles a wave, each fragment of q and k read once for
-// both): 24 ragged prompts of 32 heads 84 us against 99, since what one wave waits for the others
-// fill.  HBM is not a bound: those prompts move 125 MB in 70 us.
+// both): the ragged prompts, when scores had one term, 84 us against 99, since what one wave waits for
+// the others fill.  HBM is not a bound: those prompts move 159 MB in 82 us.
 constexpr int kChunk = 64;
 constexpr int kCols = 64;
 constexpr int kPitch = 136;      // bf16 of a row of 128 in LDS: 16-byte reads of 16 rows fall in different banks
@@ -324,8 +324,8 @@ __device__ __forceinline__ bool find_work(const ChunkArgs& c, Work& w)
     // Whole sequences, up to 64 of them (a lane ranks each), are taken from the longest to the
     // shortest, and every other row of the runs that lie side by side the other way round, so that
     // the workgroups that share a compute unit have about the same work: 24 ragged prompts of 32
-    // heads 73 us, in their own order 82; 64 of 24 heads, to 3000 tokens, 180 and 253; of one
-    // length, where it serves nothing, 71-73 either way.
+    // heads 79 us, in their own order 85; 64 of 24 heads, to 3000 tokens, 365 and 436; of one
+    // length, where it serves nothing, 79 either way.
     const unsigned at = blockIdx.x / 8;
     unsigned deal = at / c.run * 8 + blockIdx.x % 8;
     if (deal >= (unsigned)c.items * c.runs) return false;
@@ -1044,15 +1044,16 @@ struct ChunkPlan {
 };
 
 // Sequences are split where they and the blocks do not give every compute unit a workgroup (24
-// ragged bf16 prompts of 32 heads, 768 workgroups whole: 82 us in the order of the call; as 384
-// workgroups of twice the columns 99 us whole and 162 us split), into as many parts as there can be
-// workgroups at once (three prompts of 32 heads of 128, bf16, by a join of its own: 94 us for three
-// workgroups a unit, 104 us for two), of three chunks at least (2048 tokens of 24 heads: 32.2 us,
-// 32.3 in parts of two, 30.0 of four; 512 tokens 18.4, 23.4 of four).
+// ragged bf16 prompts of 32 heads, as 384 workgroups of twice the columns and with scores in one
+// term: 99 us whole and 162 us split), into as many parts as there can be workgroups at once (three
+// prompts of 32 heads of 128, bf16: 75 us for three workgroups a unit, 82 us for two; 16000 tokens of
+// 24 heads 88 and 99), of three chunks at least (2048 tokens of 24 heads: 33.4 us, 34.6 in parts of
+// two, 31.5 of four; 512 tokens 20.3, 25.5 of four).
 // Few parts are joined by those who need them, each from the parts before it, more by a launch of
-// its own: 512 tokens of 24 heads 18.4 us against 23.6, three prompts of 32 heads of 128 83 against
-// 93; but 16000 tokens, 32 parts, 107 against 85.  Only the sum of the parts is known here: where
-// four sequences or more share it, 32 are few (five fp32 prompts, 21 parts, 51 us against 57).
+// its own: 512 tokens of 24 heads 20.3 us against 25.5, three prompts of 32 heads of 128 75 against
+// 85; but 16000 tokens, 32 parts, 112 against 88.  Only the sum of the parts is known here: where
+// four sequences or more share it, 32 are few (five fp32 prompts, 21 parts, 52.7 us against 56.9),
+// unless one of them has nearly all (16000 tokens beside three of one: 115 us).
 static ChunkPlan chunk_plan(int dtype, int nseq, int64_t tokens, int H, int P, int num_cus)
 {
     ChunkPlan p;
