@@ -13,12 +13,12 @@ import pytest
 import torch
 
 from tests import linattn_ref as ref
+from tests.test_gpu_linattn import BF, F32, HF, cu_of, state_of, sum_bound, values_of
 
 pytestmark = pytest.mark.gpu
 
 if torch.cuda.is_available():
     import mamba_decode_amd as ssq
-    from tests.test_gpu_linattn import BF, F32, HF, cu_of, state_of, sum_bound, values_of
 
 
 def say(*a):

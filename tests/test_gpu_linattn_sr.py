@@ -11,13 +11,13 @@ import torch
 
 import oracle
 from tests import linattn_ref as ref
+from tests.test_gpu_linattn import BF, F32, cu_of, state_of, values_of
 
 pytestmark = pytest.mark.gpu
 
 if torch.cuda.is_available():
     import mamba_decode_amd as ssq
     from tests import parity as par
-    from tests.test_gpu_linattn import BF, F32, cu_of, state_of, values_of
 
 
 def say(*a):

@@ -9,13 +9,13 @@ import pytest
 import torch
 
 from tests import linattn_ref as ref
+from tests.test_gpu_beam import reference
+from tests.test_gpu_linattn import BF, F32, check_o, check_state, cu_of
 
 pytestmark = pytest.mark.gpu
 
 if torch.cuda.is_available():
     import mamba_decode_amd as ssq
-    from tests.test_gpu_beam import reference
-    from tests.test_gpu_linattn import BF, F32, cu_of
 
 H, P, G = 128, 64, 1
 
@@ -159,7 +159,6 @@ def test_a_large_state_follows_its_beams(fmt, batch):
 def test_one_prompt_of_millions_of_tokens(dtype):
     """Split into parts, tokens past byte 2^32 of q and v: what the state has forgotten (e^-150 over 300
     tokens is 0) does not count, so that any tokens can be checked from those shortly before them."""
-    from tests.test_gpu_linattn import check_o, check_state
     T = (1 << 25) + 77 if dtype == BF else (1 << 24) + 77
     say("one long prompt", dtype, T)
     gen = torch.Generator(device="cuda").manual_seed(5)
