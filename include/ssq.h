@@ -323,14 +323,16 @@ ssq_status ssq_stream_copy(void *dst, const void *src, size_t bytes, void *strea
  * (-infinity forgets the state; NULL: no decay), with a stride of its own (0:
  * the same decay at every token).  q, k, v and o and their strides in bytes
  * are multiples of 16, no stride but g's is shorter than a token's row, and
- * none exceeds 2^23 elements.  o overlaps no input.  The state, every sum and
- * every decay are held in fp32 or wider (a decay exp(-x) is off by
- * (2x + 4) * 2^-24 of itself at most); o is rounded once to `dtype`.  What a product reads is fp32
- * or exact, but for bf16 prompts: there the state, where q meets it, and the
- * scores q.k, where v meets them, stand as two bf16 numbers each, and so do the
- * values that a long sequence writes into the states between its parts' chunks.
- * With that a term of an output is off by up to 2^-16 of itself three times, at
- * most, before the rounding of o; the state that is left is not touched by it.
+ * none exceeds 2^23 elements.  o overlaps no input.
+ *
+ * The state, every sum and every decay are held in fp32 or wider (a decay
+ * exp(-x) is off by (2x + 4) * 2^-24 of itself at most); o is rounded once to
+ * `dtype`.  What a product reads is fp32 or exact, but for bf16 prompts: there
+ * the state, where q meets it, and the scores q.k, where v meets them, stand as
+ * two bf16 numbers each, and so do the values that a long sequence writes into
+ * the states between its parts' chunks.  With that a term of an output is off by
+ * up to 2^-16 of itself three times, at most, before the rounding of o; the
+ * state that is left is not touched by it.
  *
  * slots: device int32 [nseq], the sequence of the state (0 .. batch-1) that
  * sequence i of the call is, each at most once (twice: the state and outputs
@@ -373,8 +375,8 @@ size_t ssq_linattn_workspace(const ssq_state *state, int32_t nseq, int64_t token
  * is left as it was.
  * Each sequence goes on from its state, or from zero where fresh[i] is not 0
  * (device uint8 [nseq]; NULL: all go on), and leaves its last state; an empty
- * sequence leaves its state, zeroed if fresh.  The recurrence is fp32 from end
- * to end; a quantized state is reconstructed at the start and refit and
+ * sequence leaves its state, zeroed if fresh.  The recurrence is held in fp32
+ * from end to end; a quantized state is reconstructed at the start and refit and
  * rounded once, at the end (as ssq_prefill with one chunk; a stochastic
  * rounding draws the uniforms of the state's next token and advances it by
  * one).  o is read from the fp32 recurrence.
@@ -423,7 +425,8 @@ size_t ssq_beam_workspace(const ssq_beam_desc *desc);
  * compared in double, with exponentials in fp32: the logarithm, which all
  * candidates of a beam share, is off by some 1e-7, by 2^-18 at most, so that
  * candidates of different beams closer than that may change places (not those
- * of beams with the same logits, whose sums are the same).  Candidates are ordered by descending score, of equal
+ * of beams with the same logits, whose sums are the same).
+ * Candidates are ordered by descending score, of equal
  * ones the lower beam first, and within a beam by descending logit, of equal
  * ones the lower token first; they are written as scores [batch][nselect]
  * (fp32), tokens and parents (the beam in 0 .. beams-1) int32.  A logit of -infinity is no candidate, nor is any token of a

@@ -26,12 +26,12 @@
 // us in the join; a wave's loads of 2048 elements wait for the tile before (fetched a tile ahead
 // they need 32 registers more, three waves a SIMD for four: 40 us in fp32; 3% gained in bf16).
 // 4 x 50280 take 6.4 and 4.6 us, mostly the latency of two launches.
+#include "ssq.h"
 #include "ssq_ops_device.h"
 
 namespace ssq {
 
 constexpr int kBeamMaxShares = 16; // workgroups per row at most
-constexpr int kMaxBeams = 32;      // SSQ_MAX_BEAMS
 constexpr int kBeamPiece = 16;
 
 struct BeamShare {
@@ -520,7 +520,7 @@ static hipError_t launch_rows_of(const BeamArgs& a, BeamShare* shares, uint64_t*
 {
     const int64_t blocks = (int64_t)a.batch * a.beams * nshares;
     const size_t lds = 4 * (size_t)beam_wave_keys(a.nselect) * sizeof(uint64_t); // 36 KiB at most
-    static_assert(4 * beam_wave_keys(2 * kMaxBeams) * sizeof(uint64_t) == 36 * 1024, "a launch takes up to 64 KiB");
+    static_assert(4 * beam_wave_keys(2 * SSQ_MAX_BEAMS) * sizeof(uint64_t) == 36 * 1024, "a launch takes up to 64 KiB");
     hipLaunchKernelGGL((k_beam_rows<DT, VPL>), dim3((unsigned)blocks), dim3(256), lds, st, a, shares, best, nshares);
     return hipGetLastError();
 }
@@ -538,7 +538,7 @@ static hipError_t launch_beam_dt(const BeamArgs& a, hipStream_t st)
     if (e != hipSuccess) return e;
     const int waves = a.beams < 16 ? a.beams : 16;
     const size_t lds = beam_join_lds(waves, a.beams, a.nselect); // 20 KiB at most
-    static_assert(beam_join_lds(16, kMaxBeams, 2 * kMaxBeams) == 20 * 1024, "a launch takes up to 64 KiB");
+    static_assert(beam_join_lds(16, SSQ_MAX_BEAMS, 2 * SSQ_MAX_BEAMS) == 20 * 1024, "a launch takes up to 64 KiB");
     hipLaunchKernelGGL(k_beam_join, dim3((unsigned)a.batch), dim3(64 * waves), lds, st, a, shares, best, nshares);
     return hipGetLastError();
 }
