@@ -31,3 +31,25 @@ def test_the_normalizer_of_a_long_row(vocab, below):
     want = -2.0 - math.log(top + (vocab - top) * math.exp(-below))
     for got in out[0].tolist():
         assert abs(got - want) <= abs(want) * 2.0 ** -24 + 2.0 ** -18, got - want
+
+
+@pytest.mark.parametrize("dtype,bits,patterns", [(torch.bfloat16, torch.int16, (0x7F81, -0x7F, 0x7FC0, -1)), (torch.float16, torch.int16, (0x7C01, -0x3FF, 0x7E00, -1)),
+                                                 (torch.float32, torch.int32, (0x7F800001, -0x7FFFFF, 0x7FC00000, -1))])
+def test_every_kind_of_nan_is_no_candidate(dtype, bits, patterns):
+    """Signalling and quiet ones, of either sign."""
+    gen = torch.Generator().manual_seed(7)
+    x = torch.randn(2, 3, 20000, generator=gen).to(dtype)
+    hit = torch.rand(x.shape, generator=gen)
+    for i, p in enumerate(patterns):
+        x.view(bits)[(hit > 0.2 * i) & (hit <= 0.2 * i + 0.2)] = p
+    assert 0.7 < x.isnan().float().mean() < 0.9
+    clean = torch.where(x.isnan(), -math.inf, x.float()).to(dtype)
+    scores = -torch.rand(2, 3, generator=gen)
+    outs = []
+    for y in (x, clean):
+        out = torch.empty(2, 6, device="cuda")
+        token, parent = (torch.empty(2, 6, dtype=torch.int32, device="cuda") for _ in range(2))
+        ssq.ssq_beam_select(y.cuda(), scores.cuda(), out, token, parent)
+        outs.append((out, token, parent))
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
