@@ -8,7 +8,7 @@
  * quantization changes persistent state").  This library stores that state
  * quantized per row and updates it in place with hand-written HIP kernels.
  *
- * Two state kinds:
+ * Three state kinds:
  *  - SSQ_MAMBA2: the Mamba-2 selective-SSM state, [batch][nheads][P][N] with
  *    head dimension P and state size N.  A row is (sequence, head, p) over the
  *    N state entries ("ssm-state-quantization" README, Setup: one scale per
@@ -17,6 +17,8 @@
  *    matrix state, one dk x dv matrix per (sequence, head) ("Mamba state
  *    quantization for inference", "Mamba state quantization changes
  *    persistent state").  A row is one key channel over the value dimension.
+ *  - SSQ_GATED: the state of a gated linear recurrence, one fp32 number for
+ *    every channel of a sequence.  A row is a sequence over its channels.
  *
  * Formats: fp32 (unquantized control), and symmetric or asymmetric per-row
  * grids at 8 or 4 bits, refit at every step (README, Setup: symmetric grid
@@ -65,7 +67,8 @@
  *    the matrices) are unspecified; the call completes and every other row
  *    is computed as usual.
  *  - Kernels support row_len == 128, and rows_per_head a multiple of 16 for
- *    SSQ_MAMBA2, dk == 128 for SSQ_DELTA.
+ *    SSQ_MAMBA2, dk == 128 for SSQ_DELTA.  SSQ_GATED: fp32, nheads, ngroups
+ *    and rows_per_head 1, row_len (the channels) a multiple of 8 up to 2^20.
  */
 #ifndef SSQ_H
 #define SSQ_H
@@ -113,7 +116,7 @@ typedef enum {
  * returns S = 2 St Hs. */
 #define SSQ_DAMP_NHI 16
 
-typedef enum { SSQ_MAMBA2 = 0, SSQ_DELTA = 1 } ssq_kind;
+typedef enum { SSQ_MAMBA2 = 0, SSQ_DELTA = 1, SSQ_GATED = 2 } ssq_kind;
 
 typedef enum { SSQ_READ_POST_QUANT = 0, SSQ_READ_PRE_QUANT = 1 } ssq_readout;
 
@@ -125,9 +128,9 @@ typedef struct {
     int32_t format;        /* ssq_format */
     int32_t batch;         /* sequences */
     int32_t nheads;        /* heads */
-    int32_t ngroups;       /* SSQ_MAMBA2: B/C groups, each shared by nheads/ngroups heads; SSQ_DELTA: 1 */
-    int32_t rows_per_head; /* SSQ_MAMBA2: head dimension P; SSQ_DELTA: key dimension dk */
-    int32_t row_len;       /* SSQ_MAMBA2: state size N; SSQ_DELTA: value dimension dv */
+    int32_t ngroups;       /* SSQ_MAMBA2: B/C groups, each shared by nheads/ngroups heads; else 1 */
+    int32_t rows_per_head; /* SSQ_MAMBA2: head dimension P; SSQ_DELTA: key dimension dk; SSQ_GATED: 1 */
+    int32_t row_len;       /* SSQ_MAMBA2: state size N; SSQ_DELTA: value dimension dv; SSQ_GATED: channels */
 } ssq_desc;
 
 /* Byte layout of a state in its storage (public, so that checkpoints and
@@ -453,6 +456,198 @@ ssq_status ssq_beam_select(const ssq_beam_desc *desc, const void *logits, const 
  * stay.  Bytes move unchanged. */
 ssq_status ssq_state_reorder(ssq_state *const *states, int32_t nstates, const int32_t *parents, int32_t beams,
                              void *stream);
+
+/* Moves between sequences of states: for i = 0 .. nmoves-1, in this order,
+ * sequence to[i] of states[l] becomes what sequence from[i] of sources[l] is
+ * then, or the zero state where from[i] is -1, in every layer l = 0 ..
+ * nstates-1.  It forks (one source, many destinations), copies, compacts (a
+ * sequence may be the source of one move and the destination of a later one)
+ * and frees.  to, from: device int32 [nmoves].  A move whose to is not in 0 ..
+ * batch-1 of states[l], or whose from is neither -1 nor in 0 .. batch-1 of
+ * sources[l], is left out.  sources NULL: states themselves; else another pool,
+ * sources[l] of the kind, format and sizes of states[l] but for the batch.  The
+ * states of one call, and the sources of one call, have the same batch; no two
+ * states share memory, and no state and another's source.  States that are
+ * moved within themselves take their moves in parallel where no move reads what
+ * another one writes and none writes what another one writes, and one after the
+ * other else, or if they have more than 2^18 sequences.  Rounding modes and
+ * token counters stay.  Bytes move unchanged.
+ * nmoves is 65535 at most, nstates 1024, and a state has less than 4 KiB * 2^24
+ * of codes or fp32 entries for each sequence. */
+ssq_status ssq_state_move(ssq_state *const *states, ssq_state *const *sources, int32_t nstates, const int32_t *to,
+                          const int32_t *from, int32_t nmoves, void *stream);
+
+/* ------------------------------------------------------------------------
+ * A gated linear recurrence: every channel has a decay for every token.
+ *
+ * Per sequence and channel
+ *   h_t = a_t h_(t-1) + s_t x_t,   o_t = h_t
+ * with the decay from the gate g_t and the factor on the input from the decay:
+ *   SSQ_GATE_LOG      a = exp(g), g <= 0 (-infinity forgets the state)
+ *   SSQ_GATE_SIGMOID  a = 1/(1 + exp(-g))
+ *   SSQ_INPUT_PLAIN   s = 1
+ *   SSQ_INPUT_COMPLEMENT  s = 1 - a
+ *   SSQ_INPUT_NORM    s = sqrt(1 - a^2)
+ *
+ * x, g, o and their gradients: [tokens][channels] in `dtype`, each with a
+ * stride in elements from one token to the next, so that they may be slices of
+ * one projection's output; bases and strides are multiples of 16 bytes, no
+ * stride is below `channels` or above 2^23.  Outputs overlap no input and no
+ * other output.  channels: a multiple of 8, up to 2^20.  The state, decays,
+ * factors and sums are fp32 (1 - a and 1 - a^2 are taken from the gate, without
+ * a difference of near numbers; a decay exp(-x) is off by (2x + 4) * 2^-24 of
+ * itself at most, one below 2^-126 may be zero), outputs are rounded once to `dtype`.
+ *
+ * cu_seqlens, slots, fresh: as in ssq_linattn_prefill.  state: an SSQ_GATED
+ * state, whose sequences go on and keep their last state; NULL: all sequences
+ * start from zero, nothing is kept, and slots and fresh are NULL.
+ *
+ * Values of x, g or the state that are not finite (gates of +-infinity apart,
+ * +infinity of SSQ_GATE_SIGMOID only) leave the outputs and gradients of their
+ * sequence and channel unspecified, earlier tokens included; every other
+ * sequence and channel is computed as usual.
+ * ------------------------------------------------------------------------ */
+typedef enum { SSQ_GATE_LOG = 0, SSQ_GATE_SIGMOID = 1 } ssq_gate;
+typedef enum { SSQ_INPUT_PLAIN = 0, SSQ_INPUT_COMPLEMENT = 1, SSQ_INPUT_NORM = 2 } ssq_input;
+#define SSQ_GATED_CHUNK 16 /* tokens from one checkpoint to the next */
+
+typedef struct {
+    int32_t dtype;    /* ssq_dtype of x, g and o */
+    int32_t gate;     /* ssq_gate */
+    int32_t input;    /* ssq_input */
+    int32_t channels;
+    const void *x;
+    const void *g;
+    void *o;
+    int64_t x_stride; /* elements from one token to the next */
+    int64_t g_stride;
+    int64_t o_stride;
+} ssq_gated_io;
+
+/* Rows [channels] of fp32 checkpoints for these sizes: tokens/SSQ_GATED_CHUNK +
+ * nseq; -1 if one is negative or more than a call takes. */
+int64_t ssq_gated_checkpoint_rows(int32_t nseq, int64_t tokens);
+
+/* Bytes of device workspace that ssq_gated_scan and ssq_gated_scan_backward
+ * need for these sizes (0: none); (size_t)-1 if one is negative or more than
+ * a call takes.  It does not always grow with them: a workspace for several
+ * sizes is as large as the largest of their answers. */
+size_t ssq_gated_workspace(int32_t channels, int32_t nseq, int64_t tokens);
+
+/* Prompts, or a training step's sequences, one after the other in `tokens`
+ * rows.  checkpoints: NULL, or device memory of ssq_gated_checkpoint_rows()
+ * rows, 16-byte aligned, that receives what the gradient needs: the state
+ * before every SSQ_GATED_CHUNK'th token of each sequence, chunk j of sequence
+ * i in row cu_seqlens[i]/SSQ_GATED_CHUNK + i + j (rows of no chunk are left).
+ * Results do not depend on other sequences of the call, but may differ in
+ * rounding with the call's sizes.  nseq*channels is 2^26 at most, tokens below
+ * 2^31 - 128.  workspace: as for ssq_linattn_prefill. */
+ssq_status ssq_gated_scan(ssq_state *state, const ssq_gated_io *io, int32_t nseq, int64_t tokens,
+                          const int32_t *cu_seqlens, const int32_t *slots, const uint8_t *fresh, float *checkpoints,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
+typedef struct {
+    int32_t dtype; /* as in ssq_gated_io */
+    int32_t gate;
+    int32_t input;
+    int32_t channels;
+    const void *x;
+    const void *g;
+    const void *dout; /* gradient of o */
+    void *dx;
+    void *dg;
+    int64_t x_stride;
+    int64_t g_stride;
+    int64_t dout_stride;
+    int64_t dx_stride;
+    int64_t dg_stride;
+    const float *dlast; /* [nseq][channels] gradient of the last states, or NULL: zero */
+    float *dfirst;      /* [nseq][channels] receives the gradient of the states the sequences started from, or NULL */
+} ssq_gated_grad;
+
+/* Gradients of ssq_gated_scan, from its checkpoints:
+ *   dh_t = do_t + a_(t+1) dh_(t+1)  (at the last token do_t + dlast)
+ *   dx_t = s_t dh_t,   dg_t = dh_t (a'_t h_(t-1) + s'_t x_t),   dfirst = a_1 dh_1
+ * a', s': derivatives along the gate.  Where SSQ_INPUT_NORM has s = 0, s' is
+ * taken as 0.  The states between the checkpoints are computed again, in fp32.
+ * x, g, cu_seqlens, slots, nseq, tokens and checkpoints are those of the scan;
+ * state (only its batch is looked at) and slots tell which sequences the scan
+ * left out, which are left out here too: their dx, dg and dfirst stay.  Rows of
+ * dx and dg of no sequence stay as they are; an empty sequence has dfirst =
+ * dlast.  dfirst of a fresh sequence is the gradient of the zero it started
+ * from. */
+ssq_status ssq_gated_scan_backward(const ssq_state *state, const ssq_gated_grad *io, int32_t nseq, int64_t tokens,
+                                   const int32_t *cu_seqlens, const int32_t *slots, const float *checkpoints,
+                                   void *workspace, size_t workspace_bytes, void *stream);
+
+/* One token for each of nseq sequences (row i of the tensors is sequence i,
+ * slots as in ssq_linattn_step).  nseq*channels is 2^31 at most. */
+ssq_status ssq_gated_step(ssq_state *state, const ssq_gated_io *io, int32_t nseq, const int32_t *slots, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Group norm with an activation, channels last.
+ *
+ * Each token's channels stand in groups of `width`, each normalised by itself:
+ *   u = x, or x*silu(z) (SSQ_ACT_GATE_INPUT)
+ *   m = (u - mean(u)) / sqrt(var(u) + eps)   with `center`, var of the group (over width)
+ *   m = u / sqrt(mean(u^2) + eps)            without
+ *   n = m*weight + bias
+ *   y = silu(n) (SSQ_ACT_SILU), n*silu(z) (SSQ_ACT_GATE_OUTPUT) or n (SSQ_ACT_GATE_INPUT)
+ * with silu(v) = v/(1 + exp(-v)).
+ *
+ * x, z, y and their gradients: [tokens][groups*width] in `dtype` with strides
+ * as for the recurrence; weight, bias and their gradients: [groups*width]
+ * fp32, 16-byte aligned (weight NULL: 1, bias NULL: 0).  z is NULL for
+ * SSQ_ACT_SILU.  Outputs overlap no input and no other output.  width: a
+ * multiple of 8 up to 16384; groups*width up to 2^20.  Everything between is
+ * fp32: the mean first, then the squares of the distances from it; outputs are
+ * rounded once.  eps > 0.  Values of u beyond 2^56, whose squares overflow, and values of x or z that are not finite leave
+ * their token's group unspecified (and dweight and dbias of its channels); all else is
+ * computed as usual.
+ * ------------------------------------------------------------------------ */
+typedef enum { SSQ_ACT_SILU = 0, SSQ_ACT_GATE_OUTPUT = 1, SSQ_ACT_GATE_INPUT = 2 } ssq_act;
+
+typedef struct {
+    int32_t dtype; /* ssq_dtype of x, z and y */
+    int32_t act;   /* ssq_act */
+    int32_t center;
+    int32_t groups;
+    int32_t width;
+    float eps;
+    const float *weight;
+    const float *bias;
+    const void *x;
+    const void *z;
+    int64_t x_stride; /* elements from one token to the next */
+    int64_t z_stride;
+} ssq_norm_io;
+
+/* tokens*groups is 2^31 at most. */
+ssq_status ssq_group_norm(const ssq_norm_io *io, void *y, int64_t y_stride, int64_t tokens, void *stream);
+
+typedef struct {
+    const void *dy;
+    void *dx;
+    void *dz;       /* NULL exactly where z is */
+    float *dweight; /* sums over all tokens; NULL: not wanted */
+    float *dbias;   /* likewise */
+    int64_t dy_stride;
+    int64_t dx_stride;
+    int64_t dz_stride;
+} ssq_norm_grad;
+
+/* Bytes of device workspace ssq_group_norm_backward needs; (size_t)-1 if a
+ * size is not one that it takes. */
+size_t ssq_group_norm_workspace(int32_t groups, int32_t width, int64_t tokens);
+
+/* Gradients of ssq_group_norm, from its inputs; the statistics are computed
+ * again.  With dn the gradient of n and r = 1/sqrt(..):
+ *   dweight = sum dn*m, dbias = sum dn (fp32, in an order that depends on the
+ *   sizes alone), du = r (dm - mean(dm) [with center] - m mean(dm*m)), dm =
+ *   dn*weight, and dx, dz by the product rule.  No tokens: dweight and dbias
+ *   are zero.  workspace: as for ssq_linattn_prefill. */
+ssq_status ssq_group_norm_backward(const ssq_norm_io *io, const ssq_norm_grad *grad, int64_t tokens, void *workspace,
+                                   size_t workspace_bytes, void *stream);
 
 /* Static text for a status code (an ssq_status value); any other value gives
  * "unknown ssq_status".  Taken as int32_t so that an out-of-range code is an

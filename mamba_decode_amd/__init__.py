@@ -27,12 +27,18 @@ SSQ_OK, SSQ_ERR_INVALID_ARG, SSQ_ERR_UNSUPPORTED, SSQ_ERR_KIND_MISMATCH, SSQ_ERR
 SSQ_FP32, SSQ_INT8_SYM, SSQ_INT8_ASYM, SSQ_INT4_SYM, SSQ_INT4_ASYM, SSQ_DAMP = range(6)
 SSQ_DAMP_NHI = 16
 # ssq_kind
-SSQ_MAMBA2, SSQ_DELTA = 0, 1
+SSQ_MAMBA2, SSQ_DELTA, SSQ_GATED = range(3)
 # ssq_readout
 SSQ_READ_POST_QUANT, SSQ_READ_PRE_QUANT = 0, 1
 # ssq_dtype
 SSQ_DTYPE_FP32, SSQ_DTYPE_BF16, SSQ_DTYPE_FP16 = range(3)
 SSQ_MAX_BEAMS = 32
+# ssq_gate, ssq_input
+SSQ_GATE_LOG, SSQ_GATE_SIGMOID = 0, 1
+SSQ_INPUT_PLAIN, SSQ_INPUT_COMPLEMENT, SSQ_INPUT_NORM = range(3)
+SSQ_GATED_CHUNK = 16
+# ssq_act
+SSQ_ACT_SILU, SSQ_ACT_GATE_OUTPUT, SSQ_ACT_GATE_INPUT = range(3)
 # ssq_rounding
 SSQ_ROUND_NEAREST, SSQ_ROUND_STOCHASTIC = 0, 1
 
@@ -71,6 +77,30 @@ class ssq_beam_desc(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int32), ("batch", ctypes.c_int32), ("beams", ctypes.c_int32),
                 ("vocab", ctypes.c_int32), ("nselect", ctypes.c_int32), ("pad_token", ctypes.c_int32),
                 ("row_stride", ctypes.c_int64)]
+
+
+_i32, _i64, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
+
+
+class ssq_gated_io(ctypes.Structure):
+    _fields_ = [("dtype", _i32), ("gate", _i32), ("input", _i32), ("channels", _i32), ("x", _vp), ("g", _vp), ("o", _vp),
+                ("x_stride", _i64), ("g_stride", _i64), ("o_stride", _i64)]
+
+
+class ssq_gated_grad(ctypes.Structure):
+    _fields_ = [("dtype", _i32), ("gate", _i32), ("input", _i32), ("channels", _i32), ("x", _vp), ("g", _vp), ("dout", _vp),
+                ("dx", _vp), ("dg", _vp), ("x_stride", _i64), ("g_stride", _i64), ("dout_stride", _i64), ("dx_stride", _i64),
+                ("dg_stride", _i64), ("dlast", _vp), ("dfirst", _vp)]
+
+
+class ssq_norm_io(ctypes.Structure):
+    _fields_ = [("dtype", _i32), ("act", _i32), ("center", _i32), ("groups", _i32), ("width", _i32), ("eps", ctypes.c_float),
+                ("weight", _vp), ("bias", _vp), ("x", _vp), ("z", _vp), ("x_stride", _i64), ("z_stride", _i64)]
+
+
+class ssq_norm_grad(ctypes.Structure):
+    _fields_ = [("dy", _vp), ("dx", _vp), ("dz", _vp), ("dweight", _vp), ("dbias", _vp), ("dy_stride", _i64),
+                ("dx_stride", _i64), ("dz_stride", _i64)]
 
 
 def _load():
@@ -128,6 +158,25 @@ def _load():
     L.ssq_beam_select.restype = st
     L.ssq_state_reorder.argtypes = [ctypes.POINTER(vp), ctypes.c_int32, vp, ctypes.c_int32, vp]
     L.ssq_state_reorder.restype = st
+    size = ctypes.c_size_t
+    L.ssq_state_move.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(vp), _i32, vp, vp, _i32, vp]
+    L.ssq_state_move.restype = st
+    L.ssq_gated_checkpoint_rows.argtypes = [_i32, _i64]
+    L.ssq_gated_checkpoint_rows.restype = _i64
+    L.ssq_gated_workspace.argtypes = [_i32, _i32, _i64]
+    L.ssq_gated_workspace.restype = size
+    L.ssq_gated_scan.argtypes = [vp, ctypes.POINTER(ssq_gated_io), _i32, _i64, vp, vp, vp, vp, vp, size, vp]
+    L.ssq_gated_scan.restype = st
+    L.ssq_gated_scan_backward.argtypes = [vp, ctypes.POINTER(ssq_gated_grad), _i32, _i64, vp, vp, vp, vp, size, vp]
+    L.ssq_gated_scan_backward.restype = st
+    L.ssq_gated_step.argtypes = [vp, ctypes.POINTER(ssq_gated_io), _i32, vp, vp]
+    L.ssq_gated_step.restype = st
+    L.ssq_group_norm.argtypes = [ctypes.POINTER(ssq_norm_io), vp, _i64, _i64, vp]
+    L.ssq_group_norm.restype = st
+    L.ssq_group_norm_workspace.argtypes = [_i32, _i32, _i64]
+    L.ssq_group_norm_workspace.restype = size
+    L.ssq_group_norm_backward.argtypes = [ctypes.POINTER(ssq_norm_io), ctypes.POINTER(ssq_norm_grad), _i64, vp, size, vp]
+    L.ssq_group_norm_backward.restype = st
     return L
 
 
@@ -545,5 +594,187 @@ def ssq_state_reorder(states, parents, stream=None):
         if s.desc.batch != batch:
             raise ValueError(f"a state has {s.desc.batch} sequences, parents names {batch}")
     n = len(states)
-    handles = (ctypes.c_void_p * max(1, n))(*[s.handle.value if s.handle is not None else None for s in states])
-    _check(lib.ssq_state_reorder(handles, n, p, parents.shape[1], _stream_ptr(stream, dev)), "ssq_state_reorder")
+    _check(lib.ssq_state_reorder(_handles(states), n, p, parents.shape[1], _stream_ptr(stream, dev)), "ssq_state_reorder")
+
+
+def _handles(states):
+    return (ctypes.c_void_p * max(1, len(states)))(*[s.handle.value if s.handle is not None else None for s in states])
+
+
+def ssq_state_move(states, to, from_, sources=None, stream=None):
+    """Moves between sequences, one after the other: sequence ``to[i]`` of every state becomes what sequence ``from_[i]``
+    of its source is then, or the zero state where ``from_[i]`` is -1.  ``states``: a State or a sequence of them (the
+    layers of a model); ``sources``: the same number of States of another pool, None for the states themselves; to,
+    from_: int32 ``[nmoves]`` on the device."""
+    dev = torch.cuda.current_device()
+    states = [states] if isinstance(states, State) else states
+    sources = [sources] if isinstance(sources, State) else sources
+    if sources is not None and len(sources) != len(states):
+        raise ValueError(f"{len(states)} states have {len(sources)} sources")
+    n = to.numel() if isinstance(to, torch.Tensor) else 0
+    tp = _ptr(to, "to", torch.int32, (n,), dev)
+    fp = _ptr(from_, "from_", torch.int32, (n,), dev)
+    _check(lib.ssq_state_move(_handles(states), None if sources is None else _handles(sources), len(states), tp, fp,
+                              _int32(n, "nmoves"), _stream_ptr(stream, dev)), "ssq_state_move")
+
+
+def _rows(t, name: str, dtype, tokens: int, channels: int, dev: int):
+    """Pointer and stride between tokens of a [tokens][channels] or [tokens][groups][width] tensor whose tokens are packed."""
+    shape = (tokens, channels)
+    if isinstance(t, torch.Tensor) and t.dim() == 3:
+        shape = (tokens, t.shape[1], channels // max(1, t.shape[1]))
+    p, stride = _tokens(t, name, dtype, shape, dev)
+    return p, (channels if tokens == 0 else stride)  # no row is read: any stride serves
+
+
+def _token_rows(t, name: str):
+    """dtype, tokens and channels of a [tokens][channels] tensor."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES or t.dim() != 2:
+        raise ValueError(f"{name} must be a float32, bfloat16 or float16 tensor [tokens, channels]")
+    return t.dtype, t.shape[0], t.shape[1]
+
+
+def ssq_gated_checkpoint_rows(nseq: int, tokens: int) -> int:
+    """Rows of the float32 checkpoints ``[rows, channels]`` that ``ssq_gated_scan`` writes for its gradient."""
+    if tokens >= 1 << 63:
+        raise ValueError("tokens is more than 63 bits hold")
+    n = lib.ssq_gated_checkpoint_rows(_int32(nseq, "nseq"), tokens)
+    if n < 0:
+        raise ValueError("sizes must not be negative or more than a call takes")
+    return n
+
+
+def ssq_gated_workspace(channels: int, nseq: int, tokens: int) -> int:
+    """Bytes of workspace ``ssq_gated_scan`` and ``ssq_gated_scan_backward`` need for these sizes."""
+    if tokens >= 1 << 63:
+        raise ValueError("tokens is more than 63 bits hold")
+    n = lib.ssq_gated_workspace(_int32(channels, "channels"), _int32(nseq, "nseq"), tokens)
+    if n == _SIZE_MAX:
+        raise ValueError(ssq_last_error())
+    return n
+
+
+def _sequences(cu_seqlens, slots, dev: int):
+    nseq = cu_seqlens.numel() - 1 if isinstance(cu_seqlens, torch.Tensor) else 0
+    if nseq < 0:
+        raise ValueError("cu_seqlens has nseq + 1 entries")
+    cu = _ptr(cu_seqlens, "cu_seqlens", torch.int32, (nseq + 1,), dev)
+    return nseq, cu, None if slots is None else _ptr(slots, "slots", torch.int32, (nseq,), dev)
+
+
+def _gated_io(x, g, o, gate: int, input: int, dev: int):
+    dtype, tokens, channels = _token_rows(x, "x")
+    xp, xs = _rows(x, "x", dtype, tokens, channels, dev)
+    gp, gs = _rows(g, "g", dtype, tokens, channels, dev)
+    op, os_ = _rows(o, "o", dtype, tokens, channels, dev)
+    return tokens, ssq_gated_io(_DTYPES[dtype], _int32(gate, "gate"), _int32(input, "input"), _int32(channels, "channels"),
+                                xp, gp, op, xs, gs, os_)
+
+
+def ssq_gated_scan(state: State | None, x, g, o, cu_seqlens, gate: int = SSQ_GATE_LOG, input: int = SSQ_INPUT_PLAIN,
+                   slots=None, fresh=None, checkpoints=None, workspace: torch.Tensor | None = None, stream=None):
+    """A gated linear recurrence over ragged sequences: ``h = a h + s x`` in every channel, ``o = h``.
+
+    x, g, o ``[tokens, channels]`` (float32, bfloat16 or float16; any stride between tokens that is a multiple of 16
+    bytes and not below a token's row), cu_seqlens int32 ``[nseq + 1]``, slots int32 ``[nseq]`` or None, fresh uint8 or
+    bool ``[nseq]`` or None; all on the device.  ``state``: an SSQ_GATED state, or None to start from zero.
+    ``checkpoints``: float32 ``[ssq_gated_checkpoint_rows(nseq, tokens), channels]`` for the gradient, or None.
+    ``workspace``: uint8, at least ``ssq_gated_workspace`` bytes, or None to take it from torch."""
+    dev = torch.cuda.current_device()
+    tokens, io = _gated_io(x, g, o, gate, input, dev)
+    nseq, cu, sp = _sequences(cu_seqlens, slots, dev)
+    fp = _flags(fresh, "fresh", (nseq,), dev)
+    cp = None
+    if checkpoints is not None:
+        cp = _ptr(checkpoints, "checkpoints", torch.float32, (ssq_gated_checkpoint_rows(nseq, tokens), io.channels), dev)
+    on = _stream_ptr(stream, dev)
+    ws, wp, wn = _workspace(workspace, ssq_gated_workspace(io.channels, nseq, tokens), stream, dev)
+    _check(lib.ssq_gated_scan(None if state is None else state.handle, io, nseq, tokens, cu, sp, fp, cp, wp, wn, on),
+           "ssq_gated_scan")
+
+
+def ssq_gated_scan_backward(checkpoints, x, g, do, dx, dg, cu_seqlens, gate: int = SSQ_GATE_LOG,
+                            input: int = SSQ_INPUT_PLAIN, dlast=None, dfirst=None, state: State | None = None, slots=None,
+                            workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of ``ssq_gated_scan`` (the same x, g, cu_seqlens, gate, input, state and slots, and the checkpoints that
+    it wrote): dx and dg from do, the gradient of o (all shaped and strided as x).  dlast: float32 ``[nseq, channels]``,
+    the gradient of the last states, or None; dfirst: the same of the states the sequences started from is written."""
+    dev = torch.cuda.current_device()
+    dtype, tokens, channels = _token_rows(x, "x")
+    ptrs, strides = zip(*[_rows(t, name, dtype, tokens, channels, dev)
+                          for t, name in ((x, "x"), (g, "g"), (do, "do"), (dx, "dx"), (dg, "dg"))])
+    nseq, cu, sp = _sequences(cu_seqlens, slots, dev)
+    ends = [None if t is None else _ptr(t, name, torch.float32, (nseq, channels), dev)
+            for t, name in ((dlast, "dlast"), (dfirst, "dfirst"))]
+    io = ssq_gated_grad(_DTYPES[dtype], _int32(gate, "gate"), _int32(input, "input"), _int32(channels, "channels"), *ptrs,
+                        *strides, *ends)
+    cp = _ptr(checkpoints, "checkpoints", torch.float32, (ssq_gated_checkpoint_rows(nseq, tokens), channels), dev)
+    on = _stream_ptr(stream, dev)
+    ws, wp, wn = _workspace(workspace, ssq_gated_workspace(channels, nseq, tokens), stream, dev)
+    _check(lib.ssq_gated_scan_backward(None if state is None else state.handle, io, nseq, tokens, cu, sp, cp, wp, wn, on),
+           "ssq_gated_scan_backward")
+
+
+def ssq_gated_step(state: State, x, g, o, gate: int = SSQ_GATE_LOG, input: int = SSQ_INPUT_PLAIN, slots=None, stream=None):
+    """One token of the gated recurrence for ``nseq = x.shape[0]`` sequences: row i of the tensors (as in
+    ``ssq_gated_scan``) is sequence ``slots[i]`` of the state, or sequence i without slots."""
+    dev = torch.cuda.current_device()
+    nseq, io = _gated_io(x, g, o, gate, input, dev)
+    sp = None if slots is None else _ptr(slots, "slots", torch.int32, (nseq,), dev)
+    _check(lib.ssq_gated_step(state.handle, io, _int32(nseq, "nseq"), sp, _stream_ptr(stream, dev)), "ssq_gated_step")
+
+
+def ssq_group_norm_workspace(groups: int, width: int, tokens: int) -> int:
+    """Bytes of workspace ``ssq_group_norm_backward`` needs."""
+    if tokens >= 1 << 63:
+        raise ValueError("tokens is more than 63 bits hold")
+    n = lib.ssq_group_norm_workspace(_int32(groups, "groups"), _int32(width, "width"), tokens)
+    if n == _SIZE_MAX:
+        raise ValueError(ssq_last_error())
+    return n
+
+
+def _norm_io(x, z, weight, bias, act: int, center: bool, eps: float, dev: int):
+    if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPES or x.dim() != 3:
+        raise ValueError("x must be a float32, bfloat16 or float16 tensor [tokens, groups, width]")
+    xp, xs = _tokens(x, "x", x.dtype, x.shape, dev)
+    zp, zs = (None, 0) if z is None else _tokens(z, "z", x.dtype, x.shape, dev)
+    tokens, groups, width = x.shape
+    if tokens == 0:  # no row is read: any stride serves
+        xs = zs = groups * width
+    wp, bp = (None if t is None else _ptr(t, name, torch.float32, x.shape[1:], dev) for t, name in ((weight, "weight"), (bias, "bias")))
+    return ssq_norm_io(_DTYPES[x.dtype], _int32(act, "act"), 1 if center else 0, _int32(groups, "groups"), _int32(width, "width"),
+                       eps, wp, bp, xp, zp, xs, zs)
+
+
+def ssq_group_norm(x, y, weight=None, bias=None, z=None, act: int = SSQ_ACT_SILU, center: bool = True, eps: float = 1e-5,
+                   stream=None):
+    """Group norm with an activation, channels last: every token's groups normalised by themselves.
+
+    x, z, y ``[tokens, groups, width]`` (float32, bfloat16 or float16; any stride between tokens that is a multiple of 16
+    bytes and not below a token's row), z None for SSQ_ACT_SILU; weight, bias ``[groups, width]`` float32 or None.
+    ``center``: mean and variance, else the root mean square alone."""
+    dev = torch.cuda.current_device()
+    io = _norm_io(x, z, weight, bias, act, center, eps, dev)
+    tokens, row = x.shape[0], io.groups * io.width
+    yp, ys = _tokens(y, "y", x.dtype, x.shape, dev)
+    _check(lib.ssq_group_norm(io, yp, ys if tokens else row, tokens, _stream_ptr(stream, dev)), "ssq_group_norm")
+
+
+def ssq_group_norm_backward(dy, x, dx, weight=None, bias=None, z=None, dz=None, dweight=None, dbias=None,
+                            act: int = SSQ_ACT_SILU, center: bool = True, eps: float = 1e-5,
+                            workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of ``ssq_group_norm`` (the same x, z, weight, bias, act, center and eps): dx and dz from dy (all shaped
+    and strided as x), and dweight and dbias, float32 ``[groups, width]``, where they are given."""
+    dev = torch.cuda.current_device()
+    io = _norm_io(x, z, weight, bias, act, center, eps, dev)
+    tokens, groups, width = x.shape
+    row = groups * width
+    pairs = [(None, row) if t is None and name == "dz" else _tokens(t, name, x.dtype, x.shape, dev)
+             for t, name in ((dy, "dy"), (dx, "dx"), (dz, "dz"))]
+    wp, bp = (None if t is None else _ptr(t, name, torch.float32, x.shape[1:], dev) for t, name in ((dweight, "dweight"), (dbias, "dbias")))
+    strides = [s if tokens else row for _, s in pairs]
+    grad = ssq_norm_grad(*(p for p, _ in pairs), wp, bp, *strides)
+    on = _stream_ptr(stream, dev)
+    ws, wsp, wn = _workspace(workspace, ssq_group_norm_workspace(groups, width, tokens), stream, dev)
+    _check(lib.ssq_group_norm_backward(io, grad, tokens, wsp, wn, on), "ssq_group_norm_backward")

@@ -19,7 +19,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libssq.so")
 
 SOURCES = ["ssq_api.cpp", "ssq_mamba2.hip", "ssq_delta.hip", "ssq_copy.hip", "ssq_linattn_step.hip",
-           "ssq_linattn_prefill.hip", "ssq_beam.hip", "ssq_reorder.hip"]
+           "ssq_linattn_prefill.hip", "ssq_beam.hip", "ssq_reorder.hip", "ssq_gated.hip", "ssq_norm.hip", "ssq_move.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

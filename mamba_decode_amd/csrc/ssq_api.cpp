@@ -62,13 +62,21 @@ bool mul_ok(size_t a, size_t b, size_t* out)
 ssq_status check_desc(const ssq_desc* d, ssq_layout* lay)
 {
     if (!d) return fail(SSQ_ERR_INVALID_ARG, "desc is NULL");
-    if (d->kind != SSQ_MAMBA2 && d->kind != SSQ_DELTA) return fail(SSQ_ERR_INVALID_ARG, "unknown state kind");
+    if (d->kind != SSQ_MAMBA2 && d->kind != SSQ_DELTA && d->kind != SSQ_GATED) return fail(SSQ_ERR_INVALID_ARG, "unknown state kind");
     if (!fmt_valid(d->format)) return fail(SSQ_ERR_INVALID_ARG, "unknown format");
     if (d->batch <= 0 || d->nheads <= 0 || d->ngroups <= 0 || d->rows_per_head <= 0 || d->row_len <= 0)
         return fail(SSQ_ERR_INVALID_ARG, "every dimension must be positive");
     if (d->nheads % d->ngroups != 0) return fail(SSQ_ERR_INVALID_ARG, "ngroups must divide nheads");
     if (d->kind == SSQ_DELTA && d->ngroups != 1) return fail(SSQ_ERR_INVALID_ARG, "a delta state has ngroups == 1");
-    if (d->row_len != 128) return fail(SSQ_ERR_UNSUPPORTED, "kernels are built for row_len == 128");
+    if (d->kind == SSQ_GATED) {
+        if (d->nheads != 1 || d->rows_per_head != 1)
+            return fail(SSQ_ERR_INVALID_ARG, "a gated state has nheads == ngroups == rows_per_head == 1");
+        if (d->format != SSQ_FP32) return fail(SSQ_ERR_UNSUPPORTED, "a gated state is fp32");
+        if (d->row_len % 8 != 0 || d->row_len > ssq::kMaxChannels)
+            return fail(SSQ_ERR_UNSUPPORTED, "a gated state has a multiple of 8 channels, 2^20 at most");
+    } else if (d->row_len != 128) {
+        return fail(SSQ_ERR_UNSUPPORTED, "kernels are built for row_len == 128");
+    }
     if (d->kind == SSQ_MAMBA2 && d->rows_per_head % 16 != 0)
         return fail(SSQ_ERR_UNSUPPORTED, "Mamba-2 kernels need rows_per_head to be a multiple of 16");
     if (d->kind == SSQ_DELTA && d->rows_per_head != 128)
@@ -175,6 +183,18 @@ int64_t grid_rows(const ssq_state* st)
     return (int64_t)(st->lay.rows / 128) * (128 - SSQ_DAMP_NHI);
 }
 
+// a gated state's numbers, which are fp32 as they stand; a launch stays below 2^32 work-items
+hipError_t copy_state(void* dst, const void* src, size_t bytes, hipStream_t st)
+{
+    const size_t most = (size_t)1 << 35;
+    for (size_t at = 0; at < bytes; at += most) {
+        const hipError_t e = ssq::launch_stream_copy((uint8_t*)dst + at, (const uint8_t*)src + at,
+                                                     (int64_t)(bytes - at < most ? bytes - at : most), st);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 #define SSQ_REQUIRE(cond, status, msg)            \
     do {                                           \
         if (!(cond)) return fail((status), (msg)); \
@@ -238,7 +258,9 @@ ssq_status ssq_alloc_state(const ssq_desc* desc, void* storage, const float* ini
     // every byte of the storage is written: zero first (padding, the token counter), then the
     // quantized rows of `init`
     e = ssq::launch_zero_fill(st->storage, lay.total_bytes, hs);
-    if (e == hipSuccess && init) {
+    if (e == hipSuccess && init && desc->kind == SSQ_GATED) {
+        e = copy_state(st->storage, init, lay.rows * lay.row_bytes, hs);
+    } else if (e == hipSuccess && init) {
         ssq::QArgs a{};
         a.codes = codes_ptr(st);
         a.scale = scale_ptr(st);
@@ -337,7 +359,7 @@ static ssq_status fill_m2(ssq_state* st, const float* x, const float* dt, const 
                           const float* C, const float* D, float* y, int32_t readout, ssq::M2Args* a)
 {
     SSQ_REQUIRE(st, SSQ_ERR_INVALID_ARG, "state is NULL");
-    SSQ_REQUIRE(st->desc.kind == SSQ_MAMBA2, SSQ_ERR_KIND_MISMATCH, "a Mamba-2 call on a delta state");
+    SSQ_REQUIRE(st->desc.kind == SSQ_MAMBA2, SSQ_ERR_KIND_MISMATCH, "a Mamba-2 call on a state of another kind");
     SSQ_REQUIRE(x && dt && A && B && C && D && y, SSQ_ERR_INVALID_ARG, "an input or output pointer is NULL");
     SSQ_REQUIRE(aligned(x, 4) && aligned(dt, 4) && aligned(A, 4) && aligned(D, 4) && aligned(y, 4),
                 SSQ_ERR_INVALID_ARG, "x, dt, A, D and y must be 4-byte aligned");
@@ -414,7 +436,7 @@ static ssq_status delta_common(ssq_state* st, const float* q, const float* k, co
                                const float* beta, float* o, int32_t readout, void* stream, bool kda)
 {
     SSQ_REQUIRE(st, SSQ_ERR_INVALID_ARG, "state is NULL");
-    SSQ_REQUIRE(st->desc.kind == SSQ_DELTA, SSQ_ERR_KIND_MISMATCH, "a delta-rule call on a Mamba-2 state");
+    SSQ_REQUIRE(st->desc.kind == SSQ_DELTA, SSQ_ERR_KIND_MISMATCH, "a delta-rule call on a state of another kind");
     SSQ_REQUIRE(q && k && v && alpha && beta && o, SSQ_ERR_INVALID_ARG, "an input or output pointer is NULL");
     SSQ_REQUIRE(aligned(q, 4) && aligned(k, 4) && aligned(alpha, 4) && aligned(beta, 4) && aligned(o, 4),
                 SSQ_ERR_INVALID_ARG, "q, k, alpha, beta and o must be 4-byte aligned");
@@ -468,6 +490,9 @@ ssq_status ssq_dequant(const ssq_state* st, float* out, void* stream)
     SSQ_REQUIRE(aligned(out, 16), SSQ_ERR_INVALID_ARG, "out must be 16-byte aligned");
     ssq_status s = check_device(st);
     if (s != SSQ_OK) return s;
+    if (st->desc.kind == SSQ_GATED)
+        return from_hip(copy_state(out, st->storage, st->lay.rows * st->lay.row_bytes, (hipStream_t)stream),
+                        "dequant launch");
     ssq::QArgs a{};
     a.codes = codes_ptr(st);
     a.scale = scale_ptr(st);
@@ -656,6 +681,25 @@ ssq_status ssq_beam_select(const ssq_beam_desc* d, const void* logits, const flo
     return from_hip(ssq::launch_beam_select(d->dtype, a, (hipStream_t)stream), "beam selection launch");
 }
 
+// the arrays of a state and each sequence's bytes in them; 4 at most
+static int state_parts(const ssq_state* st, ssq::ReorderPart* parts)
+{
+    const int64_t rows = (int64_t)(st->lay.rows / (size_t)st->desc.batch);
+    const int64_t low = st->desc.format == SSQ_DAMP ? rows / 128 * (128 - SSQ_DAMP_NHI) : rows;
+    int n = 0;
+    parts[n++] = {codes_ptr(st), low * (int64_t)st->lay.row_bytes};
+    if (scale_ptr(st)) parts[n++] = {(uint8_t*)scale_ptr(st), low * 4};
+    if (zero_ptr(st)) parts[n++] = {(uint8_t*)zero_ptr(st), low * 4};
+    if (hi_ptr(st)) parts[n++] = {(uint8_t*)hi_ptr(st), (rows - low) * 256};
+    return n;
+}
+
+static bool share_memory(const ssq_state* a, const ssq_state* b)
+{
+    const uintptr_t p = (uintptr_t)a->storage, q = (uintptr_t)b->storage;
+    return p < q + b->lay.total_bytes && q < p + a->lay.total_bytes;
+}
+
 ssq_status ssq_state_reorder(ssq_state* const* states, int32_t nstates, const int32_t* parents, int32_t beams,
                              void* stream)
 {
@@ -675,25 +719,320 @@ ssq_status ssq_state_reorder(ssq_state* const* states, int32_t nstates, const in
         const ssq_status s = check_device(st);
         if (s != SSQ_OK) return s;
         // two handles over the same bytes would move them twice at once
-        const uintptr_t p = (uintptr_t)st->storage;
-        for (int j = 0; j < i; ++j) {
-            const uintptr_t q = (uintptr_t)states[j]->storage;
-            SSQ_REQUIRE(p + st->lay.total_bytes <= q || q + states[j]->lay.total_bytes <= p, SSQ_ERR_INVALID_ARG,
-                        "two of the states share memory");
-        }
-        // rows are ordered by sequence, and a sequence's rows are a multiple of 16: so are its bytes in every array
+        for (int j = 0; j < i; ++j)
+            SSQ_REQUIRE(!share_memory(st, states[j]), SSQ_ERR_INVALID_ARG, "two of the states share memory");
+        // rows are ordered by sequence, and a sequence's rows are a multiple of 16 (a gated state's channels of 8): its
+        // bytes in every array are a multiple of 16
         const int64_t rows = (int64_t)(st->lay.rows / (size_t)st->desc.batch);
-        const int64_t low = st->desc.format == SSQ_DAMP ? rows / 128 * (128 - SSQ_DAMP_NHI) : rows;
-        parts[n++] = {codes_ptr(st), low * (int64_t)st->lay.row_bytes};
-        if (scale_ptr(st)) parts[n++] = {(uint8_t*)scale_ptr(st), low * 4};
-        if (zero_ptr(st)) parts[n++] = {(uint8_t*)zero_ptr(st), low * 4};
-        if (hi_ptr(st)) parts[n++] = {(uint8_t*)hi_ptr(st), (rows - low) * 256};
+        n += state_parts(st, parts + n);
         SSQ_REQUIRE(ssq::reorder_blocks(rows * (int64_t)st->lay.row_bytes, st->desc.batch / beams) <= ssq::kMaxBlocks,
                     SSQ_ERR_UNSUPPORTED, "a state has too many bytes for each beam");
     }
     if (beams == 1) return ok();
     return from_hip(ssq::launch_reorder(parts, n, parents, beams, states[0]->desc.batch / beams, (hipStream_t)stream),
                     "state reorder launch");
+}
+
+// ---------------------------------------------------------------------------
+// moves between sequences
+// ---------------------------------------------------------------------------
+ssq_status ssq_state_move(ssq_state* const* states, ssq_state* const* sources, int32_t nstates, const int32_t* to,
+                          const int32_t* from, int32_t nmoves, void* stream)
+{
+    constexpr int kMost = 1024; // states of one call
+    SSQ_REQUIRE(nstates >= 0 && nstates <= kMost, SSQ_ERR_INVALID_ARG, "nstates must be 0 .. 1024");
+    SSQ_REQUIRE(nmoves >= 0 && nmoves <= ssq::kMaxMoves, SSQ_ERR_INVALID_ARG, "nmoves must be 0 .. 65535");
+    if (nstates == 0 || nmoves == 0) return ok();
+    SSQ_REQUIRE(states && to && from, SSQ_ERR_INVALID_ARG, "states, to or from is NULL");
+    SSQ_REQUIRE(aligned(to, 4) && aligned(from, 4), SSQ_ERR_INVALID_ARG, "to and from must be 4-byte aligned");
+    ssq::MovePart parts[4 * kMost];
+    int n = 0;
+    for (int i = 0; i < nstates; ++i) {
+        const ssq_state* st = states[i];
+        const ssq_state* src = sources ? sources[i] : st;
+        SSQ_REQUIRE(st && src, SSQ_ERR_INVALID_ARG, "a state is NULL");
+        SSQ_REQUIRE(st->desc.batch == states[0]->desc.batch, SSQ_ERR_INVALID_ARG, "the states differ in their batch");
+        ssq_status s = check_device(st);
+        if (s != SSQ_OK) return s;
+        if (sources) {
+            SSQ_REQUIRE(src->desc.batch == sources[0]->desc.batch, SSQ_ERR_INVALID_ARG, "the sources differ in their batch");
+            SSQ_REQUIRE(src->desc.kind == st->desc.kind, SSQ_ERR_KIND_MISMATCH, "a source is of another kind");
+            SSQ_REQUIRE(src->desc.format == st->desc.format && src->desc.nheads == st->desc.nheads &&
+                            src->desc.rows_per_head == st->desc.rows_per_head && src->desc.row_len == st->desc.row_len,
+                        SSQ_ERR_INVALID_ARG, "a source is of another format or size");
+            s = check_device(src);
+            if (s != SSQ_OK) return s;
+        }
+        for (int j = 0; j < nstates; ++j) {
+            SSQ_REQUIRE(j >= i || !share_memory(st, states[j]), SSQ_ERR_INVALID_ARG, "two of the states share memory");
+            SSQ_REQUIRE(!sources || !sources[j] || !share_memory(st, sources[j]), SSQ_ERR_INVALID_ARG,
+                        "a state and a source share memory");
+        }
+        ssq::ReorderPart d[4], f[4];
+        const int m = state_parts(st, d);
+        (void)state_parts(src, f);
+        for (int j = 0; j < m; ++j) {
+            SSQ_REQUIRE(d[j].bytes <= ssq::kMaxBlocks * ssq::kColumnBytes, SSQ_ERR_UNSUPPORTED,
+                        "a state has too many bytes for each sequence");
+            parts[n++] = {d[j].p, f[j].p, d[j].bytes};
+        }
+    }
+    return from_hip(ssq::launch_move(parts, n, to, from, nmoves, states[0]->desc.batch,
+                                     (sources ? sources : states)[0]->desc.batch, !sources, (hipStream_t)stream),
+                    "state move launch");
+}
+
+// ---------------------------------------------------------------------------
+// gated linear recurrence
+// ---------------------------------------------------------------------------
+// one tensor of [tokens][channels]
+static ssq_status check_rows(const void* p, int64_t stride, int dtype, int64_t channels, int64_t tokens, const char* name)
+{
+    const int64_t unit = dtype == SSQ_DTYPE_FP32 ? 4 : 8; // elements in 16 bytes
+    SSQ_REQUIRE(p || tokens == 0, SSQ_ERR_INVALID_ARG, std::string(name) + " is NULL");
+    SSQ_REQUIRE(aligned(p, 16) && stride % unit == 0, SSQ_ERR_INVALID_ARG,
+                std::string(name) + " must be 16-byte aligned, its stride a multiple of 16 bytes");
+    SSQ_REQUIRE(stride >= channels, SSQ_ERR_INVALID_ARG, std::string(name) + ": a stride is shorter than a token's row");
+    SSQ_REQUIRE(stride <= ((int64_t)1 << 23), SSQ_ERR_UNSUPPORTED, "strides must not exceed 2^23 elements");
+    return SSQ_OK;
+}
+
+#define SSQ_TRY(call)                      \
+    do {                                   \
+        const ssq_status s_ = (call);      \
+        if (s_ != SSQ_OK) return s_;       \
+    } while (0)
+
+static ssq_status check_gated(const ssq_state* st, int dtype, int gate, int input, int channels, int32_t nseq,
+                              int64_t tokens, const int32_t* slots, int64_t most)
+{
+    SSQ_REQUIRE(!st || st->desc.kind == SSQ_GATED, SSQ_ERR_KIND_MISMATCH, "the gated recurrence runs on an SSQ_GATED state");
+    SSQ_REQUIRE(dtype_valid(dtype), SSQ_ERR_INVALID_ARG, "unknown dtype");
+    SSQ_REQUIRE(gate == SSQ_GATE_LOG || gate == SSQ_GATE_SIGMOID, SSQ_ERR_INVALID_ARG, "unknown gate");
+    SSQ_REQUIRE(input >= SSQ_INPUT_PLAIN && input <= SSQ_INPUT_NORM, SSQ_ERR_INVALID_ARG, "unknown input factor");
+    SSQ_REQUIRE(channels > 0, SSQ_ERR_INVALID_ARG, "channels must be positive");
+    SSQ_REQUIRE(channels % 8 == 0 && channels <= ssq::kMaxChannels, SSQ_ERR_UNSUPPORTED,
+                "channels must be a multiple of 8, 2^20 at most");
+    SSQ_REQUIRE(!st || st->desc.row_len == channels, SSQ_ERR_INVALID_ARG, "the state has another number of channels");
+    SSQ_REQUIRE(nseq >= 0 && tokens >= 0, SSQ_ERR_INVALID_ARG, "nseq and tokens must not be negative");
+    SSQ_REQUIRE(tokens <= kMostTokens, SSQ_ERR_UNSUPPORTED, "a call takes fewer than 2^31-128 tokens");
+    SSQ_REQUIRE(nseq <= most / channels, SSQ_ERR_UNSUPPORTED, "the call covers too many sequences and channels");
+    SSQ_REQUIRE(st || !slots, SSQ_ERR_INVALID_ARG, "slots without a state");
+    SSQ_REQUIRE(!st || slots || nseq <= st->desc.batch, SSQ_ERR_INVALID_ARG, "without slots nseq must not exceed the batch");
+    SSQ_REQUIRE(aligned(slots, 4), SSQ_ERR_INVALID_ARG, "slots must be 4-byte aligned");
+    return SSQ_OK;
+}
+
+static ssq_status check_gated_workspace(int channels, int32_t nseq, int64_t tokens, const void* workspace, size_t bytes)
+{
+    const size_t need = ssq_gated_workspace(channels, nseq, tokens);
+    SSQ_REQUIRE(need == 0 || (workspace && bytes >= need), SSQ_ERR_INVALID_ARG, "the workspace is too small");
+    SSQ_REQUIRE(aligned(workspace, 256), SSQ_ERR_INVALID_ARG, "the workspace must be 256-byte aligned");
+    return SSQ_OK;
+}
+
+static ssq_status fill_gated(const ssq_state* st, const ssq_gated_io* io, int32_t nseq, int64_t tokens, const int32_t* slots,
+                             int64_t most, ssq::GatedArgs* a)
+{
+    SSQ_REQUIRE(io, SSQ_ERR_INVALID_ARG, "io is NULL");
+    SSQ_TRY(check_gated(st, io->dtype, io->gate, io->input, io->channels, nseq, tokens, slots, most));
+    SSQ_TRY(check_rows(io->x, io->x_stride, io->dtype, io->channels, tokens, "x"));
+    SSQ_TRY(check_rows(io->g, io->g_stride, io->dtype, io->channels, tokens, "g"));
+    SSQ_TRY(check_rows(io->o, io->o_stride, io->dtype, io->channels, tokens, "o"));
+    if (st) SSQ_TRY(check_device(st));
+    *a = ssq::GatedArgs{};
+    a->x = io->x;
+    a->g = io->g;
+    a->o = io->o;
+    a->xs = io->x_stride;
+    a->gs = io->g_stride;
+    a->os = io->o_stride;
+    a->h = st ? (float*)codes_ptr(st) : nullptr;
+    a->slots = slots;
+    a->tokens = tokens;
+    a->nseq = nseq;
+    a->batch = st ? st->desc.batch : 0;
+    a->channels = io->channels;
+    return SSQ_OK;
+}
+
+int64_t ssq_gated_checkpoint_rows(int32_t nseq, int64_t tokens)
+{
+    if (nseq < 0 || tokens < 0 || tokens > kMostTokens) return -1;
+    return tokens / SSQ_GATED_CHUNK + nseq;
+}
+
+static int current_cus()
+{
+    int dev = -1;
+    if (hipGetDevice(&dev) != hipSuccess) {
+        (void)hipGetLastError();
+        dev = -1;
+    }
+    return num_cus(dev);
+}
+
+size_t ssq_gated_workspace(int32_t channels, int32_t nseq, int64_t tokens)
+{
+    if (check_gated(nullptr, SSQ_DTYPE_FP32, SSQ_GATE_LOG, SSQ_INPUT_PLAIN, channels, nseq, tokens, nullptr,
+                    ssq::kMaxGatedRows) != SSQ_OK)
+        return (size_t)-1;
+    return ssq::gated_workspace(channels, nseq, tokens, current_cus());
+}
+
+ssq_status ssq_gated_scan(ssq_state* st, const ssq_gated_io* io, int32_t nseq, int64_t tokens, const int32_t* cu_seqlens,
+                          const int32_t* slots, const uint8_t* fresh, float* checkpoints, void* workspace,
+                          size_t workspace_bytes, void* stream)
+{
+    ssq::GatedArgs a;
+    SSQ_TRY(fill_gated(st, io, nseq, tokens, slots, ssq::kMaxGatedRows, &a));
+    SSQ_REQUIRE(st || !fresh, SSQ_ERR_INVALID_ARG, "fresh without a state");
+    SSQ_REQUIRE(nseq == 0 || cu_seqlens, SSQ_ERR_INVALID_ARG, "cu_seqlens is NULL");
+    SSQ_REQUIRE(aligned(cu_seqlens, 4), SSQ_ERR_INVALID_ARG, "cu_seqlens must be 4-byte aligned");
+    SSQ_REQUIRE(aligned(checkpoints, 16), SSQ_ERR_INVALID_ARG, "checkpoints must be 16-byte aligned");
+    SSQ_TRY(check_gated_workspace(io->channels, nseq, tokens, workspace, workspace_bytes));
+    if (nseq == 0) return ok();
+    a.cu = cu_seqlens;
+    a.fresh = fresh;
+    a.ckpt = checkpoints;
+    return from_hip(ssq::launch_gated_scan(io->dtype, io->gate, io->input, a, workspace, current_cus(), (hipStream_t)stream),
+                    "gated scan launch");
+}
+
+ssq_status ssq_gated_scan_backward(const ssq_state* st, const ssq_gated_grad* io, int32_t nseq, int64_t tokens,
+                                   const int32_t* cu_seqlens, const int32_t* slots, const float* checkpoints,
+                                   void* workspace, size_t workspace_bytes, void* stream)
+{
+    SSQ_REQUIRE(io, SSQ_ERR_INVALID_ARG, "io is NULL");
+    SSQ_TRY(check_gated(st, io->dtype, io->gate, io->input, io->channels, nseq, tokens, slots, ssq::kMaxGatedRows));
+    SSQ_TRY(check_rows(io->x, io->x_stride, io->dtype, io->channels, tokens, "x"));
+    SSQ_TRY(check_rows(io->g, io->g_stride, io->dtype, io->channels, tokens, "g"));
+    SSQ_TRY(check_rows(io->dout, io->dout_stride, io->dtype, io->channels, tokens, "dout"));
+    SSQ_TRY(check_rows(io->dx, io->dx_stride, io->dtype, io->channels, tokens, "dx"));
+    SSQ_TRY(check_rows(io->dg, io->dg_stride, io->dtype, io->channels, tokens, "dg"));
+    SSQ_REQUIRE(nseq == 0 || cu_seqlens, SSQ_ERR_INVALID_ARG, "cu_seqlens is NULL");
+    SSQ_REQUIRE(aligned(cu_seqlens, 4), SSQ_ERR_INVALID_ARG, "cu_seqlens must be 4-byte aligned");
+    SSQ_REQUIRE(checkpoints || tokens == 0 || nseq == 0, SSQ_ERR_INVALID_ARG, "checkpoints is NULL");
+    SSQ_REQUIRE(aligned(checkpoints, 16) && aligned(io->dlast, 16) && aligned(io->dfirst, 16), SSQ_ERR_INVALID_ARG,
+                "checkpoints, dlast and dfirst must be 16-byte aligned");
+    SSQ_TRY(check_gated_workspace(io->channels, nseq, tokens, workspace, workspace_bytes));
+    if (nseq == 0) return ok();
+    ssq::GatedArgs a{};
+    a.x = io->x;
+    a.g = io->g;
+    a.dout = io->dout;
+    a.dx = io->dx;
+    a.dg = io->dg;
+    a.dlast = io->dlast;
+    a.dfirst = io->dfirst;
+    a.xs = io->x_stride;
+    a.gs = io->g_stride;
+    a.dos = io->dout_stride;
+    a.dxs = io->dx_stride;
+    a.dgs = io->dg_stride;
+    a.ckpt = const_cast<float*>(checkpoints);
+    a.cu = cu_seqlens;
+    a.slots = slots;
+    a.tokens = tokens;
+    a.nseq = nseq;
+    a.batch = st ? st->desc.batch : 0;
+    a.channels = io->channels;
+    return from_hip(ssq::launch_gated_backward(io->dtype, io->gate, io->input, a, workspace, current_cus(), (hipStream_t)stream),
+                    "gated scan gradient launch");
+}
+
+ssq_status ssq_gated_step(ssq_state* st, const ssq_gated_io* io, int32_t nseq, const int32_t* slots, void* stream)
+{
+    ssq::GatedArgs a;
+    SSQ_REQUIRE(st, SSQ_ERR_INVALID_ARG, "state is NULL");
+    SSQ_TRY(fill_gated(st, io, nseq, nseq, slots, ssq::kMaxGatedStep, &a));
+    if (nseq == 0) return ok();
+    return from_hip(ssq::launch_gated_step(io->dtype, io->gate, io->input, a, (hipStream_t)stream), "gated step launch");
+}
+
+// ---------------------------------------------------------------------------
+// group norm
+// ---------------------------------------------------------------------------
+static ssq_status check_norm_size(int64_t groups, int64_t width, int64_t tokens)
+{
+    SSQ_REQUIRE(groups > 0 && width > 0 && tokens >= 0, SSQ_ERR_INVALID_ARG,
+                "groups and width must be positive, tokens not negative");
+    SSQ_REQUIRE(width % 8 == 0 && width <= ssq::kMaxNormWidth, SSQ_ERR_UNSUPPORTED, "width must be a multiple of 8, 16384 at most");
+    SSQ_REQUIRE(groups * width <= ssq::kMaxChannels, SSQ_ERR_UNSUPPORTED, "a token has 2^20 channels at most");
+    SSQ_REQUIRE(tokens <= ((int64_t)1 << 31) / groups, SSQ_ERR_UNSUPPORTED, "tokens * groups must not exceed 2^31");
+    return SSQ_OK;
+}
+
+static ssq_status fill_norm(const ssq_norm_io* io, int64_t tokens, ssq::NormArgs* a)
+{
+    SSQ_REQUIRE(io, SSQ_ERR_INVALID_ARG, "io is NULL");
+    SSQ_REQUIRE(dtype_valid(io->dtype), SSQ_ERR_INVALID_ARG, "unknown dtype");
+    SSQ_REQUIRE(io->act >= SSQ_ACT_SILU && io->act <= SSQ_ACT_GATE_INPUT, SSQ_ERR_INVALID_ARG, "unknown activation");
+    SSQ_TRY(check_norm_size(io->groups, io->width, tokens));
+    SSQ_REQUIRE(io->eps >= 1.17549435e-38f && io->eps < 1e30f, SSQ_ERR_INVALID_ARG, "eps must be a positive number");
+    const int64_t row = (int64_t)io->groups * io->width;
+    SSQ_TRY(check_rows(io->x, io->x_stride, io->dtype, row, tokens, "x"));
+    if (io->act == SSQ_ACT_SILU) SSQ_REQUIRE(!io->z, SSQ_ERR_INVALID_ARG, "SSQ_ACT_SILU has no z");
+    else SSQ_TRY(check_rows(io->z, io->z_stride, io->dtype, row, tokens, "z"));
+    SSQ_REQUIRE(aligned(io->weight, 16) && aligned(io->bias, 16), SSQ_ERR_INVALID_ARG, "weight and bias must be 16-byte aligned");
+    *a = ssq::NormArgs{};
+    a->x = io->x;
+    a->z = io->z;
+    a->weight = io->weight;
+    a->bias = io->bias;
+    a->xs = io->x_stride;
+    a->zs = io->z_stride;
+    a->tokens = tokens;
+    a->groups = io->groups;
+    a->width = io->width;
+    a->eps = io->eps;
+    a->center = io->center != 0;
+    return SSQ_OK;
+}
+
+ssq_status ssq_group_norm(const ssq_norm_io* io, void* y, int64_t y_stride, int64_t tokens, void* stream)
+{
+    ssq::NormArgs a;
+    SSQ_TRY(fill_norm(io, tokens, &a));
+    SSQ_TRY(check_rows(y, y_stride, io->dtype, (int64_t)io->groups * io->width, tokens, "y"));
+    if (tokens == 0) return ok();
+    a.y = y;
+    a.ys = y_stride;
+    return from_hip(ssq::launch_group_norm(io->dtype, io->act, a, (hipStream_t)stream), "group norm launch");
+}
+
+size_t ssq_group_norm_workspace(int32_t groups, int32_t width, int64_t tokens)
+{
+    if (check_norm_size(groups, width, tokens) != SSQ_OK) return (size_t)-1;
+    return ssq::norm_workspace(groups, width, tokens);
+}
+
+ssq_status ssq_group_norm_backward(const ssq_norm_io* io, const ssq_norm_grad* grad, int64_t tokens, void* workspace,
+                                   size_t workspace_bytes, void* stream)
+{
+    ssq::NormArgs a;
+    SSQ_TRY(fill_norm(io, tokens, &a));
+    SSQ_REQUIRE(grad, SSQ_ERR_INVALID_ARG, "grad is NULL");
+    const int64_t row = (int64_t)io->groups * io->width;
+    SSQ_TRY(check_rows(grad->dy, grad->dy_stride, io->dtype, row, tokens, "dy"));
+    SSQ_TRY(check_rows(grad->dx, grad->dx_stride, io->dtype, row, tokens, "dx"));
+    if (io->act == SSQ_ACT_SILU) SSQ_REQUIRE(!grad->dz, SSQ_ERR_INVALID_ARG, "SSQ_ACT_SILU has no dz");
+    else SSQ_TRY(check_rows(grad->dz, grad->dz_stride, io->dtype, row, tokens, "dz"));
+    SSQ_REQUIRE(aligned(grad->dweight, 16) && aligned(grad->dbias, 16), SSQ_ERR_INVALID_ARG,
+                "dweight and dbias must be 16-byte aligned");
+    const size_t need = ssq_group_norm_workspace(io->groups, io->width, tokens);
+    SSQ_REQUIRE(need == 0 || (workspace && workspace_bytes >= need), SSQ_ERR_INVALID_ARG, "the workspace is too small");
+    SSQ_REQUIRE(aligned(workspace, 256), SSQ_ERR_INVALID_ARG, "the workspace must be 256-byte aligned");
+    a.dy = grad->dy;
+    a.dx = grad->dx;
+    a.dz = grad->dz;
+    a.dweight = grad->dweight;
+    a.dbias = grad->dbias;
+    a.dys = grad->dy_stride;
+    a.dxs = grad->dx_stride;
+    a.dzs = grad->dz_stride;
+    a.ws = (float*)workspace;
+    return from_hip(ssq::launch_group_norm_backward(io->dtype, io->act, a, (hipStream_t)stream), "group norm gradient launch");
 }
 
 const char* ssq_status_string(int32_t status)

@@ -1,5 +1,5 @@
 // ssq_ops.h -- argument blocks and launchers of the linear-attention, beam-search and
-// state-reordering kernels, shared with the C-ABI layer (not part of the public interface).
+// state-reordering kernels, of the gated recurrence, the group norm and the moves of states, shared with the C-ABI layer (not part of the public interface).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -60,6 +60,71 @@ struct ReorderPart {
 constexpr int64_t kColumnBytes = 256 * 16; // what a workgroup moves of each sequence of a group
 constexpr int64_t reorder_blocks(int64_t bytes, int64_t groups) { return (bytes + kColumnBytes - 1) / kColumnBytes * groups; }
 
+// gated linear recurrence
+struct GatedArgs {
+    const void* x;
+    const void* g;
+    void* o;            // scan, step
+    const void* dout;   // gradient: of o
+    void* dx;
+    void* dg;
+    const float* dlast; // [nseq][channels] or nullptr
+    float* dfirst;      // [nseq][channels] or nullptr
+    int64_t xs, gs, os, dos, dxs, dgs; // elements from one token to the next
+    float* h;           // the state [batch][channels]; nullptr: from zero, not kept
+    float* ckpt;        // [tokens/16 + nseq][channels]; scan: or nullptr
+    const int32_t* cu;  // [nseq + 1]
+    const int32_t* slots;
+    const uint8_t* fresh;
+    int64_t tokens;
+    int nseq, batch, channels; // batch: of the slots (0: there are none)
+};
+enum Gate : int { GATE_LOG = 0, GATE_SIGMOID = 1 };
+enum Input : int { IN_PLAIN = 0, IN_COMPLEMENT = 1, IN_NORM = 2 };
+constexpr int kGatedChunk = 16; // tokens from one checkpoint to the next
+constexpr int64_t kMaxGatedRows = (int64_t)1 << 26; // nseq * channels of a scan
+constexpr int64_t kMaxGatedStep = (int64_t)1 << 31;
+constexpr int kMaxChannels = 1 << 20;
+
+// group norm with an activation
+enum Act : int { ACT_SILU = 0, ACT_GATE_OUTPUT = 1, ACT_GATE_INPUT = 2 };
+struct NormArgs {
+    const void* x;
+    const void* z;
+    const float* weight;
+    const float* bias;
+    void* y;
+    const void* dy;
+    void* dx;
+    void* dz;
+    float* dweight;
+    float* dbias;
+    float* ws;
+    int64_t xs, zs, ys, dys, dxs, dzs;
+    int64_t tokens;
+    int groups, width;
+    float eps;
+    bool center;
+};
+constexpr int kMaxNormWidth = 16384;
+
+// one array of a state that sequences move in: `bytes` (a multiple of 16) for each sequence
+struct MovePart {
+    uint8_t* dst;
+    const uint8_t* src;
+    int64_t bytes;
+};
+constexpr int kMaxMoves = 65535;
+
+size_t gated_workspace(int channels, int nseq, int64_t tokens, int num_cus);
+hipError_t launch_gated_scan(int dtype, int gate, int input, const GatedArgs& a, void* ws, int num_cus, hipStream_t st);
+hipError_t launch_gated_backward(int dtype, int gate, int input, const GatedArgs& a, void* ws, int num_cus, hipStream_t st);
+hipError_t launch_gated_step(int dtype, int gate, int input, const GatedArgs& a, hipStream_t st);
+size_t norm_workspace(int groups, int width, int64_t tokens);
+hipError_t launch_group_norm(int dtype, int act, const NormArgs& a, hipStream_t st);
+hipError_t launch_group_norm_backward(int dtype, int act, const NormArgs& a, hipStream_t st);
+hipError_t launch_move(const MovePart* parts, int nparts, const int32_t* to, const int32_t* from, int nmoves, int batch,
+                       int sources, bool inside, hipStream_t st);
 hipError_t launch_linattn_step(int fmt, int dtype, const LinArgs& a, bool pre, hipStream_t st);
 size_t linattn_workspace(int fmt, int nseq, int64_t tokens, int H, int P, int num_cus);
 hipError_t launch_linattn_prefill(int fmt, int dtype, const LinArgs& a, void* ws, int num_cus, hipStream_t st);
