@@ -6,77 +6,380 @@
 
 namespace ssq {
 
-// one thread a sequence and channel, one token after the other
-template <int DT, int GATE, int INPUT>
-__global__ __launch_bounds__(256) void k_gated_scan(GatedArgs a)
-{
-    const int c = (int)(blockIdx.x % ((a.channels + 255) / 256)) * 256 + threadIdx.x;
-    const int seq = (int)(blockIdx.x / ((a.channels + 255) / 256));
-    if (c >= a.channels) return;
-    const int slot = gated_slot(a, seq);
-    if (slot < 0) return;
-    const Span sp = gated_span(a, seq);
-    float* state = a.h ? a.h + (int64_t)slot * a.channels + c : nullptr;
-    float h = state && !(a.fresh && a.fresh[seq]) ? *state : 0.0f;
-    const int64_t row = sp.begin / kGatedChunk + seq;
-    for (int64_t t = 0; t < sp.len; ++t) {
-        if (a.ckpt && t % kGatedChunk == 0) a.ckpt[(row + t / kGatedChunk) * a.channels + c] = h;
-        const GateValue v = gate_value<GATE, INPUT>(load_elem<DT>(a.g, (sp.begin + t) * a.gs + c));
-        h = __builtin_fmaf(v.a, h, v.s * load_elem<DT>(a.x, (sp.begin + t) * a.xs + c));
-        store_elem<DT>(a.o, (sp.begin + t) * a.os + c, h);
+// The tile of a workgroup: a slice of channels, LC lanes of CPL channels (4 bytes of x), and W
+// waves x 64/LC groups of lanes along the tokens, each with a chunk of 16 tokens in registers.
+template <int DT, int LC_, int W_>
+struct Tile {
+    static constexpr int LC = LC_, W = W_, K = kGatedChunk;
+    static constexpr int SIZE = DT == DT_FP32 ? 4 : 2, CPL = 4 / SIZE, S = LC * CPL;
+    static constexpr int TL = 64 / LC, SEGS = W * TL, WAVE_TOKENS = TL * K, TOKENS = SEGS * K;
+    static_assert(TL <= 4, "a wave's rows stay below 2^31 bytes at the largest stride");
+    int wave, tl, c, ch; // wave, group of lanes, first channel within the slice and of all
+    uint32_t bad;        // beyond every descriptor's bytes where the lane's channels are none
+
+    __device__ __forceinline__ Tile(int slice, int channels)
+    {
+        wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+        const int lane = threadIdx.x & 63;
+        tl = lane / LC;
+        c = lane % LC * CPL;
+        ch = slice * S + c;
+        bad = ch < channels ? 0u : kNowhere;
     }
-    if (state) *state = h;
+    __device__ __forceinline__ int seg() const { return wave * TL + tl; }
+    // the wave's rows from token t0 of a tensor on, `left` of them at most
+    __device__ __forceinline__ Rsrc rows(const void* p, int64_t t0, int64_t stride, int64_t left, int channels) const
+    {
+        const int64_t n = left < WAVE_TOKENS ? left : WAVE_TOKENS;
+        const uint32_t bytes = n > 0 ? (uint32_t)((n - 1) * stride * SIZE) + (uint32_t)channels * SIZE : 0u;
+        return uniform_rsrc((uint64_t)p + (uint64_t)(t0 * stride * SIZE), bytes);
+    }
+    // the wave's checkpoints, from chunk j of a sequence on, and the lane's place in them
+    __device__ __forceinline__ Rsrc checkpoints(const float* p, int64_t row, int64_t left, int channels) const
+    {
+        const int64_t chunks = (left + K - 1) / K, n = chunks < TL ? chunks : TL;
+        return uniform_rsrc((uint64_t)p + (uint64_t)(row * channels * 4), p && left > 0 ? (uint32_t)(n * channels * 4) : 0u);
+    }
+    __device__ __forceinline__ uint32_t checkpoint(int channels) const { return ((uint32_t)tl * (uint32_t)channels + (uint32_t)ch) * 4u | bad; }
+    __device__ __forceinline__ uint32_t at(int64_t stride) const { return ((uint32_t)(tl * K) * (uint32_t)stride + (uint32_t)ch) * SIZE | bad; }
+    __device__ __forceinline__ void load(Rsrc r, int64_t stride, uint32_t* v) const
+    {
+        const uint32_t off = at(stride), step = (uint32_t)stride * SIZE;
+#pragma unroll
+        for (int j = 0; j < K; ++j) v[j] = __builtin_amdgcn_raw_buffer_load_b32(r, off, j * step, 0);
+    }
+    __device__ __forceinline__ void store(Rsrc r, int64_t stride, int j, uint32_t v) const
+    {
+        __builtin_amdgcn_raw_buffer_store_b32(v, r, at(stride), (uint32_t)j * (uint32_t)stride * SIZE, kAuxStore);
+    }
+    static __device__ __forceinline__ float get(uint32_t w, int e)
+    {
+        if constexpr (CPL == 1) return __uint_as_float(w);
+        else return to_f32<DT>(e ? w >> 16 : w & 0xFFFFu);
+    }
+    static __device__ __forceinline__ uint32_t put(const float* v)
+    {
+        if constexpr (CPL == 1) return __float_as_uint(v[0]);
+        else return pack_elems<DT>(v[0], v[1]);
+    }
+};
+
+// workgroup i's place where each XCD takes a contiguous range of `n`
+__device__ __forceinline__ int64_t xcd_grouped(int64_t i, int64_t n)
+{
+    const int64_t q = n / 8, r = n % 8, xcd = i % 8;
+    return xcd * q + (xcd < r ? xcd : r) + i / 8;
 }
 
-template <int DT, int GATE, int INPUT>
-__global__ __launch_bounds__(256) void k_gated_backward(GatedArgs a)
+// WHOLE: a workgroup takes a sequence from its start to its end.  PART_SUM, PART_OUT: it takes a part of one, first
+// what the part does to a state (product of its decays, and the state from zero), then the outputs, from the
+// state that the parts before leave.
+enum Stage { WHOLE, PART_SUM, PART_OUT };
+
+// what a workgroup works on
+struct GatedWork {
+    int seq, part, slice;
+};
+__device__ __forceinline__ GatedWork gated_work(const GatedArgs& a)
 {
-    const int c = (int)(blockIdx.x % ((a.channels + 255) / 256)) * 256 + threadIdx.x;
-    const int seq = (int)(blockIdx.x / ((a.channels + 255) / 256));
-    if (c >= a.channels) return;
-    if (gated_slot(a, seq) < 0) return;
-    const Span sp = gated_span(a, seq);
-    const int64_t at = (int64_t)seq * a.channels + c;
-    float dh = a.dlast ? a.dlast[at] : 0.0f;
-    const int64_t row = sp.begin / kGatedChunk + seq;
-    for (int64_t j = (sp.len + kGatedChunk - 1) / kGatedChunk - 1; j >= 0; --j) {
-        const int n = (int)(sp.len - j * kGatedChunk < kGatedChunk ? sp.len - j * kGatedChunk : kGatedChunk);
-        const int64_t t0 = sp.begin + j * kGatedChunk;
-        float before[kGatedChunk];
-        float h = a.ckpt[(row + j) * a.channels + c];
-        for (int i = 0; i < n; ++i) {
-            before[i] = h;
-            const GateValue v = gate_value<GATE, INPUT>(load_elem<DT>(a.g, (t0 + i) * a.gs + c));
-            h = __builtin_fmaf(v.a, h, v.s * load_elem<DT>(a.x, (t0 + i) * a.xs + c));
-        }
-        for (int i = n - 1; i >= 0; --i) {
-            const GateSlope v = gate_slope<GATE, INPUT>(load_elem<DT>(a.g, (t0 + i) * a.gs + c));
-            const float x = load_elem<DT>(a.x, (t0 + i) * a.xs + c);
-            dh += load_elem<DT>(a.dout, (t0 + i) * a.dos + c);
-            store_elem<DT>(a.dx, (t0 + i) * a.dxs + c, v.s * dh);
-            store_elem<DT>(a.dg, (t0 + i) * a.dgs + c, dh * __builtin_fmaf(v.da, before[i], v.ds * x));
-            dh *= v.a;
+    const int64_t i = xcd_grouped(blockIdx.x, gridDim.x), j = i / a.slices;
+    return {(int)(j / a.parts), (int)(j % a.parts), (int)(i % a.slices)};
+}
+
+// Gates of tokens that are not there keep the state: a log gate reads 0, a sigmoid's gets infinity.
+template <int DT, int GATE, class T>
+__device__ __forceinline__ void keep_absent(const T& t, int64_t left, uint32_t* rg)
+{
+    if constexpr (GATE == GATE_SIGMOID) {
+        if (left < T::WAVE_TOKENS) { // the wave's; the same in all lanes
+#pragma unroll
+            for (int j = 0; j < T::K; ++j)
+                if (t.tl * T::K + j >= left) rg[j] = DT == DT_FP32 ? 0x7F800000u : DT == DT_BF16 ? 0x7F807F80u : 0x7C007C00u;
         }
     }
-    if (a.dfirst) a.dfirst[at] = dh;
+}
+
+// What the lanes of a slice carry from segment to segment of a tile: s_a, s_b hold what a segment does to a state, s_h
+// receives the state before each; `product` goes on over all of them.
+template <int SEGS, int S, bool BACK, bool SUM>
+struct Carry {
+    float (*s_a)[S];
+    float (*s_b)[S];
+    float (*s_h)[S];
+    __device__ __forceinline__ void along(float& h, float& product) const
+    {
+#pragma unroll
+        for (int k = 0; k < SEGS; ++k) {
+            const int i = BACK ? SEGS - 1 - k : k;
+            if (!SUM) s_h[i][threadIdx.x] = h;
+            h = __builtin_fmaf(s_a[i][threadIdx.x], h, s_b[i][threadIdx.x]);
+            if (SUM) product *= s_a[i][threadIdx.x];
+        }
+    }
+};
+
+template <int DT, int GATE, int INPUT, int LC, int W>
+struct Scan {
+    using T = Tile<DT, LC, W>;
+    static constexpr int K = T::K, CPL = T::CPL;
+    // product of the decays, and the state from zero, behind each token
+    float through[K][CPL], own[K][CPL];
+
+    static __device__ __forceinline__ void load(const GatedArgs& a, const T& t, const Span& sp, int64_t base, int64_t end, uint32_t* rg, uint32_t* rx)
+    {
+        const int64_t t0 = base + t.wave * T::WAVE_TOKENS, left = end - t0;
+        t.load(t.rows(a.g, sp.begin + t0, a.gs, left, a.channels), a.gs, rg);
+        t.load(t.rows(a.x, sp.begin + t0, a.xs, left, a.channels), a.xs, rx);
+    }
+    __device__ __forceinline__ void sums(const T& t, int64_t left, uint32_t* rg, const uint32_t* rx, float (*s_a)[T::S], float (*s_b)[T::S])
+    {
+        keep_absent<DT, GATE>(t, left, rg);
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+#pragma unroll
+            for (int e = 0; e < CPL; ++e) {
+                const GateValue v = gate_value<GATE, INPUT>(T::get(rg[j], e));
+                const float in = v.s * T::get(rx[j], e);
+                through[j][e] = j ? through[j - 1][e] * v.a : v.a;
+                own[j][e] = j ? __builtin_fmaf(v.a, own[j - 1][e], in) : in;
+            }
+#pragma unroll
+        for (int e = 0; e < CPL; ++e) {
+            s_a[t.seg()][t.c + e] = through[K - 1][e];
+            s_b[t.seg()][t.c + e] = own[K - 1][e];
+        }
+    }
+    __device__ __forceinline__ void outputs(const GatedArgs& a, const T& t, const Span& sp, int seq, int64_t base, int64_t end, float (*s_h)[T::S])
+    {
+        const int64_t t0 = base + t.wave * T::WAVE_TOKENS, row = sp.begin / K + seq + t0 / K;
+        float before[CPL];
+        uint32_t ck[CPL];
+#pragma unroll
+        for (int e = 0; e < CPL; ++e) {
+            before[e] = s_h[t.seg()][t.c + e];
+            ck[e] = __float_as_uint(before[e]);
+        }
+        buf_store_words<CPL, 0>(t.checkpoints(a.ckpt, row, end - t0, a.channels), t.checkpoint(a.channels), 0u, ck);
+        const Rsrc ro = t.rows(a.o, sp.begin + t0, a.os, end - t0, a.channels);
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            float o[CPL];
+#pragma unroll
+            for (int e = 0; e < CPL; ++e) o[e] = __builtin_fmaf(through[j][e], before[e], own[j][e]);
+            t.store(ro, a.os, j, T::put(o));
+        }
+    }
+};
+
+template <int DT, int GATE, int INPUT, int STAGE, int LC, int W>
+__global__ __launch_bounds__(W * 64, 3) void k_gated_scan(GatedArgs a)
+{
+    using T = Tile<DT, LC, W>;
+    constexpr int K = T::K, S = T::S;
+    __shared__ float s_a[T::SEGS][S], s_b[T::SEGS][S], s_h[T::SEGS][S];
+    const GatedWork work = gated_work(a);
+    const int seq = work.seq, slot = gated_slot(a, seq);
+    if (slot < 0) return;
+    const Span sp = gated_span(a, seq);
+    const int64_t begin = STAGE == WHOLE ? 0 : work.part * a.part_tokens;
+    const bool last = STAGE == WHOLE || begin + a.part_tokens >= sp.len;
+    if (work.part > 0 && begin >= sp.len) return;
+    if (STAGE == PART_SUM && last) return;
+    const int64_t end = last ? sp.len : begin + a.part_tokens;
+    const T t(work.slice, a.channels);
+    const int mine = work.slice * S + threadIdx.x; // the channel that this thread carries along the chunks
+    const bool carrier = threadIdx.x < S && mine < a.channels;
+    float* state = a.h && carrier ? a.h + (int64_t)slot * a.channels + mine : nullptr;
+    const int64_t pitch = (int64_t)a.nseq * a.parts * a.channels;
+    float* sums = a.sums + (int64_t)seq * a.parts * a.channels + mine;
+    float h = 0.0f, product = 1.0f;
+    if (work.part == 0) {
+        // the first of several parts has its start from the sums, as the last one overwrites the state
+        if (STAGE == PART_OUT && !last) h = carrier ? sums[0] : 0.0f;
+        else if (state && !(a.fresh && a.fresh[seq])) h = *state;
+        if (STAGE == PART_SUM && carrier) sums[0] = h;
+    } else if (STAGE == PART_OUT && carrier) {
+        h = sums[pitch];
+#pragma unroll 8
+        for (int p = 1; p < work.part; ++p) h = __builtin_fmaf(sums[(int64_t)p * a.channels], h, sums[pitch + (int64_t)p * a.channels]);
+    }
+    const Carry<T::SEGS, S, false, STAGE == PART_SUM> carry{s_a, s_b, s_h};
+    Scan<DT, GATE, INPUT, LC, W> scan;
+    uint32_t rx[K], rg[K], nx[K], ng[K];
+    scan.load(a, t, sp, begin, end, ng, nx);
+    for (int64_t base = begin; base < end; base += T::TOKENS) {
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            rx[j] = nx[j];
+            rg[j] = ng[j];
+        }
+        scan.load(a, t, sp, base + T::TOKENS, end, ng, nx); // nothing, behind the end
+        scan.sums(t, end - base - t.wave * T::WAVE_TOKENS, rg, rx, s_a, s_b);
+        __syncthreads();
+        if (threadIdx.x < S) carry.along(h, product);
+        __syncthreads();
+        if constexpr (STAGE != PART_SUM) scan.outputs(a, t, sp, seq, base, end, s_h);
+    }
+    if constexpr (STAGE == PART_SUM) {
+        if (carrier) {
+            if (work.part) sums[(int64_t)work.part * a.channels] = product;
+            sums[pitch + (int64_t)work.part * a.channels] = h;
+        }
+    } else if (state && last) {
+        *state = h;
+    }
+}
+
+template <int DT, int GATE, int INPUT, int STAGE, int LC, int W>
+struct Back {
+    using T = Tile<DT, LC, W>;
+    static constexpr int K = T::K, CPL = T::CPL;
+    // each token's decay, factor, and the slope of its state along its gate; gradients of its output
+    float va[K][CPL], vs[K][CPL], slope[K][CPL];
+    uint32_t dy[K];
+    struct Raw {
+        uint32_t x[K], g[K], d[K], s[CPL];
+    };
+
+    static __device__ __forceinline__ void load(const GatedArgs& a, const T& t, const Span& sp, int seq, int64_t base, int64_t end, Raw* r)
+    {
+        const int64_t t0 = base + t.wave * T::WAVE_TOKENS, left = end - t0;
+        t.load(t.rows(a.g, sp.begin + t0, a.gs, left, a.channels), a.gs, r->g);
+        t.load(t.rows(a.dout, sp.begin + t0, a.dos, left, a.channels), a.dos, r->d);
+        if constexpr (STAGE == PART_SUM) return;
+        t.load(t.rows(a.x, sp.begin + t0, a.xs, left, a.channels), a.xs, r->x);
+        buf_load_words<CPL, 0>(t.checkpoints(a.ckpt, sp.begin / K + seq + t0 / K, left, a.channels), t.checkpoint(a.channels), 0u, r->s);
+    }
+    __device__ __forceinline__ void sums(const T& t, int64_t left, Raw* r, float (*s_a)[T::S], float (*s_b)[T::S])
+    {
+        keep_absent<DT, GATE>(t, left, r->g);
+#pragma unroll
+        for (int e = 0; e < CPL; ++e) {
+            float h = STAGE == PART_SUM ? 0.0f : __uint_as_float(r->s[e]), p = 1.0f, back = 0.0f;
+#pragma unroll
+            for (int j = 0; j < K; ++j) {
+                const GateSlope v = gate_slope<GATE, INPUT>(T::get(r->g[j], e));
+                if constexpr (STAGE != PART_SUM) {
+                    const float x = T::get(r->x[j], e);
+                    slope[j][e] = __builtin_fmaf(v.da, h, v.ds * x);
+                    h = __builtin_fmaf(v.a, h, v.s * x);
+                    vs[j][e] = v.s;
+                }
+                va[j][e] = v.a;
+                p *= v.a;
+            }
+#pragma unroll
+            for (int j = K - 1; j >= 0; --j) back = va[j][e] * (T::get(r->d[j], e) + back);
+            s_a[t.seg()][t.c + e] = p;
+            s_b[t.seg()][t.c + e] = back;
+        }
+#pragma unroll
+        for (int j = 0; j < K; ++j) dy[j] = r->d[j];
+    }
+    __device__ __forceinline__ void outputs(const GatedArgs& a, const T& t, const Span& sp, int64_t base, int64_t end, float (*s_h)[T::S])
+    {
+        const int64_t t0 = base + t.wave * T::WAVE_TOKENS;
+        float back[CPL];
+#pragma unroll
+        for (int e = 0; e < CPL; ++e) back[e] = s_h[t.seg()][t.c + e];
+        const Rsrc rdx = t.rows(a.dx, sp.begin + t0, a.dxs, end - t0, a.channels);
+        const Rsrc rdg = t.rows(a.dg, sp.begin + t0, a.dgs, end - t0, a.channels);
+#pragma unroll
+        for (int j = K - 1; j >= 0; --j) {
+            float dx[CPL], dg[CPL];
+#pragma unroll
+            for (int e = 0; e < CPL; ++e) {
+                const float dh = T::get(dy[j], e) + back[e];
+                dx[e] = vs[j][e] * dh;
+                dg[e] = slope[j][e] * dh;
+                back[e] = va[j][e] * dh;
+            }
+            t.store(rdx, a.dxs, j, T::put(dx));
+            t.store(rdg, a.dgs, j, T::put(dg));
+        }
+    }
+};
+
+// Backwards through the chunks.  PART_SUM: what a part makes of the gradient behind it.
+template <int DT, int GATE, int INPUT, int STAGE, int LC, int W>
+__global__ __launch_bounds__(W * 64, STAGE == PART_SUM ? 3 : 2) void k_gated_backward(GatedArgs a)
+{
+    using T = Tile<DT, LC, W>;
+    constexpr int S = T::S;
+    __shared__ float s_a[T::SEGS][S], s_b[T::SEGS][S], s_h[T::SEGS][S];
+    const GatedWork work = gated_work(a);
+    const int seq = work.seq;
+    if (gated_slot(a, seq) < 0) return;
+    const Span sp = gated_span(a, seq);
+    const int64_t begin = STAGE == WHOLE ? 0 : work.part * a.part_tokens;
+    if (work.part > 0 && begin >= sp.len) return;
+    if (STAGE == PART_SUM && work.part == 0) return;
+    const int64_t end = STAGE == WHOLE || begin + a.part_tokens >= sp.len ? sp.len : begin + a.part_tokens;
+    const T t(work.slice, a.channels);
+    const int mine = work.slice * S + threadIdx.x;
+    const bool carrier = threadIdx.x < S && mine < a.channels;
+    const int64_t edge = (int64_t)seq * a.channels + mine, pitch = (int64_t)a.nseq * a.parts * a.channels;
+    float* sums = a.sums + (int64_t)seq * a.parts * a.channels + mine;
+    float d = 0.0f, product = 1.0f; // gradient of the state behind the tokens that are left
+    if (STAGE != PART_SUM && carrier) {
+        if (a.dlast) d = a.dlast[edge];
+        if constexpr (STAGE == PART_OUT) {
+            const int n = (int)((sp.len + a.part_tokens - 1) / a.part_tokens);
+#pragma unroll 8
+            for (int p = n - 1; p > work.part; --p) d = __builtin_fmaf(sums[(int64_t)p * a.channels], d, sums[pitch + (int64_t)p * a.channels]);
+        }
+    }
+    const Carry<T::SEGS, S, true, STAGE == PART_SUM> carry{s_a, s_b, s_h};
+    Back<DT, GATE, INPUT, STAGE, LC, W> back;
+    typename Back<DT, GATE, INPUT, STAGE, LC, W>::Raw r;
+    int64_t base = end > begin ? begin + (end - begin - 1) / T::TOKENS * T::TOKENS : begin - T::TOKENS;
+    back.load(a, t, sp, seq, base, base >= begin ? end : base, &r);
+    for (; base >= begin; base -= T::TOKENS) {
+        back.sums(t, end - base - t.wave * T::WAVE_TOKENS, &r, s_a, s_b);
+        back.load(a, t, sp, seq, base - T::TOKENS, base > begin ? end : base - T::TOKENS, &r); // nothing, before the first
+        __syncthreads();
+        if (threadIdx.x < S) carry.along(d, product);
+        __syncthreads();
+        if constexpr (STAGE != PART_SUM) back.outputs(a, t, sp, base, end, s_h);
+    }
+    if constexpr (STAGE == PART_SUM) {
+        if (carrier) {
+            sums[(int64_t)work.part * a.channels] = product;
+            sums[pitch + (int64_t)work.part * a.channels] = d;
+        }
+    } else if (carrier && a.dfirst && work.part == 0) {
+        a.dfirst[edge] = d;
+    }
 }
 
 // One token: a thread takes 8 channels of a sequence.
 template <int DT, int GATE, int INPUT>
-__global__ __launch_bounds__(256) void k_gated_step(GatedArgs a)
+__global__ __launch_bounds__(256) void k_gated_step(GatedArgs a, uint32_t threads)
 {
-    const int per = a.channels / 8;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= (int64_t)a.nseq * per) return;
+    const uint32_t i = blockIdx.x * 256 + threadIdx.x, per = (uint32_t)a.channels / 8;
+    if (i >= threads) return;
     const int seq = (int)(i / per), c = (int)(i % per) * 8;
     const int slot = gated_slot(a, seq);
     if (slot < 0) return;
+    float g[8], x[8];
+    uint32_t h[8];
+    float* state = a.h + (int64_t)slot * a.channels + c;
+    load_words<8>(state, h);
+    load_elems<DT, 8>(elem_ptr<DT>(a.g, seq * a.gs + c), g);
+    load_elems<DT, 8>(elem_ptr<DT>(a.x, seq * a.xs + c), x);
+#pragma unroll
     for (int e = 0; e < 8; ++e) {
-        float* state = a.h + (int64_t)slot * a.channels + c + e;
-        const GateValue v = gate_value<GATE, INPUT>(load_elem<DT>(a.g, seq * a.gs + c + e));
-        const float h = __builtin_fmaf(v.a, *state, v.s * load_elem<DT>(a.x, seq * a.xs + c + e));
-        *state = h;
-        store_elem<DT>(a.o, seq * a.os + c + e, h);
+        const GateValue v = gate_value<GATE, INPUT>(g[e]);
+        h[e] = __float_as_uint(__builtin_fmaf(v.a, __uint_as_float(h[e]), v.s * x[e]));
+    }
+    store_words<8>(state, h);
+    if constexpr (DT == DT_FP32) {
+        store_words<8>(static_cast<float*>(a.o) + seq * a.os + c, h);
+    } else {
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = pack_elems<DT>(__uint_as_float(h[2 * e]), __uint_as_float(h[2 * e + 1]));
+        store_words<4>(static_cast<uint16_t*>(a.o) + seq * a.os + c, o);
     }
 }
 
@@ -103,24 +406,88 @@ static hipError_t with_gate(int dtype, int gate, int input, F f)
     return hipErrorInvalidValue;
 }
 
-size_t gated_workspace(int, int, int64_t, int) { return 0; }
-
-hipError_t launch_gated_scan(int dtype, int gate, int input, const GatedArgs& a, void*, int, hipStream_t st)
+// How a call is split.  A compute unit has some 512 cache lines under way, so that rows of 64 bytes come at half the
+// rate of whole lines, and a workgroup's tiles follow each other: many workgroups first, wide rows then.  bf16 on one card,
+// scan and gradient in us:
+//   256 workgroups of 256-byte rows     8 x 2048 tokens, 4096 channels   61 + 98 (128-byte rows 71 + 107)
+//   192 of 128-byte rows                5 x 611 tokens, 1544 channels (fp32)  13 + 18 (64-byte rows 13 + 20, 256-byte rows 16 + 23)
+//   128 of 64-byte rows                 8192 tokens, 8192 channels       100 (128-byte rows in parts 139, whole 125)
+//   fewer, and more than two tiles      8192 tokens, 2048 channels       41 + 58 in parts (64-byte rows whole 71 + 156)
+// Parts cost a second pass over what they read, and a launch.
+constexpr int kPartLanes = 32;
+struct GatedPlan {
+    int lc;             // lanes across the channels
+    int slices, parts;  // parts 1: whole sequences
+    int64_t part_tokens;
+};
+static GatedPlan gated_plan(bool back, int cpl, int channels, int nseq, int64_t tokens)
 {
-    const dim3 grid((unsigned)((int64_t)a.nseq * ((a.channels + 255) / 256))), wg(256);
+    const auto slices = [&](int lc) { return (channels + lc * cpl - 1) / (lc * cpl); };
+    const auto wgs = [&](int lc) { return (int64_t)nseq * slices(lc); };
+    const auto whole = [&](int lc) { return GatedPlan{lc, slices(lc), 1, 0}; };
+    if (nseq == 0) return whole(64);
+    if (wgs(64) >= 256) return whole(64);
+    if (wgs(32) >= 192) return whole(32);
+    const int64_t mean = (tokens + nseq - 1) / nseq, tile = (back ? 4 : 8) * 64 / kPartLanes * kGatedChunk;
+    if (wgs(16) >= 128 || mean <= 512) return whole(16);
+    const int64_t want = (512 + wgs(kPartLanes) - 1) / wgs(kPartLanes); // parts of a sequence of the mean length
+    GatedPlan p{kPartLanes, slices(kPartLanes), 1, ((mean + want - 1) / want + tile - 1) / tile * tile};
+    p.parts = (int)((tokens + p.part_tokens - 1) / p.part_tokens);
+    return p;
+}
+
+size_t gated_workspace(int channels, int nseq, int64_t tokens, int)
+{
+    size_t most = 0;
+    for (int i = 0; i < 4; ++i) {
+        const GatedPlan p = gated_plan(i & 1, 1 + i / 2, channels, nseq, tokens);
+        const size_t n = p.parts > 1 ? (size_t)nseq * p.parts * channels * 8 : 0;
+        if (n > most) most = n;
+    }
+    return most;
+}
+
+template <int DT, int GATE, int INPUT, bool BACK, int STAGE, int LC, int W>
+static hipError_t launch_gated(const GatedArgs& a, hipStream_t st)
+{
+    const dim3 grid((unsigned)((int64_t)a.nseq * a.slices * a.parts)), wg(W * 64);
+    if constexpr (BACK) hipLaunchKernelGGL((k_gated_backward<DT, GATE, INPUT, STAGE, LC, W>), grid, wg, 0, st, a);
+    else hipLaunchKernelGGL((k_gated_scan<DT, GATE, INPUT, STAGE, LC, W>), grid, wg, 0, st, a);
+    return hipGetLastError();
+}
+
+template <bool BACK>
+static hipError_t launch_gated(int dtype, int gate, int input, const GatedArgs& args, void* ws, hipStream_t st)
+{
     return with_gate(dtype, gate, input, [&](auto dt, auto ga, auto in) {
-        hipLaunchKernelGGL((k_gated_scan<decltype(dt)::value, decltype(ga)::value, decltype(in)::value>), grid, wg, 0, st, a);
-        return hipGetLastError();
+        constexpr int DT = decltype(dt)::value, GA = decltype(ga)::value, IN = decltype(in)::value;
+        const GatedPlan p = gated_plan(BACK, DT == DT_FP32 ? 1 : 2, args.channels, args.nseq, args.tokens);
+        GatedArgs a = args;
+        a.slices = p.slices;
+        a.parts = p.parts;
+        a.part_tokens = p.part_tokens;
+        a.sums = (float*)ws;
+        if (p.parts > 1) {
+            constexpr int W = BACK ? 4 : 8; // gradient of 32768 tokens, 256 channels: 29 us, 8 waves 36; scan 29 and 25
+            // what a part makes of a gradient is its decays' doing alone
+            const hipError_t e = launch_gated<DT, GA, BACK ? IN_PLAIN : IN, BACK, PART_SUM, kPartLanes, W>(a, st);
+            return e != hipSuccess ? e : launch_gated<DT, GA, IN, BACK, PART_OUT, kPartLanes, W>(a, st);
+        }
+        if (p.lc == 64) return launch_gated<DT, GA, IN, BACK, WHOLE, 64, 8>(a, st);
+        if (p.lc == 32) return launch_gated<DT, GA, IN, BACK, WHOLE, 32, 8>(a, st);
+        // gradient of 8 x 1024 tokens, 1024 channels: 20 us, 4 waves 24; scan of 8192 tokens, 8192 channels: 105 and 100
+        return launch_gated<DT, GA, IN, BACK, WHOLE, 16, BACK ? 8 : 4>(a, st);
     });
 }
 
-hipError_t launch_gated_backward(int dtype, int gate, int input, const GatedArgs& a, void*, int, hipStream_t st)
+hipError_t launch_gated_scan(int dtype, int gate, int input, const GatedArgs& a, void* ws, int, hipStream_t st)
 {
-    const dim3 grid((unsigned)((int64_t)a.nseq * ((a.channels + 255) / 256))), wg(256);
-    return with_gate(dtype, gate, input, [&](auto dt, auto ga, auto in) {
-        hipLaunchKernelGGL((k_gated_backward<decltype(dt)::value, decltype(ga)::value, decltype(in)::value>), grid, wg, 0, st, a);
-        return hipGetLastError();
-    });
+    return launch_gated<false>(dtype, gate, input, a, ws, st);
+}
+
+hipError_t launch_gated_backward(int dtype, int gate, int input, const GatedArgs& a, void* ws, int, hipStream_t st)
+{
+    return launch_gated<true>(dtype, gate, input, a, ws, st);
 }
 
 hipError_t launch_gated_step(int dtype, int gate, int input, const GatedArgs& a, hipStream_t st)
@@ -128,7 +495,7 @@ hipError_t launch_gated_step(int dtype, int gate, int input, const GatedArgs& a,
     const int64_t n = (int64_t)a.nseq * (a.channels / 8);
     const dim3 grid((unsigned)((n + 255) / 256)), wg(256);
     return with_gate(dtype, gate, input, [&](auto dt, auto ga, auto in) {
-        hipLaunchKernelGGL((k_gated_step<decltype(dt)::value, decltype(ga)::value, decltype(in)::value>), grid, wg, 0, st, a);
+        hipLaunchKernelGGL((k_gated_step<decltype(dt)::value, decltype(ga)::value, decltype(in)::value>), grid, wg, 0, st, a, (uint32_t)n);
         return hipGetLastError();
     });
 }

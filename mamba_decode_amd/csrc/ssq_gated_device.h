@@ -10,19 +10,21 @@ constexpr float kLog2e = 1.44269504088896341f;
 
 __device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
-// 1 - e^y for y <= 0 without the difference of near numbers: for y > -1/2 the series of
-// (1 - e^y) / -y to the term y^7/8!, which leaves 2^-8/9! = 1.1e-8 of it at most.
-__device__ __forceinline__ float one_minus_exp(float y, float e)
+// 1 - e^(Y g) for g <= 0 and Y = 1 or 2 without the difference of near numbers, e = e^(Y g): for
+// y = Y g > -1/2 the polynomial of degree 4 nearest to (1 - e^y) / -y in relative error, fitted to it, which is
+// off by 1.8 * 2^-24; below, the difference is 0.39 of its larger side at least.
+template <int Y>
+__device__ __forceinline__ float one_minus_exp(float g, float e)
 {
-    float p = 1.0f / 40320.0f;
-    p = __builtin_fmaf(p, y, 1.0f / 5040.0f);
-    p = __builtin_fmaf(p, y, 1.0f / 720.0f);
-    p = __builtin_fmaf(p, y, 1.0f / 120.0f);
-    p = __builtin_fmaf(p, y, 1.0f / 24.0f);
-    p = __builtin_fmaf(p, y, 1.0f / 6.0f);
-    p = __builtin_fmaf(p, y, 0.5f);
-    p = __builtin_fmaf(p, y, 1.0f);
-    return y > -0.5f ? -y * p : 1.0f - e;
+    constexpr float y = Y;
+    float p = -0.00677103545f * y * y * y * y * y;
+    p = __builtin_fmaf(p, g, -0.0410012762f * y * y * y * y);
+    p = __builtin_fmaf(p, g, -0.166548151f * y * y * y);
+    p = __builtin_fmaf(p, g, -0.499992498f * y * y);
+    p = __builtin_fmaf(p, g, -0.999999923f * y);
+    float near = g * p;
+    asm volatile("" : "+v"(near)); // both sides and a select: a branch around the polynomial would be taken token by token
+    return g > -0.5f / y ? near : 1.0f - e;
 }
 
 struct GateValue {
@@ -33,43 +35,69 @@ struct GateSlope {
     float a, s, da, ds; // and their derivatives along the gate
 };
 
+// The sigmoid and one minus it, from e = exp(-g): neither is a difference.  Where e overflows, e * a is
+// not a number and the minimum is 1.
+__device__ __forceinline__ void sigmoid_pair(float g, float* a, float* rest)
+{
+    const float e = exp_fast(-g);
+    *a = __builtin_amdgcn_rcpf(1.0f + e);
+    *rest = fminf(e * *a, 1.0f);
+}
+
 template <int GATE, int INPUT>
 __device__ __forceinline__ GateSlope gate_slope(float g)
 {
     GateSlope r;
-    float rest; // 1 - a
     if constexpr (GATE == GATE_LOG) {
         r.a = exp_fast(g);
         r.da = r.a;
-        rest = INPUT == IN_COMPLEMENT ? one_minus_exp(g, r.a) : 0.0f;
+        if constexpr (INPUT == IN_COMPLEMENT) {
+            r.s = one_minus_exp<1>(g, r.a);
+            r.ds = -r.a;
+        }
+        if constexpr (INPUT == IN_NORM) {
+            const float sq = r.a * r.a;
+            r.s = __builtin_amdgcn_sqrtf(one_minus_exp<2>(g, sq));
+            r.ds = r.s > 0.0f ? -sq * __builtin_amdgcn_rcpf(r.s) : 0.0f;
+        }
     } else {
-        // e <= 1: neither side of the sigmoid is a difference
-        const float e = exp_fast(-fabsf(g));
-        const float big = __builtin_amdgcn_rcpf(1.0f + e), small = e * big;
-        r.a = g >= 0.0f ? big : small;
-        rest = g >= 0.0f ? small : big;
-        r.da = big * small;
+        float rest;
+        sigmoid_pair(g, &r.a, &rest);
+        r.da = r.a * rest;
+        if constexpr (INPUT == IN_COMPLEMENT) {
+            r.s = rest;
+            r.ds = -r.da;
+        }
+        if constexpr (INPUT == IN_NORM) { // ds = -a^2 (1 - a) / s = -a^2 s / (1 + a)
+            const float up = 1.0f + r.a;
+            r.s = __builtin_amdgcn_sqrtf(rest * up);
+            r.ds = -r.a * r.a * r.s * __builtin_amdgcn_rcpf(up);
+        }
     }
     if constexpr (INPUT == IN_PLAIN) {
         r.s = 1.0f;
         r.ds = 0.0f;
-    } else if constexpr (INPUT == IN_COMPLEMENT) {
-        r.s = rest;
-        r.ds = -r.da;
-    } else {
-        const float sq = GATE == GATE_LOG ? one_minus_exp(2.0f * g, r.a * r.a) : rest * (1.0f + r.a);
-        r.s = __builtin_amdgcn_sqrtf(fmaxf(sq, 0.0f));
-        r.ds = r.s > 0.0f ? -r.a * r.da * __builtin_amdgcn_rcpf(r.s) : 0.0f;
     }
     return r;
 }
 
+// what is not used of the slopes is not computed
 template <int GATE, int INPUT>
 __device__ __forceinline__ GateValue gate_value(float g)
 {
     const GateSlope r = gate_slope<GATE, INPUT>(g);
     return {r.a, r.s};
 }
+
+// A descriptor of the wave's: without the readfirstlanes the compiler would loop over its lanes' values.  Loads
+// through it need no branch for rows that are not there, and where loads ahead stand in no branch the compiler
+// counts them instead of waiting for all of them.
+__device__ __forceinline__ Rsrc uniform_rsrc(uint64_t base, uint32_t bytes)
+{
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)base), hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(base >> 32));
+    return make_rsrc((const void*)(((uint64_t)hi << 32) | lo), (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes));
+}
+constexpr uint32_t kNowhere = 0x80000000u; // an offset beyond every descriptor's bytes
 
 // a sequence's tokens, within 0 .. tokens whatever cu says
 struct Span {

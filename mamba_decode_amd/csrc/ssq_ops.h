@@ -78,6 +78,9 @@ struct GatedArgs {
     const uint8_t* fresh;
     int64_t tokens;
     int nseq, batch, channels; // batch: of the slots (0: there are none)
+    int slices, parts;   // workgroups along the channels, and along a sequence's tokens at most
+    int64_t part_tokens;
+    float* sums;         // [2][nseq][parts][channels] of a call in parts
 };
 enum Gate : int { GATE_LOG = 0, GATE_SIGMOID = 1 };
 enum Input : int { IN_PLAIN = 0, IN_COMPLEMENT = 1, IN_NORM = 2 };

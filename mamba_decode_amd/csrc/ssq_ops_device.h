@@ -59,6 +59,15 @@ __device__ __forceinline__ void store_elem(void* p, int64_t i, float v)
     static_cast<typename Elem<DT>::T*>(p)[i] = (typename Elem<DT>::T)v;
 }
 
+// two of them, in one conversion where the type has one
+template <int DT>
+__device__ __forceinline__ uint32_t pack_elems(float lo, float hi)
+{
+    typedef typename Elem<DT>::T T2 __attribute__((ext_vector_type(2)));
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){lo, hi}, T2));
+}
+
 template <int DT>
 __device__ __forceinline__ const void* elem_ptr(const void* p, int64_t i)
 {
