@@ -598,7 +598,7 @@ def ssq_state_reorder(states, parents, stream=None):
 
 
 def _handles(states):
-    return (ctypes.c_void_p * max(1, len(states)))(*[s.handle.value if s.handle is not None else None for s in states])
+    return (ctypes.c_void_p * max(1, len(states)))(*[s.handle for s in states])
 
 
 def ssq_state_move(states, to, from_, sources=None, stream=None):
