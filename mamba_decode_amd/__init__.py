@@ -403,6 +403,14 @@ _DTYPES = {torch.float32: SSQ_DTYPE_FP32, torch.bfloat16: SSQ_DTYPE_BF16, torch.
 # The calls below are short enough on the device that their checks count: one function sees to a
 # tensor's dtype, device, shape and layout and says what is wrong only if something is.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+def _current_device() -> int:
+    if _get_device is not None and torch.cuda.is_initialized():
+        return _get_device()
+    return torch.cuda.current_device()
+
 
 
 def _stream_ptr(stream, dev: int) -> int:
@@ -606,7 +614,7 @@ def ssq_state_move(states, to, from_, sources=None, stream=None):
     of its source is then, or the zero state where ``from_[i]`` is -1.  ``states``: a State or a sequence of them (the
     layers of a model); ``sources``: the same number of States of another pool, None for the states themselves; to,
     from_: int32 ``[nmoves]`` on the device."""
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     states = [states] if isinstance(states, State) else states
     sources = [sources] if isinstance(sources, State) else sources
     if sources is not None and len(sources) != len(states):
@@ -618,20 +626,21 @@ def ssq_state_move(states, to, from_, sources=None, stream=None):
                               _int32(n, "nmoves"), _stream_ptr(stream, dev)), "ssq_state_move")
 
 
-def _rows(t, name: str, dtype, tokens: int, channels: int, dev: int):
-    """Pointer and stride between tokens of a [tokens][channels] or [tokens][groups][width] tensor whose tokens are packed."""
-    shape = (tokens, channels)
-    if isinstance(t, torch.Tensor) and t.dim() == 3:
-        shape = (tokens, t.shape[1], channels // max(1, t.shape[1]))
-    p, stride = _tokens(t, name, dtype, shape, dev)
-    return p, (channels if tokens == 0 else stride)  # no row is read: any stride serves
+def _rows(t, name: str, dtype, shape, dev: int):
+    """Pointer and stride between tokens of a [tokens][channels] tensor whose tokens are packed."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        _refuse(t, name, dtype, shape, dev)
+    between, within = t.stride()
+    if within != 1 and shape[1] != 1:
+        raise ValueError(f"the channels of {name} must be packed within a token")
+    return t.data_ptr(), between if shape[0] > 1 else shape[1]
 
 
 def _token_rows(t, name: str):
-    """dtype, tokens and channels of a [tokens][channels] tensor."""
+    """dtype and shape of a [tokens][channels] tensor."""
     if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES or t.dim() != 2:
         raise ValueError(f"{name} must be a float32, bfloat16 or float16 tensor [tokens, channels]")
-    return t.dtype, t.shape[0], t.shape[1]
+    return t.dtype, t.shape
 
 
 def ssq_gated_checkpoint_rows(nseq: int, tokens: int) -> int:
@@ -663,12 +672,12 @@ def _sequences(cu_seqlens, slots, dev: int):
 
 
 def _gated_io(x, g, o, gate: int, input: int, dev: int):
-    dtype, tokens, channels = _token_rows(x, "x")
-    xp, xs = _rows(x, "x", dtype, tokens, channels, dev)
-    gp, gs = _rows(g, "g", dtype, tokens, channels, dev)
-    op, os_ = _rows(o, "o", dtype, tokens, channels, dev)
-    return tokens, ssq_gated_io(_DTYPES[dtype], _int32(gate, "gate"), _int32(input, "input"), _int32(channels, "channels"),
-                                xp, gp, op, xs, gs, os_)
+    dtype, shape = _token_rows(x, "x")
+    xp, xs = _rows(x, "x", dtype, shape, dev)
+    gp, gs = _rows(g, "g", dtype, shape, dev)
+    op, os_ = _rows(o, "o", dtype, shape, dev)
+    return shape[0], ssq_gated_io(_DTYPES[dtype], _int32(gate, "gate"), _int32(input, "input"), _int32(shape[1], "channels"),
+                                  xp, gp, op, xs, gs, os_)
 
 
 def ssq_gated_scan(state: State | None, x, g, o, cu_seqlens, gate: int = SSQ_GATE_LOG, input: int = SSQ_INPUT_PLAIN,
@@ -680,7 +689,7 @@ def ssq_gated_scan(state: State | None, x, g, o, cu_seqlens, gate: int = SSQ_GAT
     bool ``[nseq]`` or None; all on the device.  ``state``: an SSQ_GATED state, or None to start from zero.
     ``checkpoints``: float32 ``[ssq_gated_checkpoint_rows(nseq, tokens), channels]`` for the gradient, or None.
     ``workspace``: uint8, at least ``ssq_gated_workspace`` bytes, or None to take it from torch."""
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     tokens, io = _gated_io(x, g, o, gate, input, dev)
     nseq, cu, sp = _sequences(cu_seqlens, slots, dev)
     fp = _flags(fresh, "fresh", (nseq,), dev)
@@ -699,9 +708,10 @@ def ssq_gated_scan_backward(checkpoints, x, g, do, dx, dg, cu_seqlens, gate: int
     """Gradients of ``ssq_gated_scan`` (the same x, g, cu_seqlens, gate, input, state and slots, and the checkpoints that
     it wrote): dx and dg from do, the gradient of o (all shaped and strided as x).  dlast: float32 ``[nseq, channels]``,
     the gradient of the last states, or None; dfirst: the same of the states the sequences started from is written."""
-    dev = torch.cuda.current_device()
-    dtype, tokens, channels = _token_rows(x, "x")
-    ptrs, strides = zip(*[_rows(t, name, dtype, tokens, channels, dev)
+    dev = _current_device()
+    dtype, shape = _token_rows(x, "x")
+    tokens, channels = shape
+    ptrs, strides = zip(*[_rows(t, name, dtype, shape, dev)
                           for t, name in ((x, "x"), (g, "g"), (do, "do"), (dx, "dx"), (dg, "dg"))])
     nseq, cu, sp = _sequences(cu_seqlens, slots, dev)
     ends = [None if t is None else _ptr(t, name, torch.float32, (nseq, channels), dev)
@@ -718,7 +728,7 @@ def ssq_gated_scan_backward(checkpoints, x, g, do, dx, dg, cu_seqlens, gate: int
 def ssq_gated_step(state: State, x, g, o, gate: int = SSQ_GATE_LOG, input: int = SSQ_INPUT_PLAIN, slots=None, stream=None):
     """One token of the gated recurrence for ``nseq = x.shape[0]`` sequences: row i of the tensors (as in
     ``ssq_gated_scan``) is sequence ``slots[i]`` of the state, or sequence i without slots."""
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     nseq, io = _gated_io(x, g, o, gate, input, dev)
     sp = None if slots is None else _ptr(slots, "slots", torch.int32, (nseq,), dev)
     _check(lib.ssq_gated_step(state.handle, io, _int32(nseq, "nseq"), sp, _stream_ptr(stream, dev)), "ssq_gated_step")
@@ -737,12 +747,14 @@ def ssq_group_norm_workspace(groups: int, width: int, tokens: int) -> int:
 def _norm_io(x, z, weight, bias, act: int, center: bool, eps: float, dev: int):
     if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPES or x.dim() != 3:
         raise ValueError("x must be a float32, bfloat16 or float16 tensor [tokens, groups, width]")
-    xp, xs = _tokens(x, "x", x.dtype, x.shape, dev)
-    zp, zs = (None, 0) if z is None else _tokens(z, "z", x.dtype, x.shape, dev)
-    tokens, groups, width = x.shape
+    shape = x.shape
+    xp, xs = _tokens(x, "x", x.dtype, shape, dev)
+    zp, zs = (None, 0) if z is None else _tokens(z, "z", x.dtype, shape, dev)
+    tokens, groups, width = shape
     if tokens == 0:  # no row is read: any stride serves
         xs = zs = groups * width
-    wp, bp = (None if t is None else _ptr(t, name, torch.float32, x.shape[1:], dev) for t, name in ((weight, "weight"), (bias, "bias")))
+    wp = None if weight is None else _ptr(weight, "weight", torch.float32, shape[1:], dev)
+    bp = None if bias is None else _ptr(bias, "bias", torch.float32, shape[1:], dev)
     return ssq_norm_io(_DTYPES[x.dtype], _int32(act, "act"), 1 if center else 0, _int32(groups, "groups"), _int32(width, "width"),
                        eps, wp, bp, xp, zp, xs, zs)
 
@@ -754,7 +766,7 @@ def ssq_group_norm(x, y, weight=None, bias=None, z=None, act: int = SSQ_ACT_SILU
     x, z, y ``[tokens, groups, width]`` (float32, bfloat16 or float16; any stride between tokens that is a multiple of 16
     bytes and not below a token's row), z None for SSQ_ACT_SILU; weight, bias ``[groups, width]`` float32 or None.
     ``center``: mean and variance, else the root mean square alone."""
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     io = _norm_io(x, z, weight, bias, act, center, eps, dev)
     tokens, row = x.shape[0], io.groups * io.width
     yp, ys = _tokens(y, "y", x.dtype, x.shape, dev)
@@ -766,7 +778,7 @@ def ssq_group_norm_backward(dy, x, dx, weight=None, bias=None, z=None, dz=None, 
                             workspace: torch.Tensor | None = None, stream=None):
     """Gradients of ``ssq_group_norm`` (the same x, z, weight, bias, act, center and eps): dx and dz from dy (all shaped
     and strided as x), and dweight and dbias, float32 ``[groups, width]``, where they are given."""
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     io = _norm_io(x, z, weight, bias, act, center, eps, dev)
     tokens, groups, width = x.shape
     row = groups * width

@@ -862,22 +862,12 @@ int64_t ssq_gated_checkpoint_rows(int32_t nseq, int64_t tokens)
     return tokens / SSQ_GATED_CHUNK + nseq;
 }
 
-static int current_cus()
-{
-    int dev = -1;
-    if (hipGetDevice(&dev) != hipSuccess) {
-        (void)hipGetLastError();
-        dev = -1;
-    }
-    return num_cus(dev);
-}
-
 size_t ssq_gated_workspace(int32_t channels, int32_t nseq, int64_t tokens)
 {
     if (check_gated(nullptr, SSQ_DTYPE_FP32, SSQ_GATE_LOG, SSQ_INPUT_PLAIN, channels, nseq, tokens, nullptr,
                     ssq::kMaxGatedRows) != SSQ_OK)
         return (size_t)-1;
-    return ssq::gated_workspace(channels, nseq, tokens, current_cus());
+    return ssq::gated_workspace(channels, nseq, tokens);
 }
 
 ssq_status ssq_gated_scan(ssq_state* st, const ssq_gated_io* io, int32_t nseq, int64_t tokens, const int32_t* cu_seqlens,
@@ -895,7 +885,7 @@ ssq_status ssq_gated_scan(ssq_state* st, const ssq_gated_io* io, int32_t nseq, i
     a.cu = cu_seqlens;
     a.fresh = fresh;
     a.ckpt = checkpoints;
-    return from_hip(ssq::launch_gated_scan(io->dtype, io->gate, io->input, a, workspace, current_cus(), (hipStream_t)stream),
+    return from_hip(ssq::launch_gated_scan(io->dtype, io->gate, io->input, a, workspace, (hipStream_t)stream),
                     "gated scan launch");
 }
 
@@ -937,7 +927,7 @@ ssq_status ssq_gated_scan_backward(const ssq_state* st, const ssq_gated_grad* io
     a.nseq = nseq;
     a.batch = st ? st->desc.batch : 0;
     a.channels = io->channels;
-    return from_hip(ssq::launch_gated_backward(io->dtype, io->gate, io->input, a, workspace, current_cus(), (hipStream_t)stream),
+    return from_hip(ssq::launch_gated_backward(io->dtype, io->gate, io->input, a, workspace, (hipStream_t)stream),
                     "gated scan gradient launch");
 }
 

@@ -6,6 +6,8 @@
 
 namespace ssq {
 
+constexpr int kGroupSlices = 16; // fewer are not dealt to the XCDs in groups
+
 // The tile of a workgroup: a slice of channels, LC lanes of CPL channels (4 bytes of x), and W
 // waves x 64/LC groups of lanes along the tokens, each with a chunk of 16 tokens in registers.
 template <int DT, int LC_, int W_>
@@ -64,11 +66,11 @@ struct Tile {
     }
 };
 
-// workgroup i's place where each XCD takes a contiguous range of `n`
-__device__ __forceinline__ int64_t xcd_grouped(int64_t i, int64_t n)
+// Slice of workgroup i of a sequence (workgroups go to the 8 XCDs in turn): each XCD takes neighbouring slices, whose rows
+// share cache lines where they are half a line or not aligned to lines, and all XCDs take part in each sequence.
+__device__ __forceinline__ int slice_of(int i, int slices)
 {
-    const int64_t q = n / 8, r = n % 8, xcd = i % 8;
-    return xcd * q + (xcd < r ? xcd : r) + i / 8;
+    return slices < kGroupSlices ? i : i % 8 * (slices / 8) + i / 8;
 }
 
 // WHOLE: a workgroup takes a sequence from its start to its end.  PART_SUM, PART_OUT: it takes a part of one, first
@@ -76,14 +78,31 @@ __device__ __forceinline__ int64_t xcd_grouped(int64_t i, int64_t n)
 // state that the parts before leave.
 enum Stage { WHOLE, PART_SUM, PART_OUT };
 
-// what a workgroup works on
+// the r-th longest of 64 sequences or fewer, of equal ones the first first
+__device__ __forceinline__ int longest(const GatedArgs& a, int r)
+{
+    const int lane = threadIdx.x & 63;
+    const int len = lane < a.nseq ? (int)gated_span(a, lane).len : -1;
+    int rank = 0;
+    for (int i = 0; i < a.nseq; ++i) {
+        const int other = __builtin_amdgcn_readlane(len, i);
+        rank += other > len || (other == len && i < lane);
+    }
+    return __builtin_ctzll(__ballot(lane < a.nseq && rank == r));
+}
+
+// What a workgroup works on.  More whole sequences than run at once are taken from the longest on, so that what is left for
+// the end is short (24 sequences of 350 to 1050 tokens, 2048 channels: 49 us, 58 in the call's order).
 struct GatedWork {
     int seq, part, slice;
 };
+template <int STAGE, int LC>
 __device__ __forceinline__ GatedWork gated_work(const GatedArgs& a)
 {
-    const int64_t i = xcd_grouped(blockIdx.x, gridDim.x), j = i / a.slices;
-    return {(int)(j / a.parts), (int)(j % a.parts), (int)(i % a.slices)};
+    const int j = (int)(blockIdx.x / a.slices), i = (int)(blockIdx.x % a.slices);
+    GatedWork w{j / a.parts, j % a.parts, slice_of(i, a.slices)};
+    if (STAGE == WHOLE && a.nseq > 1 && a.nseq <= 64 && gridDim.x > 256) w.seq = longest(a, w.seq);
+    return w;
 }
 
 // Gates of tokens that are not there keep the state: a log gate reads 0, a sigmoid's gets infinity.
@@ -177,7 +196,7 @@ __global__ __launch_bounds__(W * 64, 3) void k_gated_scan(GatedArgs a)
     using T = Tile<DT, LC, W>;
     constexpr int K = T::K, S = T::S;
     __shared__ float s_a[T::SEGS][S], s_b[T::SEGS][S], s_h[T::SEGS][S];
-    const GatedWork work = gated_work(a);
+    const GatedWork work = gated_work<STAGE, LC>(a);
     const int seq = work.seq, slot = gated_slot(a, seq);
     if (slot < 0) return;
     const Span sp = gated_span(a, seq);
@@ -186,6 +205,7 @@ __global__ __launch_bounds__(W * 64, 3) void k_gated_scan(GatedArgs a)
     if (work.part > 0 && begin >= sp.len) return;
     if (STAGE == PART_SUM && last) return;
     const int64_t end = last ? sp.len : begin + a.part_tokens;
+    if (work.slice * S >= a.channels) return;
     const T t(work.slice, a.channels);
     const int mine = work.slice * S + threadIdx.x; // the channel that this thread carries along the chunks
     const bool carrier = threadIdx.x < S && mine < a.channels;
@@ -307,7 +327,7 @@ __global__ __launch_bounds__(W * 64, STAGE == PART_SUM ? 3 : 2) void k_gated_bac
     using T = Tile<DT, LC, W>;
     constexpr int S = T::S;
     __shared__ float s_a[T::SEGS][S], s_b[T::SEGS][S], s_h[T::SEGS][S];
-    const GatedWork work = gated_work(a);
+    const GatedWork work = gated_work<STAGE, LC>(a);
     const int seq = work.seq;
     if (gated_slot(a, seq) < 0) return;
     const Span sp = gated_span(a, seq);
@@ -315,6 +335,7 @@ __global__ __launch_bounds__(W * 64, STAGE == PART_SUM ? 3 : 2) void k_gated_bac
     if (work.part > 0 && begin >= sp.len) return;
     if (STAGE == PART_SUM && work.part == 0) return;
     const int64_t end = STAGE == WHOLE || begin + a.part_tokens >= sp.len ? sp.len : begin + a.part_tokens;
+    if (work.slice * S >= a.channels) return;
     const T t(work.slice, a.channels);
     const int mine = work.slice * S + threadIdx.x;
     const bool carrier = threadIdx.x < S && mine < a.channels;
@@ -406,14 +427,14 @@ static hipError_t with_gate(int dtype, int gate, int input, F f)
     return hipErrorInvalidValue;
 }
 
-// How a call is split.  A compute unit has some 512 cache lines under way, so that rows of 64 bytes come at half the
-// rate of whole lines, and a workgroup's tiles follow each other: many workgroups first, wide rows then.  bf16 on one card,
-// scan and gradient in us:
-//   256 workgroups of 256-byte rows     8 x 2048 tokens, 4096 channels   61 + 98 (128-byte rows 71 + 107)
-//   192 of 128-byte rows                5 x 611 tokens, 1544 channels (fp32)  13 + 18 (64-byte rows 13 + 20, 256-byte rows 16 + 23)
-//   128 of 64-byte rows                 8192 tokens, 8192 channels       100 (128-byte rows in parts 139, whole 125)
-//   fewer, and more than two tiles      8192 tokens, 2048 channels       41 + 58 in parts (64-byte rows whole 71 + 156)
-// Parts cost a second pass over what they read, and a launch.
+// How a call is split.  A compute unit has some 512 cache lines under way whatever its waves do, so that rows of 64 bytes,
+// half a line each, come at half the rate of whole lines; and a workgroup's tiles follow each other.  So: enough workgroups to
+// fill the card, and then rows as wide as they can be.  bf16, scan + gradient in us:
+//   300 workgroups of 256-byte rows   24 sequences of 350 to 1050 tokens, 2048 channels   49 (128-byte rows 57)
+//   192 of 128-byte rows              8 of 2048 tokens on average, 4096 channels    57 + 83 (256-byte rows 60 + 95)
+//   128 of 64-byte rows               8192 tokens, 8192 channels                    98 (128-byte rows 120)
+//   parts, for 64-byte rows fewer     8192 tokens, 2048 channels                    39 + 53 (whole 71 + 156)
+// Parts cost a second pass over what they read, and a launch: not for sequences of 512 tokens or fewer.
 constexpr int kPartLanes = 32;
 struct GatedPlan {
     int lc;             // lanes across the channels
@@ -426,7 +447,7 @@ static GatedPlan gated_plan(bool back, int cpl, int channels, int nseq, int64_t 
     const auto wgs = [&](int lc) { return (int64_t)nseq * slices(lc); };
     const auto whole = [&](int lc) { return GatedPlan{lc, slices(lc), 1, 0}; };
     if (nseq == 0) return whole(64);
-    if (wgs(64) >= 256) return whole(64);
+    if (wgs(64) >= 300) return whole(64);
     if (wgs(32) >= 192) return whole(32);
     const int64_t mean = (tokens + nseq - 1) / nseq, tile = (back ? 4 : 8) * 64 / kPartLanes * kGatedChunk;
     if (wgs(16) >= 128 || mean <= 512) return whole(16);
@@ -436,7 +457,7 @@ static GatedPlan gated_plan(bool back, int cpl, int channels, int nseq, int64_t 
     return p;
 }
 
-size_t gated_workspace(int channels, int nseq, int64_t tokens, int)
+size_t gated_workspace(int channels, int nseq, int64_t tokens)
 {
     size_t most = 0;
     for (int i = 0; i < 4; ++i) {
@@ -463,7 +484,7 @@ static hipError_t launch_gated(int dtype, int gate, int input, const GatedArgs& 
         constexpr int DT = decltype(dt)::value, GA = decltype(ga)::value, IN = decltype(in)::value;
         const GatedPlan p = gated_plan(BACK, DT == DT_FP32 ? 1 : 2, args.channels, args.nseq, args.tokens);
         GatedArgs a = args;
-        a.slices = p.slices;
+        a.slices = p.slices < kGroupSlices ? p.slices : (p.slices + 7) / 8 * 8; // those beyond the channels end at once
         a.parts = p.parts;
         a.part_tokens = p.part_tokens;
         a.sums = (float*)ws;
@@ -480,12 +501,12 @@ static hipError_t launch_gated(int dtype, int gate, int input, const GatedArgs& 
     });
 }
 
-hipError_t launch_gated_scan(int dtype, int gate, int input, const GatedArgs& a, void* ws, int, hipStream_t st)
+hipError_t launch_gated_scan(int dtype, int gate, int input, const GatedArgs& a, void* ws, hipStream_t st)
 {
     return launch_gated<false>(dtype, gate, input, a, ws, st);
 }
 
-hipError_t launch_gated_backward(int dtype, int gate, int input, const GatedArgs& a, void* ws, int, hipStream_t st)
+hipError_t launch_gated_backward(int dtype, int gate, int input, const GatedArgs& a, void* ws, hipStream_t st)
 {
     return launch_gated<true>(dtype, gate, input, a, ws, st);
 }

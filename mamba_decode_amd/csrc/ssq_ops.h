@@ -119,9 +119,9 @@ struct MovePart {
 };
 constexpr int kMaxMoves = 65535;
 
-size_t gated_workspace(int channels, int nseq, int64_t tokens, int num_cus);
-hipError_t launch_gated_scan(int dtype, int gate, int input, const GatedArgs& a, void* ws, int num_cus, hipStream_t st);
-hipError_t launch_gated_backward(int dtype, int gate, int input, const GatedArgs& a, void* ws, int num_cus, hipStream_t st);
+size_t gated_workspace(int channels, int nseq, int64_t tokens);
+hipError_t launch_gated_scan(int dtype, int gate, int input, const GatedArgs& a, void* ws, hipStream_t st);
+hipError_t launch_gated_backward(int dtype, int gate, int input, const GatedArgs& a, void* ws, hipStream_t st);
 hipError_t launch_gated_step(int dtype, int gate, int input, const GatedArgs& a, hipStream_t st);
 size_t norm_workspace(int groups, int width, int64_t tokens);
 hipError_t launch_group_norm(int dtype, int act, const NormArgs& a, hipStream_t st);
