@@ -540,8 +540,8 @@ size_t ssq_gated_workspace(int32_t channels, int32_t nseq, int64_t tokens);
  * before every SSQ_GATED_CHUNK'th token of each sequence, chunk j of sequence
  * i in row cu_seqlens[i]/SSQ_GATED_CHUNK + i + j (rows of no chunk are left).
  * Results do not depend on other sequences of the call, but may differ in
- * rounding with the call's sizes.  nseq*channels is 2^26 at most, tokens below
- * 2^31 - 128.  workspace: as for ssq_linattn_prefill. */
+ * rounding with the call's sizes.  nseq is 2^22 at most, nseq*channels 2^26,
+ * tokens below 2^31 - 128.  workspace: as for ssq_linattn_prefill. */
 ssq_status ssq_gated_scan(ssq_state *state, const ssq_gated_io *io, int32_t nseq, int64_t tokens,
                           const int32_t *cu_seqlens, const int32_t *slots, const uint8_t *fresh, float *checkpoints,
                           void *workspace, size_t workspace_bytes, void *stream);
@@ -581,7 +581,7 @@ ssq_status ssq_gated_scan_backward(const ssq_state *state, const ssq_gated_grad 
                                    void *workspace, size_t workspace_bytes, void *stream);
 
 /* One token for each of nseq sequences (row i of the tensors is sequence i,
- * slots as in ssq_linattn_step).  nseq*channels is 2^31 at most. */
+ * slots as in ssq_linattn_step).  nseq is 2^22 at most, nseq*channels 2^31. */
 ssq_status ssq_gated_step(ssq_state *state, const ssq_gated_io *io, int32_t nseq, const int32_t *slots, void *stream);
 
 /* ------------------------------------------------------------------------

@@ -816,7 +816,8 @@ static ssq_status check_gated(const ssq_state* st, int dtype, int gate, int inpu
     SSQ_REQUIRE(!st || st->desc.row_len == channels, SSQ_ERR_INVALID_ARG, "the state has another number of channels");
     SSQ_REQUIRE(nseq >= 0 && tokens >= 0, SSQ_ERR_INVALID_ARG, "nseq and tokens must not be negative");
     SSQ_REQUIRE(tokens <= kMostTokens, SSQ_ERR_UNSUPPORTED, "a call takes fewer than 2^31-128 tokens");
-    SSQ_REQUIRE(nseq <= most / channels, SSQ_ERR_UNSUPPORTED, "the call covers too many sequences and channels");
+    SSQ_REQUIRE(nseq <= most / channels && nseq <= ssq::kMaxGatedSeqs, SSQ_ERR_UNSUPPORTED,
+                "the call covers too many sequences and channels");
     SSQ_REQUIRE(st || !slots, SSQ_ERR_INVALID_ARG, "slots without a state");
     SSQ_REQUIRE(!st || slots || nseq <= st->desc.batch, SSQ_ERR_INVALID_ARG, "without slots nseq must not exceed the batch");
     SSQ_REQUIRE(aligned(slots, 4), SSQ_ERR_INVALID_ARG, "slots must be 4-byte aligned");

@@ -29,7 +29,8 @@ struct Tile {
         bad = ch < channels ? 0u : kNowhere;
     }
     __device__ __forceinline__ int seg() const { return wave * TL + tl; }
-    // the wave's rows from token t0 of a tensor on, `left` of them at most
+    // The wave's rows from token t0 of a tensor on, `left` of them at most.  A row's offset is the scalar one of its load or store,
+    // which the range check of these descriptors counts in.
     __device__ __forceinline__ Rsrc rows(const void* p, int64_t t0, int64_t stride, int64_t left, int channels) const
     {
         const int64_t n = left < WAVE_TOKENS ? left : WAVE_TOKENS;

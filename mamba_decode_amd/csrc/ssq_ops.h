@@ -86,6 +86,7 @@ enum Gate : int { GATE_LOG = 0, GATE_SIGMOID = 1 };
 enum Input : int { IN_PLAIN = 0, IN_COMPLEMENT = 1, IN_NORM = 2 };
 constexpr int kGatedChunk = 16; // tokens from one checkpoint to the next
 constexpr int64_t kMaxGatedRows = (int64_t)1 << 26; // nseq * channels of a scan
+constexpr int kMaxGatedSeqs = 1 << 22;              // a workgroup of 512 for each at least
 constexpr int64_t kMaxGatedStep = (int64_t)1 << 31;
 constexpr int kMaxChannels = 1 << 20;
 
