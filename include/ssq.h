@@ -467,7 +467,7 @@ ssq_status ssq_state_reorder(ssq_state *const *states, int32_t nstates, const in
  * sources[l], is left out.  sources NULL: states themselves; else another pool,
  * sources[l] of the kind, format and sizes of states[l] but for the batch.  The
  * states of one call, and the sources of one call, have the same batch; no two
- * states share memory, and no state and another's source.  States that are
+ * states share memory, nor a state and a source.  States that are
  * moved within themselves take their moves in parallel where no move reads what
  * another one writes and none writes what another one writes, and one after the
  * other else, or if they have more than 2^18 sequences.  Rounding modes and

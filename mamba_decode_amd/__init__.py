@@ -680,6 +680,13 @@ def _gated_io(x, g, o, gate: int, input: int, dev: int):
                                   xp, gp, op, xs, gs, os_)
 
 
+def _state_handle(state: State | None):
+    """The handle of a state that may be left out; a freed one is not one left out."""
+    if state is not None and state.handle is None:
+        raise ValueError("the state has been freed")
+    return None if state is None else state.handle
+
+
 def ssq_gated_scan(state: State | None, x, g, o, cu_seqlens, gate: int = SSQ_GATE_LOG, input: int = SSQ_INPUT_PLAIN,
                    slots=None, fresh=None, checkpoints=None, workspace: torch.Tensor | None = None, stream=None):
     """A gated linear recurrence over ragged sequences: ``h = a h + s x`` in every channel, ``o = h``.
@@ -698,7 +705,7 @@ def ssq_gated_scan(state: State | None, x, g, o, cu_seqlens, gate: int = SSQ_GAT
         cp = _ptr(checkpoints, "checkpoints", torch.float32, (ssq_gated_checkpoint_rows(nseq, tokens), io.channels), dev)
     on = _stream_ptr(stream, dev)
     ws, wp, wn = _workspace(workspace, ssq_gated_workspace(io.channels, nseq, tokens), stream, dev)
-    _check(lib.ssq_gated_scan(None if state is None else state.handle, io, nseq, tokens, cu, sp, fp, cp, wp, wn, on),
+    _check(lib.ssq_gated_scan(_state_handle(state), io, nseq, tokens, cu, sp, fp, cp, wp, wn, on),
            "ssq_gated_scan")
 
 
@@ -721,7 +728,7 @@ def ssq_gated_scan_backward(checkpoints, x, g, do, dx, dg, cu_seqlens, gate: int
     cp = _ptr(checkpoints, "checkpoints", torch.float32, (ssq_gated_checkpoint_rows(nseq, tokens), channels), dev)
     on = _stream_ptr(stream, dev)
     ws, wp, wn = _workspace(workspace, ssq_gated_workspace(channels, nseq, tokens), stream, dev)
-    _check(lib.ssq_gated_scan_backward(None if state is None else state.handle, io, nseq, tokens, cu, sp, cp, wp, wn, on),
+    _check(lib.ssq_gated_scan_backward(_state_handle(state), io, nseq, tokens, cu, sp, cp, wp, wn, on),
            "ssq_gated_scan_backward")
 
 

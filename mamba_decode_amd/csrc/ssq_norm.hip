@@ -402,9 +402,10 @@ static NormPlan norm_plan(int groups, int width, int64_t tokens, bool back)
     p.gblocks = (groups + p.gslots - 1) / p.gslots;
     const int64_t per = (p.wpg == 1 ? 4 : 1) * (int64_t)p.tokens; // tokens of a workgroup at a time
     int64_t blocks = (tokens + per - 1) / per;
-    // Waves in all: 16384 (8192 tokens of 8 groups of 1024: 72 us, 4096 waves 75), for the gradient, whose sums are
-    // written once for each workgroup along the tokens, 4096 (120 us; 2048 124, 8192 124).
-    int64_t most = (back ? 4096 : 16384) / ((p.wpg == 1 ? 4 : p.wpg) * (int64_t)p.gblocks);
+    // Waves in all: 16384 (8192 tokens of 8 groups of 1024: 72 us, 4096 waves 75).  The gradient's sums are written once
+    // for each workgroup along the tokens: 4096 (120 us; 2048 124, 8192 124), and of groups of several waves as many as
+    // run at once, 16 waves on each of 256 units (1999 tokens of 4104 channels in fp32, 9 waves: 28 us, 4096 waves in all 34).
+    int64_t most = !back ? 16384 / ((p.wpg == 1 ? 4 : p.wpg) * (int64_t)p.gblocks) : p.wpg == 1 ? 1024 / p.gblocks : 256 * (16 / p.wpg) / p.gblocks;
     if (most < 1) most = 1;
     if (blocks > most) { // as many rounds for all
         const int64_t rounds = (blocks + most - 1) / most;

@@ -415,6 +415,11 @@ def test_refusals():
         refused(grad, a.pop("ck"), x, x, a.pop("do"), a.pop("dx"), a.pop("dg"), a.pop("cu"), **a)
     for fmt, H, P, C2 in (("int8_sym", 1, 1, 24), ("fp32", 2, 1, 24), ("fp32", 1, 16, 24), ("fp32", 1, 1, 20), ("fp32", 1, 1, (1 << 20) + 8)):
         refused(ssq.ssq_alloc_state, ssq.make_desc(ssq.SSQ_GATED, fmt, 2, H, P, C2))
+    gone = state_of(torch.ones(2, C))
+    gone.free()  # not the same as no state
+    refused(ssq.ssq_gated_scan, gone, x, x, o, cu)
+    refused(ssq.ssq_gated_scan_backward, ck, x, x, x, t(T, C), t(T, C), cu, state=gone)
+    refused(ssq.ssq_gated_step, gone, x[:2], x[:2], o[:2])
     torch.cuda.synchronize()
     assert torch.equal(st.storage, before) and (o == 0).all()
 
