@@ -1,5 +1,16 @@
 // ssq_gated.hip -- a gated linear recurrence, h_t = a_t h_(t-1) + s_t x_t in every channel, over
 // ragged sequences, its gradient and its single-token form, gfx950.
+//
+// A run of tokens takes a state h to A h + B, A the product of its decays and B what it makes of a state of zero, and runs
+// compose: (A2, B2) after (A1, B1) is (A2 A1, A2 B1 + B2).  A lane holds 16 tokens of a few channels in registers and finds
+// their (A, B); the lanes of a slice of channels meet in LDS, each learns the state before its tokens and goes over them again,
+// from registers.  The tiles of a sequence follow each other in one workgroup, the loads of the next one under way
+// meanwhile.  So x and g are read once and o is written once.  The gradient goes through the tiles from the end, dh_t = do_t +
+// a_(t+1) dh_(t+1), and computes the states of a lane's tokens again from the one before them, which the scan keeps in fp32.
+//
+// Bytes bound it where enough workgroups have whole cache lines: 8 sequences of 2048 tokens on average, 4096 channels, bf16,
+// 56 + 84 us (585 MB in the two, 4.2 TB/s); 8192 tokens of 8192 channels (403 MB, rows of half lines) 98 us; a token
+// of 240 sequences of 8192 channels (27 MB) 7 us, 2 us of a launch among them.
 #include <type_traits>
 
 #include "ssq_gated_device.h"
@@ -374,7 +385,8 @@ __global__ __launch_bounds__(W * 64, STAGE == PART_SUM ? 3 : 2) void k_gated_bac
     }
 }
 
-// One token: a thread takes 8 channels of a sequence.
+// One token: a thread takes 8 channels of a sequence, 16 bytes of x and g and 32 of the state: one read and one write of each,
+// no wait between waves (one sequence of 2048 channels takes 2 us, a launch's time).
 template <int DT, int GATE, int INPUT>
 __global__ __launch_bounds__(256) void k_gated_step(GatedArgs a, uint32_t threads)
 {

@@ -6,7 +6,7 @@
 // that a sequence may be the source of one move and the destination of another one.
 //
 // Bytes bound it.  48 int4 layers (453 MB read and written): 8 sequences forked to 56 places, one source's places next to
-// each other in the list, 81 us, 5.6 TB/s (sources in turn 103 us: the list's order is kept), 32 copied to 32 others 69 us,
+// each other in the list, 78-81 us, 5.6-5.8 TB/s (sources in turn 103 us: the list's order is kept), 32 copied to 32 others 69 us,
 // 6.6 TB/s, 56 freed 77 us, a chain of 63 one after the other 187 us.  Loads keep their lines for the next workgroup that
 // forks the same source (with the non-temporal hint 98, 133 and 84 us), stores have the hint (without it 100 and 95 us).
 #include "ssq_ops_device.h"

@@ -4,7 +4,7 @@
 // distances from it, then the outputs.  The gradient computes the statistics again from x and z, which it reads
 // anyway, and keeps the sums over its tokens for the parameters' gradients; a second launch adds the workgroups' sums
 // in their order.  The next token's loads are under way meanwhile.  Bytes bound it: 8192 tokens of 8 groups of 1024 in
-// bf16 with a gate take 72 us (403 MB, 5.6 TB/s) and 115 us (671 MB, 5.8 TB/s) and 5 us for the parameters' second launch.
+// bf16 with a gate take 72 us (403 MB, 5.6 TB/s), 118-120 us (671 MB, 5.6 TB/s) and 5 us for the parameters' second launch.
 #include <type_traits>
 
 #include "ssq_gated_device.h"
