@@ -202,6 +202,8 @@ struct Scan {
     }
 };
 
+// 3 waves a SIMD: one workgroup of 8 waves on a unit at a time.  Two of them in 128 registers are slower: 24 ragged sequences of
+// 2048 channels 58 us (49), 8 of 2048 tokens, 4096 channels 67 (57); so are three workgroups of 4 waves, 53 and 62.
 template <int DT, int GATE, int INPUT, int STAGE, int LC, int W>
 __global__ __launch_bounds__(W * 64, 3) void k_gated_scan(GatedArgs a)
 {
@@ -333,6 +335,7 @@ struct Back {
 };
 
 // Backwards through the chunks.  PART_SUM: what a part makes of the gradient behind it.
+// 2 waves a SIMD: a third would spill (8 sequences of 2048 tokens, 4096 channels: 288 us, 83 without).
 template <int DT, int GATE, int INPUT, int STAGE, int LC, int W>
 __global__ __launch_bounds__(W * 64, STAGE == PART_SUM ? 3 : 2) void k_gated_backward(GatedArgs a)
 {
