@@ -8,7 +8,7 @@
 // meanwhile.  So x and g are read once and o is written once.  The gradient goes through the tiles from the end, dh_t = do_t +
 // a_(t+1) dh_(t+1), and computes the states of a lane's tokens again from the one before them, which the scan keeps in fp32.
 //
-// Bytes bound it where enough workgroups have whole cache lines: 8 sequences of 2048 tokens on average, 4096 channels, bf16,
+// Bytes bound it where enough workgroups have whole cache lines: 8 packed sequences, 8925 tokens in all, 4096 channels, bf16,
 // 56 + 84 us (585 MB in the two, 4.2 TB/s); 8192 tokens of 8192 channels (403 MB, rows of half lines) 98 us; a token
 // of 240 sequences of 8192 channels (27 MB) 7 us, 2 us of a launch among them.
 #include <type_traits>
@@ -104,7 +104,7 @@ __device__ __forceinline__ int longest(const GatedArgs& a, int r)
 }
 
 // What a workgroup works on.  More whole sequences than run at once are taken from the longest on, so that what is left for
-// the end is short (24 sequences of 350 to 1050 tokens, 2048 channels: 49 us, 58 in the call's order).
+// the end is short (24 sequences of up to 1040 tokens, 2048 channels: 49 us, 58 in the call's order).
 struct GatedWork {
     int seq, part, slice;
 };
@@ -203,7 +203,7 @@ struct Scan {
 };
 
 // 3 waves a SIMD: one workgroup of 8 waves on a unit at a time.  Two of them in 128 registers are slower: 24 ragged sequences of
-// 2048 channels 58 us (49), 8 of 2048 tokens, 4096 channels 67 (57); so are three workgroups of 4 waves, 53 and 62.
+// 2048 channels 58 us (49), 8 packed ones, 8925 tokens, 4096 channels 67 (57); so are three workgroups of 4 waves, 53 and 62.
 template <int DT, int GATE, int INPUT, int STAGE, int LC, int W>
 __global__ __launch_bounds__(W * 64, 3) void k_gated_scan(GatedArgs a)
 {
@@ -335,7 +335,7 @@ struct Back {
 };
 
 // Backwards through the chunks.  PART_SUM: what a part makes of the gradient behind it.
-// 2 waves a SIMD: a third would spill (8 sequences of 2048 tokens, 4096 channels: 288 us, 83 without).
+// 2 waves a SIMD: a third would spill (8925 packed tokens, 4096 channels: 288 us, 83 without).
 template <int DT, int GATE, int INPUT, int STAGE, int LC, int W>
 __global__ __launch_bounds__(W * 64, STAGE == PART_SUM ? 3 : 2) void k_gated_backward(GatedArgs a)
 {
@@ -446,11 +446,20 @@ static hipError_t with_gate(int dtype, int gate, int input, F f)
 // How a call is split.  A compute unit has some 512 cache lines under way whatever its waves do, so that rows of 64 bytes,
 // half a line each, come at half the rate of whole lines; and a workgroup's tiles follow each other.  So: enough workgroups to
 // fill the card, and then rows as wide as they can be.  bf16, scan + gradient in us:
-//   300 workgroups of 256-byte rows   24 sequences of 350 to 1050 tokens, 2048 channels   49 (128-byte rows 57)
-//   192 of 128-byte rows              8 of 2048 tokens on average, 4096 channels    57 + 83 (256-byte rows 60 + 95)
-//   128 of 64-byte rows               8192 tokens, 8192 channels                    98 (128-byte rows 120)
-//   parts, for 64-byte rows fewer     8192 tokens, 2048 channels                    39 + 53 (whole 71 + 156)
-// Parts cost a second pass over what they read, and a launch: not for sequences of 512 tokens or fewer.
+//   300 workgroups of 256-byte rows   24 sequences of up to 1040 tokens, 2048 channels      49 (128-byte rows 57)
+//   192 of 128-byte rows              8 of up to 1846 tokens, 4096 channels         57 + 83 (256-byte rows 60 + 95)
+//   64-byte rows                      8192 tokens, 8192 channels                    98 (128-byte rows 120)
+//   parts of 128-byte rows            8192 tokens, 2048 channels                    40 + 58 (whole 71 + 156)
+// Parts cost a second pass over what they read, and a launch; whole sequences take as long as the longest of them.  So parts are for
+// few workgroups of 64-byte rows, fewer in the scan, which has less to do beside that pass, and not for short sequences.  In us,
+// whole and in parts:
+//   scan      128 workgroups   1 of 4096: 37, 44;  1 of 2048: 21, 21;  0, 1, 1299 and 2588 tokens: 26, 18
+//             192              1 of 2048: 21, 35;  the four 27, 22
+//   gradient  128              1 of 4096: 75, 55;  the four 39, 19
+//             192              1 of 4096: 86, 70;  1 of 2048: 35, 35
+//             256              1 of 8192: 180, 192;  the four 42, 27;  8 of 0 to 1316 tokens 19, 25
+//   either    32 to 192        1 of 1024: 11 to 14, 14 to 20, and the gradient 15 to 19, 15 to 20
+// Whether several sequences are of one length is not known here: they count as uneven, as the ones above are.
 constexpr int kPartLanes = 32;
 struct GatedPlan {
     int lc;             // lanes across the channels
@@ -466,7 +475,8 @@ static GatedPlan gated_plan(bool back, int cpl, int channels, int nseq, int64_t 
     if (wgs(64) >= 300) return whole(64);
     if (wgs(32) >= 192) return whole(32);
     const int64_t mean = (tokens + nseq - 1) / nseq, tile = (back ? 4 : 8) * 64 / kPartLanes * kGatedChunk;
-    if (wgs(16) >= 128 || mean <= 512) return whole(16);
+    const int64_t few = !back ? (nseq == 1 ? 127 : 159) : mean / 4 < 224 ? mean / 4 : nseq == 1 ? 224 : 256;
+    if (mean <= (nseq == 1 ? 1024 : 512) || wgs(16) > few) return whole(16);
     const int64_t want = (512 + wgs(kPartLanes) - 1) / wgs(kPartLanes); // parts of a sequence of the mean length
     GatedPlan p{kPartLanes, slices(kPartLanes), 1, ((mean + want - 1) / want + tile - 1) / tile * tile};
     p.parts = (int)((tokens + p.part_tokens - 1) / p.part_tokens);
@@ -512,7 +522,7 @@ static hipError_t launch_gated(int dtype, int gate, int input, const GatedArgs& 
         }
         if (p.lc == 64) return launch_gated<DT, GA, IN, BACK, WHOLE, 64, 8>(a, st);
         if (p.lc == 32) return launch_gated<DT, GA, IN, BACK, WHOLE, 32, 8>(a, st);
-        // gradient of 8 x 1024 tokens, 1024 channels: 20 us, 4 waves 24; scan of 8192 tokens, 8192 channels: 105 and 100
+        // gradient of 8 sequences, 6312 tokens, 1024 channels: 20 us, 4 waves 24; scan of 8192 tokens, 8192 channels: 105 and 100
         return launch_gated<DT, GA, IN, BACK, WHOLE, 16, BACK ? 8 : 4>(a, st);
     });
 }

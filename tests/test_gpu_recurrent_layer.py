@@ -163,6 +163,15 @@ def test_parts(dtype, lens, channels):
     case(dtype, 0, 2, channels, lens, seed=n, slices=True)
 
 
+@pytest.mark.parametrize("dtype,lens,channels", [(BF, [1100], 4104), (F32, [1030], 2056), (F32, [2700, 0, 1500], 1080), (BF, [2700, 1], 2600)])
+def test_parts_of_the_gradient_alone(dtype, lens, channels):
+    """Sizes whose scan takes sequences whole and whose gradient takes them in parts."""
+    say("parts of the gradient", dtype, lens, channels)
+    n = len(lens)
+    assert ssq.ssq_gated_workspace(channels, n, sum(lens) + 3) > 0
+    case(dtype, 0, 1, channels, lens, tail=3, slots=list(range(n, 0, -1)), fresh=[i % 2 for i in range(n)], batch=n + 1, seed=n)
+
+
 def test_past_4_gib():
     """Rows that lie 2^18 elements apart, so that the last ones begin behind 2^32 bytes."""
     say("past 4 GiB")
