@@ -496,7 +496,8 @@ ssq_status ssq_state_move(ssq_state *const *states, ssq_state *const *sources, i
  * other output.  channels: a multiple of 8, up to 2^20.  The state, decays,
  * factors and sums are fp32 (1 - a and 1 - a^2 are taken from the gate, without
  * a difference of near numbers; a decay exp(-x) is off by (2x + 4) * 2^-24 of
- * itself at most, one below 2^-126 may be zero), outputs are rounded once to `dtype`.
+ * itself at most; a, 1 - a and 1 - a^2 may be zero where they are below 2^-126),
+ * outputs are rounded once to `dtype`.
  *
  * cu_seqlens, slots, fresh: as in ssq_linattn_prefill.  state: an SSQ_GATED
  * state, whose sequences go on and keep their last state; NULL: all sequences

@@ -35,13 +35,14 @@ struct GateSlope {
     float a, s, da, ds; // and their derivatives along the gate
 };
 
-// The sigmoid and one minus it, from e = exp(-g): neither is a difference.  Where e overflows, e * a is
-// not a number and the minimum is 1.
+// The sigmoid and one minus it, from e = exp(-g): neither is a difference.  From e = 2^24 on the latter is one to a last
+// step, and is not formed from the former: above 2^126 that is subnormal, which the reciprocal returns as zero, and e may
+// be infinity.
 __device__ __forceinline__ void sigmoid_pair(float g, float* a, float* rest)
 {
     const float e = exp_fast(-g);
     *a = __builtin_amdgcn_rcpf(1.0f + e);
-    *rest = fminf(e * *a, 1.0f);
+    *rest = e < 0x1p24f ? e * *a : 1.0f;
 }
 
 template <int GATE, int INPUT>
