@@ -108,7 +108,7 @@ __device__ __forceinline__ int longest(const GatedArgs& a, int r)
 struct GatedWork {
     int seq, part, slice;
 };
-template <int STAGE, int LC>
+template <int STAGE>
 __device__ __forceinline__ GatedWork gated_work(const GatedArgs& a)
 {
     const int j = (int)(blockIdx.x / a.slices), i = (int)(blockIdx.x % a.slices);
@@ -210,7 +210,7 @@ __global__ __launch_bounds__(W * 64, 3) void k_gated_scan(GatedArgs a)
     using T = Tile<DT, LC, W>;
     constexpr int K = T::K, S = T::S;
     __shared__ float s_a[T::SEGS][S], s_b[T::SEGS][S], s_h[T::SEGS][S];
-    const GatedWork work = gated_work<STAGE, LC>(a);
+    const GatedWork work = gated_work<STAGE>(a);
     const int seq = work.seq, slot = gated_slot(a, seq);
     if (slot < 0) return;
     const Span sp = gated_span(a, seq);
@@ -342,7 +342,7 @@ __global__ __launch_bounds__(W * 64, STAGE == PART_SUM ? 3 : 2) void k_gated_bac
     using T = Tile<DT, LC, W>;
     constexpr int S = T::S;
     __shared__ float s_a[T::SEGS][S], s_b[T::SEGS][S], s_h[T::SEGS][S];
-    const GatedWork work = gated_work<STAGE, LC>(a);
+    const GatedWork work = gated_work<STAGE>(a);
     const int seq = work.seq;
     if (gated_slot(a, seq) < 0) return;
     const Span sp = gated_span(a, seq);

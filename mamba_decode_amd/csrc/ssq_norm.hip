@@ -94,7 +94,7 @@ struct GroupSum {
                 if (y) buf[turn][wave][1] = *y;
             }
             __syncthreads();
-            // A lane reads a wave's sums, each 8 or 16 lanes all of them (4096 tokens of 8192 channels, gradient: 70 us, 74 with one
+            // A lane reads a wave's sums, each 16 lanes all of them (4096 tokens of 8192 channels, gradient: 70 us, 74 with one
             // wave's after the other).
             const int i = threadIdx.x & (MAXW - 1);
             x = lane_sum(i < wpg ? buf[turn][i][0] : 0.0f, MAXW);
@@ -428,7 +428,6 @@ static hipError_t launch_norm(const NormArgs& a, hipStream_t st)
         if (c.p.wpg == 1 && c.p.v == 1) hipLaunchKernelGGL((k_norm<DT, ACT, 1, 1, BACK>), grid, wg, 0, st, c);
         else if (c.p.v == 1) hipLaunchKernelGGL((k_norm<DT, ACT, 16, 1, BACK>), grid, wg, 0, st, c);
         else if (c.p.wpg == 1) hipLaunchKernelGGL((k_norm<DT, ACT, 1, 2, BACK>), grid, wg, 0, st, c);
-        else if (c.p.wpg <= 8) hipLaunchKernelGGL((k_norm<DT, ACT, 8, 2, BACK>), grid, wg, 0, st, c);
         else hipLaunchKernelGGL((k_norm<DT, ACT, 16, 2, BACK>), grid, wg, 0, st, c);
     }
     if (BACK && (a.dweight || a.dbias)) {
