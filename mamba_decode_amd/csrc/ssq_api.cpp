@@ -745,8 +745,6 @@ ssq_status ssq_state_move(ssq_state* const* states, ssq_state* const* sources, i
     if (nstates == 0 || nmoves == 0) return ok();
     SSQ_REQUIRE(states && to && from, SSQ_ERR_INVALID_ARG, "states, to or from is NULL");
     SSQ_REQUIRE(aligned(to, 4) && aligned(from, 4), SSQ_ERR_INVALID_ARG, "to and from must be 4-byte aligned");
-    ssq::MovePart parts[4 * kMost];
-    int n = 0;
     for (int i = 0; i < nstates; ++i) {
         const ssq_state* st = states[i];
         const ssq_state* src = sources ? sources[i] : st;
@@ -768,18 +766,29 @@ ssq_status ssq_state_move(ssq_state* const* states, ssq_state* const* sources, i
             SSQ_REQUIRE(!sources || !sources[j] || !share_memory(st, sources[j]), SSQ_ERR_INVALID_ARG,
                         "a state and a source share memory");
         }
-        ssq::ReorderPart d[4], f[4];
+        ssq::ReorderPart d[4];
         const int m = state_parts(st, d);
-        (void)state_parts(src, f);
-        for (int j = 0; j < m; ++j) {
+        for (int j = 0; j < m; ++j)
             SSQ_REQUIRE(d[j].bytes <= ssq::kMaxBlocks * ssq::kColumnBytes, SSQ_ERR_UNSUPPORTED,
                         "a state has too many bytes for each sequence");
+    }
+    // all of them checked; a launch's arrays at a time, as the callers' stacks may be small
+    ssq::MovePart parts[ssq::kMoveParts];
+    int n = 0;
+    for (int i = 0; i < nstates; ++i) {
+        ssq::ReorderPart d[4], f[4];
+        const int m = state_parts(states[i], d);
+        (void)state_parts((sources ? sources : states)[i], f);
+        for (int j = 0; j < m; ++j) {
             parts[n++] = {d[j].p, f[j].p, d[j].bytes};
+            if (n < ssq::kMoveParts && !(i == nstates - 1 && j == m - 1)) continue;
+            const hipError_t e = ssq::launch_move(parts, n, to, from, nmoves, states[0]->desc.batch,
+                                                  (sources ? sources : states)[0]->desc.batch, !sources, (hipStream_t)stream);
+            if (e != hipSuccess) return from_hip(e, "state move launch");
+            n = 0;
         }
     }
-    return from_hip(ssq::launch_move(parts, n, to, from, nmoves, states[0]->desc.batch,
-                                     (sources ? sources : states)[0]->desc.batch, !sources, (hipStream_t)stream),
-                    "state move launch");
+    return ok();
 }
 
 // ---------------------------------------------------------------------------

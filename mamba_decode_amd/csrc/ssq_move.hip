@@ -13,8 +13,6 @@
 
 namespace ssq {
 
-constexpr int kMoveParts = 160; // arrays in one launch: the kernel's arguments stay below 4 KiB
-
 struct MoveArgs {
     uint8_t* dst[kMoveParts];
     const uint8_t* src[kMoveParts];

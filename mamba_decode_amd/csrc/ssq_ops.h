@@ -119,6 +119,7 @@ struct MovePart {
     int64_t bytes;
 };
 constexpr int kMaxMoves = 65535;
+constexpr int kMoveParts = 160; // arrays in one launch: the kernel's arguments stay below 4 KiB
 
 size_t gated_workspace(int channels, int nseq, int64_t tokens);
 hipError_t launch_gated_scan(int dtype, int gate, int input, const GatedArgs& a, void* ws, hipStream_t st);
