@@ -601,10 +601,11 @@ ssq_status ssq_gated_step(ssq_state *state, const ssq_gated_io *io, int32_t nseq
  * fp32, 16-byte aligned (weight NULL: 1, bias NULL: 0).  z is NULL for
  * SSQ_ACT_SILU.  Outputs overlap no input and no other output.  width: a
  * multiple of 8 up to 16384; groups*width up to 2^20.  Everything between is
- * fp32: the mean first, then the squares of the distances from it; outputs are
- * rounded once.  eps > 0.  Values of u beyond 2^56, whose squares overflow, and values of x or z that are not finite leave
- * their token's group unspecified (and dweight and dbias of its channels); all else is
- * computed as usual.
+ * fp32: the mean first, then the squares of the distances from it (a sigmoid
+ * below 2^-126, that of -87.34, may be zero); outputs are rounded once.  eps > 0.
+ * Values of u beyond 2^56, whose squares overflow, and values of x or z that are
+ * not finite leave their token's group unspecified (and dweight and dbias of its
+ * channels); all else is computed as usual.
  * ------------------------------------------------------------------------ */
 typedef enum { SSQ_ACT_SILU = 0, SSQ_ACT_GATE_OUTPUT = 1, SSQ_ACT_GATE_INPUT = 2 } ssq_act;
 

@@ -3,8 +3,9 @@ what fp32 evaluation of the same formulas may be off by.
 
 u = 2^-24 is half a step of fp32.  A decay is an exponential of a rounded product, off by
 (2|g| + 4)u of itself; a sigmoid adds a sum, a reciprocal and a product, (2|g| + 8)u.  The factor on
-the input comes from a series of 8 terms or a difference that is at least 0.39 of its larger side, 10u
-with the root.  Every token then adds a rounding of the product and of the sum, and an evaluation in
+the input comes from a polynomial, 3.3u of itself as it is evaluated, or from g = -1/2 (for a^2: -1/4) on from a
+difference that is at least 0.39 of its larger side, ((2|g| + 4)a + 1)u / (1 - a) <= 8.7u, half of 17u with the
+root and 2u of its own: 10u and less.  Every token then adds a rounding of the product and of the sum, and an evaluation in
 pieces one more of each piece's decay: the state's error runs through the same recurrence,
   E_t = a E_(t-1) + u ((2|g| + 12) a M_(t-1) + 14 |s x| + 3 M_t),  M the recurrence on absolute values,
 which holds for any grouping of the products.  The gradient's recurrence is the same one backwards.
