@@ -443,7 +443,8 @@ static hipError_t with_gate(int dtype, int gate, int input, F f)
     return hipErrorInvalidValue;
 }
 
-// How a call is split.  A compute unit has some 512 cache lines under way whatever its waves do, so that rows of 64 bytes,
+// How a call is split.  More waves, more registers and loads further ahead change no time, wider rows do: as if a compute unit
+// had some 512 cache lines under way whatever its waves do (inferred from times, no counter shows it), so that rows of 64 bytes,
 // half a line each, come at half the rate of whole lines; and a workgroup's tiles follow each other.  So: enough workgroups to
 // fill the card, and then rows as wide as they can be.  bf16, scan + gradient in us:
 //   300 workgroups of 256-byte rows   24 sequences of up to 1040 tokens, 2048 channels      49 (128-byte rows 57)
@@ -459,7 +460,9 @@ static hipError_t with_gate(int dtype, int gate, int input, F f)
 //             192              1 of 4096: 86, 70;  1 of 2048: 35, 35
 //             256              1 of 8192: 180, 192;  the four 42, 27;  8 of 0 to 1316 tokens 19, 25
 //   either    32 to 192        1 of 1024: 11 to 14, 14 to 20, and the gradient 15 to 19, 15 to 20
-// Whether several sequences are of one length is not known here: they count as uneven, as the ones above are.
+// Whether several sequences are of one length is not known here: they count as uneven, as the ones above are.  The scan's limits
+// are from sequences of up to 4096 tokens and know no length: one of 8192 tokens of 4096 channels still runs whole, on half of
+// the units (89 us; its bytes take 31 at a copy's rate).
 constexpr int kPartLanes = 32;
 struct GatedPlan {
     int lc;             // lanes across the channels

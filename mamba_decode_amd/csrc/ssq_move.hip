@@ -9,6 +9,8 @@
 // each other in the list, 78-81 us, 5.6-5.8 TB/s (sources in turn 103 us: the list's order is kept), 32 copied to 32 others 69 us,
 // 6.6 TB/s, 56 freed 77 us, a chain of 63 one after the other 187 us.  Loads keep their lines for the next workgroup that
 // forks the same source (with the non-temporal hint 98, 133 and 84 us), stores have the hint (without it 100 and 95 us).
+// Every workgroup goes through the whole list to see whether moves meet, which is what bounds long lists of small sequences: 4000
+// moves of 2048 fp32 channels 26 us (bytes 10), 65535 of them 1.1 ms (165 us), 65535 of 64 channels 0.9 ms (5 us).
 #include "ssq_ops_device.h"
 
 namespace ssq {

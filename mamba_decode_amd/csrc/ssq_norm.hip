@@ -112,7 +112,8 @@ __global__ __launch_bounds__(MAXW == 1 ? 256 : MAXW * 64) void k_norm(NormCall c
     constexpr bool IN_WAVE = MAXW == 1;
     // Groups of more than 8192 channels leave a lane of 16 waves too few registers for the parameters, the sums of
     // their gradients and loads ahead: the parameters are read again for every token, the sums stand in LDS, each lane its own
-    // (2000 tokens of 16000 channels in bf16, gradient: 124 us, 302 us all in registers and spilled).
+    // (2000 tokens of 16000 channels in bf16, gradient: 124 us, 302 us all in registers).  The gated forms still have 8 to 24
+    // bytes of scratch a lane (gate after) and 96 to 108 (gate before) at the 128 registers of 16 waves, the one without a gate none.
     constexpr bool LEAN = BACK && MAXW == 16 && V == 2;
     __shared__ float s_grad[LEAN ? 2 * V * 2 : 1][LEAN ? MAXW * 64 : 1][4];
     __shared__ float s_sum[2][MAXW][2];
@@ -402,8 +403,9 @@ static NormPlan norm_plan(int groups, int width, int64_t tokens, bool back)
     const int64_t per = (p.wpg == 1 ? 4 : 1) * (int64_t)p.tokens; // tokens of a workgroup at a time
     int64_t blocks = (tokens + per - 1) / per;
     // Waves in all: 16384 (8192 tokens of 8 groups of 1024: 72 us, 4096 waves 75).  The gradient's sums are written once
-    // for each workgroup along the tokens: 4096 (120 us; 2048 124, 8192 124), and of groups of several waves as many as
-    // run at once, 16 waves on each of 256 units (1999 tokens of 4104 channels in fp32, 9 waves: 28 us, 4096 waves in all 34).
+    // for each workgroup along the tokens: 4096 (120 us; 2048 124, 8192 124), and of groups of several waves whole workgroups
+    // of 16 waves on each of 256 units, which from 9 waves on is one (1999 tokens of 4104 channels in fp32, 9 waves: 28 us, 4096
+    // waves in all 34; two a unit, which the registers allow, 5 us more, as the sums are written twice as often).
     int64_t most = !back ? 16384 / ((p.wpg == 1 ? 4 : p.wpg) * (int64_t)p.gblocks) : p.wpg == 1 ? 1024 / p.gblocks : 256 * (16 / p.wpg) / p.gblocks;
     if (most < 1) most = 1;
     if (blocks > most) { // as many rounds for all
